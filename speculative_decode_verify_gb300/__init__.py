@@ -20,7 +20,9 @@ __all__ = [
     "va_sample_topk_topp", "va_accept_chain", "va_tree_accept_settle", "kv_ring_append_q8", "verify_attn_q8",
     "verify_attn_q8_tree", "verify_attn_q8_step", "verify_attn_step", "va_selftest_bounded_wait", "SAMPLE_MAX_K", "SAMPLE_TILE",
     "SAMPLE_MAX_VOCAB", "NOALLOC_MAX_SPLITS", "va_workspace_bytes", "va_auto_splits", "va_auto_splits_for", "va_status_string",
-    "HEAD_DIM", "Q_HEADS", "MAX_ROWS", "TILE", "MAX_SPLITS", "MAX_TREE_NODES", "EXPORTS",
+    "kv_page_append_b8", "verify_attn_paged_b8", "va_paged_workspace_bytes", "kv_page_extend", "kv_page_reorder",
+    "kv_page_copy", "kv_page_compact", "va_page_ops_workspace_bytes", "va_beam_select", "va_beam_workspace_bytes",
+    "PAGED_MAX_SEQS", "B8_BLOCK", "HEAD_DIM", "Q_HEADS", "MAX_ROWS", "TILE", "MAX_SPLITS", "MAX_TREE_NODES", "EXPORTS",
     "VA_OK", "VA_INVALID_ARG", "VA_UNSUPPORTED", "VA_RING_TOO_SMALL", "VA_CUDA_ERROR",
 ]
 
@@ -30,9 +32,13 @@ EXPORTS = ("kv_ring_append", "verify_attn_full", "verify_attn_swa", "verify_attn
            "va_workspace_bytes", "va_auto_splits", "va_auto_splits_for", "va_status_string",
            "verify_attn_full_noalloc", "va_sample_workspace_bytes", "va_sample_topk_topp", "va_accept_chain",
            "va_tree_accept_settle", "kv_ring_append_q8", "verify_attn_q8", "verify_attn_q8_tree", "verify_attn_q8_step",
-           "verify_attn_step", "va_selftest_bounded_wait")
+           "verify_attn_step", "va_selftest_bounded_wait", "kv_page_append_b8", "verify_attn_paged_b8",
+           "va_paged_workspace_bytes", "kv_page_extend", "kv_page_reorder", "kv_page_copy", "kv_page_compact",
+           "va_page_ops_workspace_bytes", "va_beam_select", "va_beam_workspace_bytes")
 NOALLOC_MAX_SPLITS = 160
 SAMPLE_MAX_K, SAMPLE_TILE, SAMPLE_MAX_VOCAB = 32, 8192, 262144
+PAGED_MAX_SEQS, B8_BLOCK = 1024, 16
+B8_E4M3, B8_INT8 = 0, 1
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _lib = {}
@@ -85,6 +91,22 @@ def lib(variant: str = "") -> ctypes.CDLL:
         L.verify_attn_step.restype = i
         L.va_selftest_bounded_wait.argtypes = [ctypes.c_ulonglong, ctypes.c_ulonglong, p, p, p]
         L.va_selftest_bounded_wait.restype = i
+        z = ctypes.c_size_t
+        L.kv_page_append_b8.argtypes = [p, p, i, i, i, p, p, p, i, p, p, p, p, i, i, p, p]
+        L.verify_attn_paged_b8.argtypes = [p, i, i, i, i, p, p, p, i, p, p, p, p, i, i, i, f, p, p, z, p, p, p, p]
+        L.kv_page_extend.argtypes = [p, p, p, i, i, p, i, i, i, p, p, p, p, p, z, p, p]
+        L.kv_page_reorder.argtypes = [p, p, i, i, p, i, p, i, p, p]
+        L.kv_page_copy.argtypes = [p, p, i, i, i, i, p, p, p, p, p, p]
+        L.kv_page_compact.argtypes = [p, i, i, p, i, i, i, p, p, p, p, p, p, p, z, p, p]
+        L.va_beam_select.argtypes = [p, i, ctypes.c_int64, i, i, i, p, p, i, i, p, p, p, p, z, p]
+        for fn in ("kv_page_append_b8", "verify_attn_paged_b8", "kv_page_extend", "kv_page_reorder", "kv_page_copy",
+                   "kv_page_compact", "va_beam_select"):
+            getattr(L, fn).restype = i
+        L.va_paged_workspace_bytes.argtypes = [i, i, i, i]
+        L.va_page_ops_workspace_bytes.argtypes = [i, i, i]
+        L.va_beam_workspace_bytes.argtypes = [i, i, i, i]
+        for fn in ("va_paged_workspace_bytes", "va_page_ops_workspace_bytes", "va_beam_workspace_bytes"):
+            getattr(L, fn).restype = z
         L.va_workspace_bytes.argtypes = [i]
         L.va_workspace_bytes.restype = ctypes.c_size_t
         L.va_auto_splits.argtypes = [i, i]
@@ -298,6 +320,152 @@ def verify_attn_q8_step(q, k_new, v_new, n_live: int, k_codes, v_codes, k_scale,
                                           ctypes.byref(used), _ptr(dev_status), _stream(stream))
     _check("verify_attn_q8_step", st)
     return used.value
+
+
+# ----------------------------------------------------------------------------- paged 8-bit cache of many sequences
+def _addr(*tensors):
+    """Addresses of dense tensors (None: a null pointer); the C ABI takes no strides."""
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("the paged cache's calls take contiguous tensors")
+    return [None if t is None else t.data_ptr() for t in tensors]
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _pool(k_codes, v_codes, k_scale, v_scale):
+    """(layers, pages, kv heads, format, addresses) of pools [pages, heads, 64, 128] or [layers, pages, ...]."""
+    shape = k_codes.shape
+    _need(len(shape) in (4, 5) and shape[-2] == TILE and shape[-1] == HEAD_DIM and v_codes.shape == shape
+          and k_codes.dtype == v_codes.dtype and k_codes.element_size() == 1,
+          "codes are [..., pages, heads, 64, 128] of one 8-bit type")
+    want = (*shape[:-2], TILE // B8_BLOCK)
+    _need(tuple(k_scale.shape) == want and tuple(v_scale.shape) == want and k_scale.element_size() == 4
+          and v_scale.element_size() == 4, "scales are float32 [..., pages, heads, 4]")
+    fmt = B8_INT8 if str(k_codes.dtype) == "torch.int8" else B8_E4M3
+    return (1 if len(shape) == 4 else int(shape[0]), int(shape[-4]), int(shape[-3]), fmt,
+            _addr(k_codes, v_codes, k_scale, v_scale))
+
+
+def _counts(n: int, what: str, *tensors):
+    for t in tensors:
+        _need(t.numel() == n and t.element_size() == 4, what)
+
+
+def kv_page_append_b8(k_new, v_new, n_live, lens, table, k_codes, v_codes, k_scale, v_scale, dev_status=None,
+                      stream=None, variant: str = "") -> None:
+    """Code the live rows' K/V ([n_seqs, n_rows, n_kv_heads, 128] bf16) into the sequences' pages.  The pool's
+    format goes by its dtype: int8, or E4M3 (float8_e4m3fn or uint8)."""
+    layers, pages, heads, fmt, pool = _pool(k_codes, v_codes, k_scale, v_scale)
+    n, rows = int(k_new.shape[0]), int(k_new.shape[1])
+    _need(layers == 1 and k_new.shape == v_new.shape and tuple(k_new.shape) == (n, rows, heads, HEAD_DIM)
+          and k_new.element_size() == 2 and v_new.element_size() == 2, "new rows are [n_seqs, n_rows, n_kv_heads, 128]")
+    _need(table.dim() == 2 and table.shape[0] == n and table.element_size() == 4, "the table is int32 [n_seqs, max_pages]")
+    _counts(n, "one int32 a sequence", n_live, lens)
+    kn, vn, live, ln, tb, ds = _addr(k_new, v_new, n_live, lens, table, dev_status)
+    st = lib(variant).kv_page_append_b8(kn, vn, n, rows, heads, live, ln, tb, int(table.shape[1]), *pool, pages, fmt, ds,
+                                        _stream(stream))
+    _check("kv_page_append_b8", st)
+
+
+def va_paged_workspace_bytes(n_seqs: int, n_rows: int, n_kv_heads: int, group: int) -> int:
+    return int(lib().va_paged_workspace_bytes(int(n_seqs), int(n_rows), int(n_kv_heads), int(group)))
+
+
+def verify_attn_paged_b8(q, n_live, lens, table, k_codes, v_codes, k_scale, v_scale, scale: float, sink, workspace, out,
+                         out_lse=None, window: int = 0, dev_status=None, stream=None, variant: str = "") -> None:
+    """Verify attention of every sequence's live rows (q [n_seqs, n_rows, heads, 128] bf16) over its pages; writes
+    out (as q) and out_lse [n_seqs, n_rows, heads].  ``workspace``: a device byte tensor of
+    va_paged_workspace_bytes(...) bytes, zeroed once."""
+    layers, pages, kv, fmt, pool = _pool(k_codes, v_codes, k_scale, v_scale)
+    n, rows, heads, d = (int(x) for x in q.shape)
+    _need(layers == 1 and d == HEAD_DIM and heads % kv == 0 and out.shape == q.shape and q.element_size() == 2
+          and out.element_size() == 2, "q and out are [n_seqs, n_rows, n_kv_heads * group, 128] bf16")
+    _need(table.dim() == 2 and table.shape[0] == n and table.element_size() == 4, "the table is int32 [n_seqs, max_pages]")
+    _counts(n, "one int32 a sequence", n_live, lens)
+    if sink is not None:
+        _counts(heads, "one float32 sink a query head", sink)
+    if out_lse is not None:
+        _counts(n * rows * heads, "out_lse is float32 [n_seqs, n_rows, heads]", out_lse)
+    qa, live, ln, tb, sk, ws, o, lse, ds = _addr(q, n_live, lens, table, sink, workspace, out, out_lse, dev_status)
+    st = lib(variant).verify_attn_paged_b8(qa, n, rows, kv, heads // kv, live, ln, tb, int(table.shape[1]), *pool, pages,
+                                           fmt, int(window), float(scale), sk, ws,
+                                           workspace.numel() * workspace.element_size(), o, lse, ds, _stream(stream))
+    _check("verify_attn_paged_b8", st)
+
+
+def va_page_ops_workspace_bytes(n_seqs: int, max_pages: int, n_pages: int) -> int:
+    return int(lib().va_page_ops_workspace_bytes(int(n_seqs), int(max_pages), int(n_pages)))
+
+
+def kv_page_extend(table, lens, n_new, refs, k_codes, v_codes, k_scale, v_scale, workspace, dev_status=None, stream=None,
+                   variant: str = "") -> None:
+    """Pages for n_new[b] more tokens of every sequence (copy on write); lens grows by n_new.  Pools of all layers:
+    [layers, pages, heads, 64, 128]."""
+    layers, pages, heads, _, pool = _pool(k_codes, v_codes, k_scale, v_scale)
+    n, width = (int(x) for x in table.shape)
+    _counts(n, "one int32 a sequence", lens, n_new)
+    _counts(pages, "one int32 reference count a page", refs)
+    tb, ln, new, rf, ws, ds = _addr(table, lens, n_new, refs, workspace, dev_status)
+    st = lib(variant).kv_page_extend(tb, ln, new, n, width, rf, pages, layers, heads, *pool, ws,
+                                     workspace.numel() * workspace.element_size(), ds, _stream(stream))
+    _check("kv_page_extend", st)
+
+
+def kv_page_reorder(table, lens, src, refs, group: int = 0, dev_status=None, stream=None, variant: str = "") -> None:
+    """Slot j takes the sequence of slot src[j] of its group (j: kept, another: forked, -1: freed)."""
+    n, width = (int(x) for x in table.shape)
+    _counts(n, "one int32 a sequence", lens, src)
+    tb, ln, s, rf, ds = _addr(table, lens, src, refs, dev_status)
+    st = lib(variant).kv_page_reorder(tb, ln, n, width, s, int(group), rf, int(refs.numel()), ds, _stream(stream))
+    _check("kv_page_reorder", st)
+
+
+def kv_page_copy(src, dst, k_codes, v_codes, k_scale, v_scale, dev_status=None, stream=None, variant: str = "") -> None:
+    """Page dst[i] becomes a copy of page src[i], in all layers."""
+    layers, pages, heads, _, pool = _pool(k_codes, v_codes, k_scale, v_scale)
+    _counts(int(src.numel()), "as many destinations as sources, int32", src, dst)
+    s, d, ds = _addr(src, dst, dev_status)
+    st = lib(variant).kv_page_copy(s, d, int(src.numel()), pages, layers, heads, *pool, ds, _stream(stream))
+    _check("kv_page_copy", st)
+
+
+def kv_page_compact(table, refs, k_codes, v_codes, k_scale, v_scale, moved_to, n_live_pages, workspace, dev_status=None,
+                    stream=None, variant: str = "") -> None:
+    """Move the live pages to the lowest numbers; moved_to [pages] tells where, n_live_pages [1] how many there are."""
+    layers, pages, heads, _, pool = _pool(k_codes, v_codes, k_scale, v_scale)
+    n, width = (int(x) for x in table.shape)
+    _counts(pages, "one int32 a page", refs, moved_to)
+    tb, rf, mv, nl, ws, ds = _addr(table, refs, moved_to, n_live_pages, workspace, dev_status)
+    st = lib(variant).kv_page_compact(tb, n, width, rf, pages, layers, heads, *pool, mv, nl, ws,
+                                      workspace.numel() * workspace.element_size(), ds, _stream(stream))
+    _check("kv_page_compact", st)
+
+
+# ----------------------------------------------------------------------------- beam search
+def va_beam_workspace_bytes(n_groups: int, n_beams: int, vocab: int, n_out: int) -> int:
+    return int(lib().va_beam_workspace_bytes(int(n_groups), int(n_beams), int(vocab), int(n_out)))
+
+
+def va_beam_select(logits, scores, n_beams: int, parents, tokens, out_scores, workspace, finished=None, end_token: int = 0,
+                   stream=None, variant: str = "") -> None:
+    """The best n_out continuations of each request's n_beams hypotheses: logits [n_groups * n_beams, vocab] (float32
+    or bfloat16, rows at any stride that keeps them 16-byte aligned), scores [n_groups * n_beams]; writes parents,
+    tokens and out_scores [n_groups, n_out].  ``workspace``: va_beam_workspace_bytes(...) bytes, zeroed once."""
+    rows, vocab = (int(x) for x in logits.shape)
+    groups, n_out = (int(x) for x in parents.shape)
+    _need(groups * int(n_beams) == rows and (vocab == 1 or logits.stride(1) == 1)
+          and str(logits.dtype) in ("torch.float32", "torch.bfloat16"), "logits are [n_groups * n_beams, vocab]")
+    _counts(rows, "one score (and flag) a hypothesis", scores, *([] if finished is None else [finished]))
+    _counts(groups * n_out, "outputs are [n_groups, n_out]", parents, tokens, out_scores)
+    sc, fin, pa, tk, os_, ws = _addr(scores, finished, parents, tokens, out_scores, workspace)
+    st = lib(variant).va_beam_select(logits.data_ptr(), 0 if logits.element_size() == 4 else 1, int(logits.stride(0)),
+                                     groups, int(n_beams), vocab, sc, fin, int(end_token), n_out, pa, tk, os_, ws,
+                                     workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("va_beam_select", st)
 
 
 # ----------------------------------------------------------------------------- self-test

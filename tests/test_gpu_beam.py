@@ -1,0 +1,104 @@
+"""Beam search's selection against the oracle (oracle/paged.py)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.paged as P
+import speculative_decode_verify_gb300 as va
+
+pytestmark = pytest.mark.gpu
+
+
+def _select(logits, scores, beams, k, finished=None, end=0, ws=None):
+    groups = logits.shape[0] // beams
+    pa, tk = (torch.full((groups, k), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+    sc = torch.full((groups, k), float("nan"), device="cuda")
+    if ws is None:
+        ws = torch.zeros(va.va_beam_workspace_bytes(groups, beams, logits.shape[1], k), dtype=torch.uint8, device="cuda")
+    fin = None if finished is None else torch.tensor(finished, dtype=torch.int32, device="cuda")
+    va.va_beam_select(logits, torch.tensor(scores, dtype=torch.float32, device="cuda"), beams, pa, tk, sc, ws,
+                      finished=fin, end_token=end)
+    return pa, tk, sc
+
+
+def _check(logits, scores, beams, k, finished=None, end=0, ws=None):
+    got = _select(logits, scores, beams, k, finished, end, ws)
+    s32 = np.asarray(scores, np.float32).astype(np.float64)
+    pa, tk, sc, gap = P.beam_select(logits.double().cpu().numpy(), s32, beams, k, finished, end)
+    # a row's sum of exponentials is right to 2^-18 (fp32 sums of at most 8,192 terms of 2^-22 accuracy each, in
+    # trees of 32 + 5 + 8 additions), so candidates of different hypotheses that far apart keep their order
+    assert gap > 2.0 ** -17
+    assert got[0].tolist() == pa.tolist() and got[1].tolist() == tk.tolist()
+    have = got[2].double().cpu().numpy()
+    some = np.isfinite(sc)
+    assert np.array_equal(some, np.isfinite(have)) and np.array_equal(have[~some], sc[~some])
+    assert np.all(np.abs(have[some] - sc[some]) <= 2.0 ** -18 + 2.0 ** -24 * np.abs(sc[some]))
+    return got
+
+
+def _rows(seed, rows, vocab, dtype, spread=2.5, pad=8):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    wide = -(-vocab // 8) * 8 + pad
+    x = torch.full((rows, wide), float("nan"), device="cuda", dtype=dtype)    # what lies between rows is not used
+    x[:, :vocab] = (torch.randn(rows, vocab, generator=g, device="cuda") * spread).to(dtype)
+    return x[:, :vocab]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("groups,beams,vocab,k", [(1, 1, 1, 1), (1, 1, 7, 7), (2, 3, 5, 32), (3, 4, 1000, 4), (1, 2, 8192, 5),
+                                                  (2, 4, 8193, 8), (2, 8, 50001, 16), (1, 32, 3001, 32), (40, 2, 300, 3),
+                                                  (1, 3, 262144, 32)])
+def test_selection(dtype, groups, beams, vocab, k):
+    rng = np.random.default_rng(vocab)
+    _check(_rows(vocab + k, groups * beams, vocab, dtype), -5 + rng.standard_normal(groups * beams), beams, k)
+
+
+def test_finished_and_missing_hypotheses():
+    x = _rows(3, 12, 4000, torch.float32)
+    scores = [-1.0, -2.0, -np.inf, -0.5] + [0.0, -np.inf, -np.inf, -np.inf] + [-3.0, -3.5, -3.25, -np.inf]
+    _check(x, scores, 4, 6, finished=[0, 1, 0, 0] + [0, 0, 0, 0] + [1, 1, 1, 1], end=7)
+    _check(x, [-np.inf] * 12, 4, 6)
+    _check(x, [np.nan, -1, -2, -3] * 3, 4, 6, finished=[0, 0, 1, 0] * 3, end=3999)
+
+
+def test_masked_infinite_and_nan_logits():
+    x = _rows(4, 6, 9000, torch.float32, pad=0).clone()
+    x = torch.nn.functional.pad(x, (0, 8 - 9000 % 8 if 9000 % 8 else 0)).contiguous()[:, :9000]
+    x[0, 5:] = -np.inf                                     # five candidates
+    x[1] = -np.inf                                         # none
+    x[2, ::2] = float("nan")
+    x[3, 100] = x[3, 8500] = np.inf                        # share the probability
+    x[4, :8192] = -np.inf
+    x[5] = torch.finfo(torch.float32).min                  # the type's lowest value is a value like another
+    for row in range(6):
+        _check(x[row:row + 1], [-1.0], 1, 8)
+    _check(x, [-1.0, -2.0, -1.5, -40.0, -0.25, -30.0], 6, 20)
+
+
+def test_equal_logits_go_to_the_lowest_token_and_hypothesis():
+    x = torch.zeros(4, 20000, device="cuda")
+    pa, tk, _ = _select(x, [-1.0, -1.0, -1.0, -2.0], 4, 32)
+    assert pa.tolist() == [[0] * 32] and tk.tolist() == [list(range(32))]
+    x[:, 17777] = 1.0
+    x[2, 3] = 1.0
+    pa, tk, _ = _select(x[:2].contiguous(), [-1.0, -1.0], 2, 4)
+    assert pa.tolist() == [[0, 1, 0, 0]] and tk.tolist() == [[17777, 17777, 0, 1]]
+
+
+def test_one_workspace_for_every_shape_and_a_captured_call():
+    ws = torch.zeros(va.va_beam_workspace_bytes(6, 8, 60000, 32), dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(1)
+    for groups, beams, vocab, k in ((6, 8, 60000, 32), (1, 2, 30, 3), (5, 3, 20000, 9), (6, 8, 60000, 4)):
+        _check(_rows(vocab, groups * beams, vocab, torch.bfloat16), -4 + rng.standard_normal(groups * beams), beams, k, ws=ws)
+    x = _rows(5, 8, 16000, torch.float32)
+    scores = torch.linspace(-3, -1, 8, device="cuda")
+    pa, tk = (torch.zeros(2, 4, dtype=torch.int32, device="cuda") for _ in range(2))
+    sc = torch.zeros(2, 4, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        va.va_beam_select(x, scores, 4, pa, tk, sc, ws)
+    for seed in range(3):
+        x.copy_(_rows(50 + seed, 8, 16000, torch.float32))
+        graph.replay()
+        want = P.beam_select(x.double().cpu().numpy(), scores.double().tolist(), 4, 4)
+        assert want[3] < 2.0 ** -17 or (pa.tolist() == want[0].tolist() and tk.tolist() == want[1].tolist())

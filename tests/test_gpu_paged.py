@@ -1,0 +1,291 @@
+"""Coding into pages and verify attention over them, against the oracle (oracle/paged.py)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.paged as P
+import speculative_decode_verify_gb300 as va
+from paged_cases import Cache, attention_bounds, bf16, ints
+
+pytestmark = pytest.mark.gpu
+D = 128
+SCALE = D ** -0.5
+
+
+def _same_codes(got, want, fmt):
+    """The same values (a zero's sign is free); NaN codes are compared as bytes."""
+    got, want = got.view(np.uint8), want.view(np.uint8)
+    nan = (want & 0x7F) == 0x7F if fmt == "e4m3" else np.zeros(want.shape, bool)
+    np.testing.assert_array_equal(got[nan], want[nan])
+    np.testing.assert_array_equal(P.decode(got, fmt)[~nan], P.decode(want, fmt)[~nan])
+
+
+def _append(c, live, rows, dev, seed=1, spread=1.0, special=False):
+    """Append rows on the GPU pools ``dev`` and in the cache's own arrays; returns the status word."""
+    rng = np.random.default_rng(seed)
+    new, status = {}, torch.zeros(1, dtype=torch.int32, device="cuda")
+    for w in "kv":
+        x = rng.standard_normal((len(c.lens), rows, c.kv, D)).astype(np.float32) * spread
+        if special:
+            x[:, 0, 0, :5] = [np.inf, -np.inf, np.nan, 1e-30, 0.0]
+            x[:, -1, -1] = 0.0
+        new[w] = bf16(x)
+    va.kv_page_append_b8(new["k"][0].cuda(), new["v"][0].cuda(), ints(live), ints(c.lens), ints(c.table), *dev,
+                         dev_status=status)
+    for w in "kv":
+        for b, n in enumerate(c.lens):
+            if live[b] > 0:
+                P.append(new[w][1][b].astype(np.float32), n - live[b], n, c.table[b], c.codes[w][0], c.scale[w][0], c.fmt)
+    return int(status.item())
+
+
+def _check_pool(c, dev):
+    for i, w in enumerate("kv"):
+        _same_codes(dev[i].view(torch.uint8).cpu().numpy(), c.codes[w][0], c.fmt)
+        np.testing.assert_array_equal(dev[2 + i].cpu().numpy(), c.scale[w][0])   # NaN where none was written
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("lens,live,rows,kv", [
+    ([1, 16, 17, 64, 65, 130], [1, 1, 1, 1, 1, 1], 1, 1),
+    ([5, 23, 64, 70, 128, 3], [5, 6, 0, 6, 3, 3], 6, 2),          # a sequence without rows, blocks begun and new
+    ([200, 333], [200, 150], 200, 3),                              # prompts: whole, and behind a history
+    ([8], [8], 8, 8),
+])
+@pytest.mark.parametrize("spread", [1.0, 30.0])                    # 30: the older rows of a block are coded again
+def test_append_is_the_oracles_bit_for_bit(fmt, lens, live, rows, kv, spread):
+    c = Cache(21, [n - r for n, r in zip(lens, live)], kv, fmt, spare=20)
+    free = [p for p in range(c.pages) if c.refs[p] == 0]
+    c.table = [r + [-1] * 8 for r in c.table]
+    c.lens = list(lens)
+    for b, n in enumerate(lens):
+        for x in range(-(-n // 64)):
+            if c.table[b][x] < 0:
+                c.table[b][x] = free.pop()
+    dev = c.dev(0)
+    assert _append(c, live, rows, dev, spread=spread) == 0
+    _check_pool(c, dev)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_append_codes_infinities_and_nan_and_says_so(fmt):
+    c = Cache(22, [37, 64], 2, fmt)
+    dev = c.dev(0)
+    assert _append(c, [4, 2], 4, dev, special=True) == 512
+    _check_pool(c, dev)
+
+
+@pytest.mark.parametrize("bad,bit", [("count", 1024), ("length", 4), ("page", 128), ("above", 1024)])
+def test_append_leaves_a_wrong_sequence_alone(bad, bit):
+    c = Cache(23, [40, 80, 70], 1, "e4m3")
+    dev = c.dev(0)
+    before = [t.clone() for t in dev]
+    lens, live, table = list(c.lens), [2, 2, 2], [list(r) for r in c.table]
+    if bad == "count":
+        live[1] = 3
+    elif bad == "length":
+        lens[1] = 64 * len(table[1]) + 1
+    elif bad == "above":
+        lens[1] = 1
+    else:
+        table[1][1] = c.pages
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    new = torch.ones(3, 2, 1, D, dtype=torch.bfloat16, device="cuda")
+    va.kv_page_append_b8(new, new, ints(live), ints(lens), ints(table), *dev, dev_status=status)
+    assert int(status.item()) == bit
+    mine = [p for p in c.table[1] if p >= 0]
+    for a, b in zip(dev, before):
+        a, b = a.cpu().numpy(), b.cpu().numpy()
+        np.testing.assert_array_equal(a[mine].view(np.uint8), b[mine].view(np.uint8))
+        assert any(not np.array_equal(a[p].view(np.uint8), b[p].view(np.uint8)) for p in c.table[0] if p >= 0)
+
+
+# ------------------------------------------------------------------------------------------------ attention
+def _attend(c, dev, live, rows, group, window=0, sink=None, scale=SCALE, seed=9, spread=1.0, table=None, lens=None,
+            ws=None, qs=None):
+    heads = c.kv * group
+    rng = np.random.default_rng(seed)
+    qt, qn = bf16(rng.standard_normal((len(c.lens), rows, heads, D)) * spread) if qs is None else qs
+    n = len(c.lens)
+    if ws is None:
+        ws = torch.zeros(va.va_paged_workspace_bytes(n, rows, c.kv, group), dtype=torch.uint8, device="cuda")
+    out = torch.full((n, rows, heads, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n, rows, heads), float("nan"), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sk = None if sink is None else torch.tensor(sink, dtype=torch.float32, device="cuda")
+    va.verify_attn_paged_b8(qt.cuda(), ints(live), ints(lens or c.lens), ints(table or c.table), *dev, scale, sk, ws, out,
+                            lse, window=window, dev_status=status)
+    return qn, out.double().cpu().numpy(), lse.double().cpu().numpy(), int(status.item())
+
+
+def _check(c, got, live, window=0, sink=None, scale=SCALE, table=None, status=0):
+    qn, out, lse, st = got
+    want = P.attention(qn, live, c.lens, table or c.table, c.codes["k"][0], c.codes["v"][0], c.scale["k"][0],
+                       c.scale["v"][0], c.fmt, scale, sink, window)
+    assert st == status
+    tol_out, tol_lse = attention_bounds(*want)
+    assert np.array_equal(np.isfinite(lse), np.isfinite(want[1]))
+    some = np.isfinite(want[1])
+    assert np.all(np.abs(lse[some] - want[1][some]) <= tol_lse[some])
+    assert np.all(np.isfinite(out)) and np.all(np.abs(out - want[0]) <= tol_out), np.max(np.abs(out - want[0]) / tol_out)
+    for b, n in enumerate(live):
+        assert np.all(out[b, n:] == 0) and np.all(lse[b, n:] == -np.inf)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("lens,live,rows,kv,group", [
+    ([1], [1], 1, 1, 1),
+    ([1, 15, 16, 17, 63, 64, 65, 129], [1] * 8, 1, 1, 6),
+    ([300, 0, 77, 8], [8, 0, 3, 8], 8, 2, 6),                       # 48 matrix rows; an empty sequence
+    ([64, 640, 33], [5, 2, 0], 5, 3, 3),
+    ([900, 200], [7, 8], 8, 1, 8),                                  # 64 matrix rows
+    ([1000, 31, 450], [2, 1, 2], 2, 4, 5),
+    ([128, 70], [3, 4], 4, 1, 8),                                   # 32
+    ([190, 66], [3, 3], 3, 2, 8),                                   # 24
+    ([222, 99, 512], [5, 5, 1], 5, 2, 7),                           # 35
+    ([222, 99], [8, 6], 8, 1, 5),                                   # 40
+    ([222, 99], [8, 1], 8, 1, 7),                                   # 56
+])
+def test_attention_matches_the_oracle(fmt, lens, live, rows, kv, group):
+    c = Cache(31, lens, kv, fmt)
+    sink = list(np.linspace(-2, 3, kv * group))
+    _check(c, _attend(c, c.dev(0), live, rows, group, sink=sink), live, sink=sink)
+    _check(c, _attend(c, c.dev(0), live, rows, group), live)
+
+
+@pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 65, 200, 10 ** 6])
+def test_windows(window):
+    """Entries below every window are -1: those pages have been freed."""
+    c = Cache(32, [500, 64, 3, 129], 2, "int8")
+    live = [6, 6, 3, 1]
+    table = [list(r) for r in c.table]
+    for b, n in enumerate(c.lens):
+        for x in range(max(0, n - live[b] - window + 1) // 64):
+            table[b][x] = -1
+    _check(c, _attend(c, c.dev(0), live, 6, 2, window=window, table=table), live, window=window)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("spread,scale", [(40.0, SCALE), (1.0, -0.3), (1.0, 0.0), (1e-4, 5.0), (1.0, 3.0)])
+def test_peaky_flat_and_negative_scores(fmt, spread, scale):
+    c = Cache(33, [700, 90], 1, fmt)
+    _check(c, _attend(c, c.dev(0), [3, 4], 4, 6, scale=scale, spread=spread), [3, 4], scale=scale)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_scales_that_differ_by_orders_of_magnitude(fmt):
+    c = Cache(34, [400, 400], 2, fmt)
+    rng = np.random.default_rng(2)
+    for w, low, high in (("k", -3, 0), ("v", -12, 12)):
+        s = c.scale[w]
+        f = 10.0 ** rng.uniform(low, high, s.shape)
+        c.scale[w] = (s * np.sort(f, axis=1 if w == "k" else 3)).astype(np.float32)
+    c.scale["v"][:, c.table[0][2]] = 0.0                             # rows of zeros
+    _check(c, _attend(c, c.dev(0), [2, 2], 2, 6), [2, 2])
+
+
+def test_pages_that_are_none_are_masked_and_told():
+    c = Cache(35, [300, 200, 64], 1, "e4m3")
+    for bad in (-1, c.pages, 2 ** 31 - 1, -7):
+        table = [list(r) for r in c.table]
+        table[0][1] = table[2][0] = bad
+        table[1][3] = table[1][0]
+        for sink in (None, [0.5, 1.5]):
+            _check(c, _attend(c, c.dev(0), [2, 1, 2], 2, 2, table=table, sink=sink), [2, 1, 2], table=table, sink=sink,
+                   status=128)
+
+
+def test_wrong_counts_make_an_empty_sequence():
+    c = Cache(36, [300, 200, 64], 1, "e4m3")
+    for live, lens, bit in (([2, 3, 2], None, 1024), ([2, -1, 2], None, 1024), ([2, 2, 2], [300, 64 * 6 + 1, 64], 4),
+                            ([2, 2, 2], [300, 1, 64], 1024)):
+        qn, out, lse, st = _attend(c, c.dev(0), live, 2, 2, lens=lens)
+        assert st == bit and np.all(out[1] == 0) and np.all(lse[1] == -np.inf)
+        ok = [2, 0, 2]
+        want = P.attention(qn, ok, c.lens, c.table, c.codes["k"][0], c.codes["v"][0], c.scale["k"][0], c.scale["v"][0],
+                           "e4m3", SCALE)
+        tol, _ = attention_bounds(*want)
+        assert np.all(np.abs(out - want[0]) <= tol)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_many_short_and_one_long(fmt):
+    """Work split over a long axis next to sequences that share one CTA; shared pages."""
+    lens = [3000] + [int(n) for n in np.random.default_rng(4).integers(0, 150, 70)]
+    c = Cache(37, lens, 2, fmt)
+    live = [min(n, 1 + i % 2) for i, n in enumerate(lens)]
+    _check(c, _attend(c, c.dev(0), live, 2, 3), live)
+
+
+def test_one_workspace_serves_calls_of_every_shape_and_replays():
+    c = Cache(38, [200, 333, 64], 2, "e4m3")
+    dev = c.dev(0)
+    ws = torch.zeros(va.va_paged_workspace_bytes(3, 8, 2, 8), dtype=torch.uint8, device="cuda")
+    for rows, group in ((8, 8), (1, 1), (3, 6), (8, 6)):
+        live = [min(rows, 2), rows, rows]
+        _check(c, _attend(c, dev, live, rows, group, ws=ws), live)
+    # a captured call, replayed over changed lengths and interleaved with an eager call on the same workspace
+    rows, group = 2, 6
+    qt, qn = bf16(np.random.default_rng(1).standard_normal((3, rows, 12, D)))
+    q, live, lens, table = qt.cuda(), ints([1, 1, 1]), ints([1, 1, 1]), ints(c.table)
+    out, lse = torch.zeros(3, rows, 12, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, rows, 12, device="cuda")
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        va.verify_attn_paged_b8(q, live, lens, table, *dev, SCALE, None, ws, out, lse)
+    for now, n in (([200, 333, 64], [2, 1, 0]), ([70, 64, 2], [2, 2, 2]), ([200, 333, 64], [2, 1, 0])):
+        lens.copy_(ints(now))
+        live.copy_(ints(n))
+        graph.replay()
+        c2 = c
+        want = P.attention(qn, n, now, c2.table, c2.codes["k"][0], c2.codes["v"][0], c2.scale["k"][0], c2.scale["v"][0],
+                           "e4m3", SCALE)
+        tol, _ = attention_bounds(*want)
+        got = out.double().cpu().numpy()
+        assert np.all(np.abs(got - want[0]) <= tol)
+        first = out.clone()
+        _check(c, _attend(c, dev, [1, 2, 2], 2, 3, ws=ws), [1, 2, 2])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, out)             # the same inputs give the same bits
+
+
+def test_another_stream():
+    c = Cache(39, [500, 77], 2, "int8")
+    dev = c.dev(0)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = _attend(c, dev, [4, 3], 4, 6)
+    _check(c, got, [4, 3])
+
+
+def test_positions_and_pool_offsets_past_32_bits_of_bytes():
+    """A pool of over 4 GB (page numbers whose byte offsets pass 2^32) and a history of 131,080 positions."""
+    kv, fmt, n = 8, "int8", 131080
+    need = -(-n // 64)
+    pages = 4 * 2 ** 30 // (kv * 64 * D) + need + 8
+    codes = [torch.zeros(pages, kv, 64, D, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scale = [torch.zeros(pages, kv, 4, device="cuda") for _ in range(2)]
+    first = pages - need
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for c, s in zip(codes, scale):
+        c[first:] = torch.randint(-127, 128, c[first:].shape, generator=g, device="cuda", dtype=torch.int8)
+        s[first:] = torch.rand(s[first:].shape, generator=g, device="cuda") * 0.02
+    table = torch.arange(first, pages, dtype=torch.int32, device="cuda")[None]
+    q = torch.randn(1, 2, kv, D, generator=g, device="cuda").to(torch.bfloat16)
+    out, lse = torch.zeros_like(q), torch.zeros(1, 2, kv, device="cuda")
+    ws = torch.zeros(va.va_paged_workspace_bytes(1, 2, kv, 1), dtype=torch.uint8, device="cuda")
+    va.verify_attn_paged_b8(q, ints([2]), ints([n]), table, *codes, *scale, SCALE, None, ws, out, lse)
+    for h in range(kv):
+        k, v = ((c[first:, h].double() * s[first:, h].double().repeat_interleave(16, 1)[..., None]).reshape(-1, D)[:n]
+                for c, s in zip(codes, scale))
+        for r in range(2):
+            z = SCALE * (k[:n - 1 + r] @ q[0, r, h].double())
+            w = torch.softmax(z, 0)
+            want, size = w @ v[:n - 1 + r], w @ v[:n - 1 + r].abs()
+            reach = SCALE * float((k.abs() @ q[0, r, h].double().abs()).max())
+            tol, tol_lse = attention_bounds(want.cpu().numpy(), float(torch.logsumexp(z, 0)), size.cpu().numpy(),
+                                            np.array(reach))
+            assert np.all(np.abs(out[0, r, h].double().cpu().numpy() - want.cpu().numpy()) <= tol)
+            assert abs(float(lse[0, r, h]) - float(torch.logsumexp(z, 0))) <= tol_lse
