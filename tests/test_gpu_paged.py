@@ -97,7 +97,8 @@ def test_append_leaves_a_wrong_sequence_alone(bad, bit):
     for a, b in zip(dev, before):
         a, b = a.cpu().numpy(), b.cpu().numpy()
         np.testing.assert_array_equal(a[mine].view(np.uint8), b[mine].view(np.uint8))
-        assert any(not np.array_equal(a[p].view(np.uint8), b[p].view(np.uint8)) for p in c.table[0] if p >= 0)
+        if a.shape[-1] == D:                                      # codes of another sequence have changed
+            assert any(not np.array_equal(a[p].view(np.uint8), b[p].view(np.uint8)) for p in c.table[0] if p >= 0)
 
 
 # ------------------------------------------------------------------------------------------------ attention

@@ -31,6 +31,7 @@ class Pool:
                              dtype=torch.uint8, device="cuda")
 
     def moved(self, pairs):
+        pairs = list(pairs)
         for a in self.host:
             for s, d in pairs:
                 a[:, d] = a[:, s]
