@@ -59,13 +59,14 @@ def append(new, start, end, table_row, codes, scale, fmt):
 
 
 def attention(q, live, lens, table, k_codes, v_codes, k_scale, v_scale, fmt, scale, sink=None, window=0):
-    """q [n_seqs, n_rows, heads, 128] float64 -> (out, lse, spread): the output, the log-sum-exp, and per element
-    sum_j w_j |v_j| and per row max_j scale sum_d |q_d k_jd| (what a kernel's error bounds are made of)."""
+    """q [n_seqs, n_rows, heads, 128] float64 -> (out, lse, size, reach, top): the output, the log-sum-exp, per element
+    sum_j w_j |v_j|, per row max_j scale sum_d |q_d k_jd| and the number of keys times the largest value that a
+    code of the sequence's values could stand for (what a kernel's error bounds are made of)."""
     n, rows, heads, _ = q.shape
     kv = k_codes.shape[1]
     g = heads // kv
     out, size = np.zeros(q.shape), np.zeros(q.shape)
-    lse, reach = np.full(q.shape[:3], -np.inf), np.zeros(q.shape[:3])
+    lse, reach, top_v = np.full(q.shape[:3], -np.inf), np.zeros(q.shape[:3]), np.zeros(q.shape[:3])
     for b in range(n):
         for r in range(int(live[b])):
             p = int(lens[b]) - int(live[b]) + r
@@ -75,7 +76,10 @@ def attention(q, live, lens, table, k_codes, v_codes, k_scale, v_scale, fmt, sca
             for h in range(kv):
                 k = decode(k_codes[pg, h, of], fmt).astype(np.float64) * k_scale[pg, h, of // BLOCK, None].astype(np.float64)
                 v = decode(v_codes[pg, h, of], fmt).astype(np.float64) * v_scale[pg, h, of // BLOCK, None].astype(np.float64)
+                every = {int(table[b][x]) for x in range(-(-int(lens[b]) // PAGE))} & set(range(k_codes.shape[0]))
+                largest = max([float(np.nanmax(v_scale[list(every), h]))] if every else [0.0]) * float(TOP[fmt])
                 for m in range(h * g, (h + 1) * g):
+                    top_v[b, r, m] = len(js) * largest
                     s = scale * (k @ q[b, r, m])
                     z = s if sink is None else np.append(s, float(sink[m]))
                     if not z.size or z.max() == -np.inf:
@@ -85,7 +89,7 @@ def attention(q, live, lens, table, k_codes, v_codes, k_scale, v_scale, fmt, sca
                     w = np.exp(s - total)
                     out[b, r, m], size[b, r, m], lse[b, r, m] = w @ v, w @ np.abs(v), total
                     reach[b, r, m] = abs(scale) * (np.abs(k) @ np.abs(q[b, r, m])).max() if js else 0.0
-    return out, lse, size, reach
+    return out, lse, size, reach, top_v
 
 
 def reorder(table, lens, refs, src, group=0):

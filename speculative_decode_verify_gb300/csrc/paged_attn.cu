@@ -1,101 +1,139 @@
-// verify_attn_paged_b8: verify attention of a batch of sequences over their pages.
+// verify_attn_paged_b8: the call, and the second of its two launches, which merges what the split kernel
+// (paged_attn.cuh) left in parts and writes the rows that see nothing.
 #include <cmath>
 
-#include "paged.cuh"
-#include "tc_ptx.cuh"
+#include "paged_attn.cuh"
 
 namespace va {
+namespace tc {
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();   // attn_tc.cu
+}  // namespace tc
+
 namespace paged {
 
-struct AttnPagedArgs {
-    const uint16_t* q;
-    const int32_t *n_live, *lens, *table;
-    const uint8_t *k_codes, *v_codes;
-    const float *k_scale, *v_scale;
-    const float* sink;
-    uint16_t* out;
-    float* out_lse;
-    int32_t* dev_status;
-    float scale;
-    int n_seqs, n_rows, n_kv, group, max_pages, n_pages, window;
-};
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
-// One warp per (sequence, row, query head): 32 keys at a time, a key a lane for the scores, four dimensions a
-// lane for the output.
-template <bool kInt8>
-__global__ void __launch_bounds__(32) attn_paged_kernel(const AttnPagedArgs a) {
-    __shared__ float qs[kD];
+// CTA (unit, y): unit = (sequence, KV head); its (row, query head) pairs y, y + gridDim.y, ..
+// Few parts: a warp a pair.  Many (a long history over many CTAs): the warps share a pair's parts, each a
+// consecutive run with four chains of its own in order, and join through shared memory; the order is fixed.
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnPagedArgs a) {
+    __shared__ long long sums[2 * kJoinWarps];
+    __shared__ float4 acc_s[kJoinWarps][32];
+    __shared__ float2 ml_s[kJoinWarps];
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const int lane = threadIdx.x, heads = a.n_kv * a.group;
-    const int head = blockIdx.x % heads, r = blockIdx.x / heads % a.n_rows, b = blockIdx.x / heads / a.n_rows;
-    const int h = head / a.group;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x / a.n_kv, h = blockIdx.x % a.n_kv, heads = a.n_kv * a.group;
+    // tiles before this sequence, and of all
+    long long before = 0, total = 0;
+    for (int s = tid; s < a.n_seqs; s += kJoinThreads) {
+        const Seq q = load_seq(a.lens, a.n_live, s, a.n_rows, a.max_pages);
+        const long long n = (long long)span_of(q.len, q.live, a.window).n * a.n_kv;
+        total += n;
+        if (s < b) before += n;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lane == 0) {
+        sums[warp] = before;
+        sums[kJoinWarps + warp] = total;
+    }
+    __syncthreads();
+    before = total = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        before += sums[w];
+        total += sums[kJoinWarps + w];
+    }
     const Seq sq = load_seq(a.lens, a.n_live, b, a.n_rows, a.max_pages);
-    int status = sq.status;
-    const size_t row = ((size_t)b * a.n_rows + r) * heads + head;
-    float m = -INFINITY, l = 0.0f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    const bool live = r < sq.live;
-    if (live) {
-        for (int e = 0; e < 4; ++e) qs[lane + 32 * e] = __uint_as_float((uint32_t)a.q[row * kD + lane + 32 * e] << 16);
-        __syncwarp();
-        const int p = sq.len - sq.live + r;
-        const int lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
-        for (int j0 = lo / 32 * 32; j0 <= p; j0 += 32) {
-            const int j = j0 + lane;
-            const int page = __ldcg(a.table + (size_t)b * a.max_pages + j0 / kPage);
-            if (page < 0 || page >= a.n_pages) {
-                status |= VA_DEV_BAD_PAGE;
-                continue;
-            }
-            const size_t base = (size_t)page * a.n_kv + h;
-            float s = -INFINITY;
-            if (j >= lo && j <= p) {
-                const uint32_t* kr = reinterpret_cast<const uint32_t*>(a.k_codes + (base * kPage + j % kPage) * kD);
-                float acc = 0.0f;
-                for (int w = 0; w < kD / 4; ++w) {
-                    float x[4];
-                    decode4<kInt8>(__ldcg(kr + w), x);
-                    for (int e = 0; e < 4; ++e) acc = fmaf(x[e], qs[4 * w + e], acc);
-                }
-                s = acc * __ldcg(a.k_scale + base * kBlocks + j % kPage / kBlock) * a.scale;
-            }
-            float mx = s;
-            for (int o2 = 16; o2 > 0; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
-            const float mn = fmaxf(m, mx);
-            const float f = m == -INFINITY ? 0.0f : expf(m - mn);
-            const float pr = s == -INFINITY ? 0.0f : expf(s - mn);
-            m = mn;
-            l = l * f + pr;
-            for (int e = 0; e < 4; ++e) o[e] *= f;
-            for (int t = 0; t < 32; ++t) {
-                const float pt = __shfl_sync(0xffffffffu, pr, t);
-                const int jt = j0 + t;
-                if (jt < lo || jt > p) continue;
-                float x[4];
-                decode4<kInt8>(__ldcg(reinterpret_cast<const uint32_t*>(a.v_codes + (base * kPage + jt % kPage) * kD) + lane), x);
-                const float vs = __ldcg(a.v_scale + base * kBlocks + jt % kPage / kBlock);
-                for (int e = 0; e < 4; ++e) o[e] = fmaf(pt * vs, x[e], o[e]);
+    const int n_tiles = span_of(sq.len, sq.live, a.window).n;
+    // padding rows
+    for (int c = blockIdx.y * kJoinWarps + warp; c < (a.n_rows - sq.live) * a.group; c += gridDim.y * kJoinWarps) {
+        const size_t row = ((size_t)b * a.n_rows + sq.live + c / a.group) * heads + h * a.group + c % a.group;
+        reinterpret_cast<uint2*>(a.out + row * kD)[lane] = make_uint2(0u, 0u);
+        if (lane == 0 && a.out_lse) a.out_lse[row] = -INFINITY;
+    }
+    if (n_tiles == 0) return;
+    const int n_ctas = (int)min((long long)a.n_ctas, total);
+    const long long first = before + (long long)h * n_tiles;
+    const int c_first = (int)(((first + 1) * n_ctas - 1) / total), c_last = (int)(((first + n_tiles) * n_ctas - 1) / total);
+    if (c_first == c_last) return;   // the split kernel has written the rows
+    const int parts = c_last - c_first + 1;
+    auto place = [&](int c) {        // the part of CTA c: its first segment's unless the head began inside it
+        return (size_t)(2 * c + (cta_begin(c, n_ctas, total) >= first ? 0 : 1)) * kMaxCols;
+    };
+    const bool shared = parts > 16;
+    const int n_cols = sq.live * a.group, step = shared ? (int)gridDim.y : (int)gridDim.y * kJoinWarps;
+    for (int col = shared ? (int)blockIdx.y : (int)blockIdx.y * kJoinWarps + warp; col < n_cols; col += step) {
+        const int p0 = shared ? parts * warp / kJoinWarps : 0, p1 = shared ? parts * (warp + 1) / kJoinWarps : parts;
+        // the parts' references and sums, one a lane (a warp has at most 32: 160 / 8, or 16)
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (lane < p1 - p0) ml = __ldcg(a.part_ml + place(c_first + p0 + lane) + col);
+        float top = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float by = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.0f) : exp2f(ml.x - top);
+        float sum = by * ml.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 10
+        for (int p = p0; p < p1; ++p) {
+            const float w = __shfl_sync(0xffffffffu, by, p - p0);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (place(c_first + p) + col) * kD) + lane);
+            acc.x += w * v.x;
+            acc.y += w * v.y;
+            acc.z += w * v.z;
+            acc.w += w * v.w;
+        }
+        if (shared) {
+            __syncthreads();
+            acc_s[warp][lane] = acc;
+            if (lane == 0) ml_s[warp] = make_float2(top, sum);
+            __syncthreads();
+            if (warp != 0) continue;
+            top = ml_s[0].x;
+#pragma unroll
+            for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, ml_s[w].x);
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) {
+                const float2 one = ml_s[w];
+                const float f = one.x == -INFINITY ? (one.y != one.y ? one.y : 0.0f) : exp2f(one.x - top);
+                const float4 v = acc_s[w][lane];
+                acc.x += f * v.x;
+                acc.y += f * v.y;
+                acc.z += f * v.z;
+                acc.w += f * v.w;
+                sum += f * one.y;
             }
         }
-        for (int o2 = 16; o2 > 0; o2 >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o2);
+        const int head = h * a.group + col % a.group;
+        const size_t row = ((size_t)b * a.n_rows + col / a.group) * heads + head;
+        const float lse = finish(acc, top, sum, a.sink, head);
+        store_row(a.out + row * kD + 4 * lane, acc);
+        if (lane == 0 && a.out_lse) a.out_lse[row] = lse;
     }
-    float L = -INFINITY;
-    if (live) {
-        const float sink = a.sink ? a.sink[head] : -INFINITY;
-        const float top = fmaxf(m, sink);
-        if (top != -INFINITY) {
-            const float em = m == -INFINITY ? 0.0f : expf(m - top);
-            const float total = l * em + (sink == -INFINITY ? 0.0f : expf(sink - top));
-            for (int e = 0; e < 4; ++e) o[e] = total > 0.0f ? o[e] * em / total : 0.0f;
-            L = top + logf(total);
-        }
-    }
-    for (int e = 0; e < 4; ++e) {
-        const uint32_t u = __float_as_uint(o[e]);
-        a.out[row * kD + 4 * lane + e] = (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
-    }
-    if (lane == 0 && a.out_lse) a.out_lse[row] = L;
-    if (lane == 0 && status && a.dev_status) atomicOr(a.dev_status, status);
+}
+
+// A pool as rows of 128 codes; boxes of one head's 64 positions, swizzled.
+static bool encode_pool(CUtensorMap* map, const void* base, long long rows) {
+    tc::EncodeTiledFn fn = tc::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)kD};
+    const cuuint32_t box[2] = {(cuuint32_t)kD, (cuuint32_t)kPage};
+    const cuuint32_t elem[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace paged
@@ -107,7 +145,7 @@ size_t va_paged_workspace_bytes(int n_seqs, int n_rows, int n_kv_heads, int grou
     if (n_seqs < 1 || n_seqs > VA_PAGED_MAX_SEQS || n_rows < 1 || n_rows > VA_MAX_ROWS || n_kv_heads < 1 ||
         n_kv_heads > VA_PAGED_MAX_KV_HEADS || group < 1 || group > VA_PAGED_MAX_GROUP)
         return 0;
-    return 256;
+    return va::paged::kWorkspaceBytes;   // two parts a CTA, whatever the batch
 }
 
 va_status verify_attn_paged_b8(const va_bf16* q, int n_seqs, int n_rows, int n_kv_heads, int group,
@@ -124,18 +162,31 @@ va_status verify_attn_paged_b8(const va_bf16* q, int n_seqs, int n_rows, int n_k
     if (format != VA_B8_E4M3 && format != VA_B8_INT8) return VA_INVALID_ARG;
     va_status st = check_pool(k_codes, v_codes, k_scale, v_scale, 1, n_pages, n_kv_heads);
     if (st != VA_OK) return st;
+    const int sms = va::device_sm_count();
     AttnPagedArgs a;
     a.q = q; a.n_live = n_live; a.lens = lens; a.table = table;
-    a.k_codes = static_cast<const uint8_t*>(k_codes); a.v_codes = static_cast<const uint8_t*>(v_codes);
     a.k_scale = k_scale; a.v_scale = v_scale; a.sink = sink; a.out = out; a.out_lse = out_lse;
-    a.dev_status = dev_status; a.scale = scale;
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + kPartFloats);
+    a.dev_status = dev_status;
+    a.scale_log2 = scale * 1.4426950408889634f;
     a.n_seqs = n_seqs; a.n_rows = n_rows; a.n_kv = n_kv_heads; a.group = group;
     a.max_pages = max_pages; a.n_pages = n_pages; a.window = window;
+    a.n_ctas = sms > 0 && sms < kMaxCtas ? sms : kMaxCtas;
+    CUtensorMap mk, mv;
+    const long long rows = (long long)n_pages * n_kv_heads * kPage;
+    if (!encode_pool(&mk, k_codes, rows) || !encode_pool(&mv, v_codes, rows)) return VA_CUDA_ERROR;
+    st = launched(format == VA_B8_INT8 ? launch_attn_int8(a, mk, mv, (cudaStream_t)stream)
+                                       : launch_attn_e4m3(a, mk, mv, (cudaStream_t)stream));
+    if (st != VA_OK) return st;
+    // about one CTA an SM: a unit each where there are enough, else its pairs are shared out
+    const int units = n_seqs * n_kv_heads, pairs = n_rows * group;
+    const int share = units >= a.n_ctas ? 1 : (a.n_ctas + units - 1) / units;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    va::pdl_config(&cfg, attr, dim3((unsigned)(n_seqs * n_rows * n_kv_heads * group)), dim3(32), 0, (cudaStream_t)stream);
-    return launched(format == VA_B8_INT8 ? cudaLaunchKernelEx(&cfg, attn_paged_kernel<true>, a)
-                                         : cudaLaunchKernelEx(&cfg, attn_paged_kernel<false>, a));
+    va::pdl_config(&cfg, attr, dim3((unsigned)units, (unsigned)(share < pairs ? share : pairs)), dim3(kJoinThreads), 0,
+                   (cudaStream_t)stream);
+    return launched(cudaLaunchKernelEx(&cfg, attn_join_kernel, a));
 }
 
 }  // extern "C"

@@ -1,0 +1,670 @@
+// The split kernel of verify_attn_paged_b8 (instantiated per format in paged_attn_e4m3.cu / paged_attn_int8.cu).
+//
+// Work.  A sequence's visible pages, times its KV heads, are its tiles (64 keys of one head); all tiles of the
+// batch in (sequence, head, page) order are dealt evenly to one CTA an SM, whatever the lengths: CTA c of C takes
+// tiles [c N / C, (c + 1) N / C).  A run of tiles of one (sequence, head) in a CTA is a segment.  A segment that
+// covers its head writes the output itself; the others (at most the first and the last of a CTA) leave partial
+// sums that a second launch merges.
+//
+// Inside a CTA one warp feeds a ring of pages by TMA and eight warps consume it: teams of RG warps take the tiles
+// in turn, warp w of a team for its own 8 RT of the (row, query head) pairs, so no barrier joins the warps between
+// tiles.  With keys as the matrix rows, S^T = K Q^T and O^T = V^T P^T need as many 8-column tiles as there are
+// pairs / 8: a single token of six heads costs one, where queries as matrix rows would cost two.
+// The codes are widened to f16 in registers (exact for both formats) and multiplied by mma.sync: a tile of 16 KB
+// takes 64 RT RG of them, which is less than the time the tile takes to arrive until 48 pairs (the design doc has the
+// figures); a code is used by so few pairs that the load, not the product, bounds the call.
+//   Keys are taken in the order 0 5 2 7 4 1 6 3 of each eight: with the 128-byte swizzle of the loads, the 16-byte
+//   shared-memory reads of K (two rows a phase) and of V (four rows of even or odd order) then meet no bank twice.
+// The softmax is online, in base 2: p = 2^(t - m + 6) with m raised only when a score passes it by 8, so f16 holds
+// p <= 2^14 to 11 bits down to 2^-20 of the maximum (and to 2^-31 of it absolutely); sums are fp32.  The blocks' V
+// scales go into p relative to R, the largest so far (a power of two), which f16 would not hold by themselves.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "paged.cuh"
+#include "tc_ptx.cuh"
+
+namespace va {
+namespace paged {
+
+constexpr int kMaxCtas = 160;                 // CTAs of one call (one an SM)
+constexpr int kMaxCols = VA_MAX_ROWS * VA_PAGED_MAX_GROUP;   // 64 (row, query head) pairs of a KV head
+constexpr int kConsumers = 8;                 // consumer warps of a CTA
+// Three warpgroups of 168 registers a thread at launch (64,512 in all); the consumers' two then hold 232, the
+// producer's one 40 (59,392 + 5,120).
+constexpr int kAttnThreads = 32 * (kConsumers + 4);
+constexpr int kConsumerRegs = 232, kProducerRegs = 40;
+constexpr int kTileBytes = 2 * kHeadBytes;    // K and V codes of a tile
+constexpr uint64_t kWaitNs = 1000000000ull;   // a wait gives up after a second (VA_DEV_TIMEOUT)
+constexpr float kShift = 6.0f;                // p = 2^(t - m + kShift)
+constexpr float kLazy = 8.0f;                 // m is raised when a score passes it by this much
+constexpr int kTickets = 64;                  // segments that can be open at once in a CTA are fewer
+
+// Workspace: partial sums of 2 segments a CTA, [2 kMaxCtas][kMaxCols][128] floats, then their (m, l).
+constexpr size_t kPartFloats = (size_t)2 * kMaxCtas * kMaxCols * kD;
+constexpr size_t kWorkspaceBytes = sizeof(float) * (kPartFloats + (size_t)2 * kMaxCtas * kMaxCols * 2);
+
+struct AttnPagedArgs {
+    const uint16_t* q;
+    const int32_t *n_live, *lens, *table;
+    const float *k_scale, *v_scale;
+    const float* sink;
+    float* part_o;
+    float2* part_ml;
+    uint16_t* out;
+    float* out_lse;
+    int32_t* dev_status;
+    float scale_log2;                         // scale x log2 e
+    int n_seqs, n_rows, n_kv, group, max_pages, n_pages, window, n_ctas;
+};
+
+// The visible pages of a sequence: [first, first + n).
+struct Span {
+    int first, n;
+};
+__device__ __forceinline__ Span span_of(int len, int live, int window) {
+    Span s;
+    const int lo = window > 0 ? max(0, len - live - window + 1) : 0;
+    s.first = lo / kPage;
+    s.n = live > 0 ? (len + kPage - 1) / kPage - s.first : 0;
+    return s;
+}
+
+// CTA c of n takes tiles [cta_begin(c), cta_begin(c + 1)) of `total`; n is at most total.
+__device__ __forceinline__ long long cta_begin(int c, int n, long long total) { return (long long)c * total / n; }
+
+// One output row: the sum over pieces weighted to a common maximum, with the sink, rounded once.
+// o: unnormalised sum, (m, l): reference exponent and sum of 2^(t - m); returns the log-sum-exp.
+__device__ __forceinline__ float finish(float4& o, float m, float l, const float* sink, int head) {
+    const float s2 = sink ? sink[head] * 1.4426950408889634f : -INFINITY;
+    const float seen = l == 0.0f ? -INFINITY : m + log2f(l);
+    const float top = fmaxf(seen, s2);
+    if (top == -INFINITY && !(l != l)) {
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        return -INFINITY;
+    }
+    const float all = top + log2f(exp2f(seen - top) + exp2f(s2 - top));
+    const float f = l == 0.0f ? 0.0f : exp2f(seen - all) / l;
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+    return (l != l ? l : all) * 0.6931471805599453f;
+}
+
+__device__ __forceinline__ void store_row(uint16_t* dst, const float4& o) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
+    *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// ----------------------------------------------------------------------------- fragments
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Four codes c0..c3 of a word to f16 pairs (c0, c1) and (c2, c3).
+template <bool kInt8>
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if (kInt8) {
+        // 0x64xx is 1024 + xx: the biased code (+128) becomes the low byte, 1152 comes off again
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+        uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias), y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+        lo = *reinterpret_cast<const uint32_t*>(&x);
+        hi = *reinterpret_cast<const uint32_t*>(&y);
+    } else {
+        asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+            : "=r"(lo), "=r"(hi) : "r"(w));
+    }
+}
+
+// A wait that the warp makes as one: every lane leaves it with the same answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int& status) {
+    const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, kWaitNs));
+    if (!ok) {
+        if (!*abort) status |= VA_DEV_TIMEOUT;
+        __syncwarp();
+        *abort = 1;
+    }
+    return ok;
+}
+
+// The page of tile i is in its stage: first that its loads have been issued (*issued > i), because a barrier's
+// parity alone does not tell the use that is waited for from the one before the last; then that they are done.
+__device__ __forceinline__ bool page_wait(volatile int* issued, int i, uint32_t bar, uint32_t parity, volatile int* abort,
+                                          int& status) {
+    bool ok = true;
+    if (*issued <= i) {
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (*issued <= i && ok) ok = !*abort && ptx::globaltimer_ns() - t0 <= kWaitNs;
+    }
+    if (!__all_sync(0xffffffffu, ok)) {
+        if (!*abort) status |= VA_DEV_TIMEOUT;
+        __syncwarp();
+        *abort = 1;
+        return false;
+    }
+    return warp_wait(bar, parity, abort, status);
+}
+
+// ----------------------------------------------------------------------------- shared memory
+// RT: 8-pair tiles per warp; RG: warps of a team; kTeams teams; kStages: pages in flight.
+template <int RT, int RG>
+struct Shape {
+    static constexpr int kTeams = kConsumers / RG;
+    static constexpr int kCols = 8 * RT;                                 // pairs of a warp
+    static constexpr int kSlotFloats = kCols * kD;
+    static constexpr int kRingAt = 0;
+    static constexpr int kFixed = kConsumers * (kSlotFloats + 2 * kCols) * 4   // the warps' slots and their (m, l)
+                                  + (VA_PAGED_MAX_SEQS + 1) * 8 + VA_PAGED_MAX_SEQS * 5   // prefix, lengths, live rows
+                                  + 2048;                                      // barriers, tickets, scales, alignment
+    static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kTileBytes + 32);
+    static constexpr int kStages = kFit < 12 ? kFit : 12;
+    static constexpr int kBytes = 1024 + kFixed + kStages * (kTileBytes + 32);
+    static_assert(kStages >= 4, "the ring needs a few pages");
+};
+
+template <bool kInt8, int RT, int RG>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_paged_kernel(const AttnPagedArgs a, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v) {
+    using S = Shape<RT, RG>;
+    constexpr int NS = S::kStages, T = S::kTeams, kCols = S::kCols;
+    constexpr int KB = RT >= 3 ? 2 : 4;       // 16-key blocks per softmax step (registers)
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char* ring = base;
+    float* slots = reinterpret_cast<float*>(ring + NS * kTileBytes);
+    float2* slot_ml = reinterpret_cast<float2*>(slots + kConsumers * S::kSlotFloats);
+    long long* pre = reinterpret_cast<long long*>(slot_ml + kConsumers * kCols);
+    int* s_len = reinterpret_cast<int*>(pre + VA_PAGED_MAX_SEQS + 1);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s_len + VA_PAGED_MAX_SEQS + 2);
+    float* scales = reinterpret_cast<float*>(bars + 48);
+    int* tickets = reinterpret_cast<int*>(scales + NS * 8);
+    int* flags = tickets + RG * kTickets;     // [0] abort, [1] pages issued; from [2] on each stage's validity
+    signed char* s_live = reinterpret_cast<signed char*>(flags + 2 + 16);
+    const uint32_t full0 = ptx::smem_u32(bars), empty0 = full0 + 8 * 16, free0 = full0 + 8 * 32;
+    volatile int* abort = flags;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        ptx::tma_prefetch_desc(&map_k);
+        ptx::tma_prefetch_desc(&map_v);
+        for (int s = 0; s < NS; ++s) {
+            ptx::mbar_init(full0 + 8 * s, 1);
+            ptx::mbar_init(empty0 + 8 * s, RG);
+        }
+        for (int w = 0; w < kConsumers; ++w) ptx::mbar_init(free0 + 8 * w, 1);
+        ptx::mbar_init_fence();
+        flags[0] = flags[1] = 0;
+    }
+    for (int i = tid; i < RG * kTickets; i += kAttnThreads) tickets[i] = 0;
+    __syncthreads();
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+
+    // ---------------------------------------------------------------- plan: tiles before each sequence
+    int status = 0;
+    constexpr int kPer = (VA_PAGED_MAX_SEQS + kAttnThreads - 1) / kAttnThreads;   // sequences per thread
+    {
+        long long* sums = reinterpret_cast<long long*>(slots);
+        long long mine[kPer], sum = 0;
+        const int per = (a.n_seqs + kAttnThreads - 1) / kAttnThreads;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int b = tid * per + i;
+            mine[i] = 0;
+            if (i < per && b < a.n_seqs) {
+                const Seq s = load_seq(a.lens, a.n_live, b, a.n_rows, a.max_pages);
+                status |= s.status;
+                s_len[b] = s.len;
+                s_live[b] = (signed char)s.live;
+                mine[i] = (long long)span_of(s.len, s.live, a.window).n * a.n_kv;
+                sum += mine[i];
+            }
+        }
+        long long upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += t;
+        }
+        if (lane == 31) sums[warp] = upto;
+        __syncthreads();
+        long long before = upto - sum;
+        for (int w = 0; w < warp; ++w) before += sums[w];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int b = tid * per + i;
+            if (i < per && b < a.n_seqs) {
+                pre[b] = before;
+                before += mine[i];
+                if (b == a.n_seqs - 1) pre[a.n_seqs] = before;
+            }
+        }
+        if (status && a.dev_status && blockIdx.x == 0) atomicOr(a.dev_status, status);
+        status = 0;
+    }
+    __syncthreads();
+    const long long total = pre[a.n_seqs];
+    const int n_ctas = (int)min((long long)a.n_ctas, total);
+    if ((int)blockIdx.x >= n_ctas) return;
+    const long long c0 = cta_begin(blockIdx.x, n_ctas, total), c1 = cta_begin(blockIdx.x + 1, n_ctas, total);
+    auto find = [&](long long x) {             // the sequence whose tiles hold tile x
+        int lo = 0, hi = a.n_seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= x) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    };
+
+    if (warp >= kConsumers) {
+        ptx::set_max_regs_dec<kProducerRegs>();
+        if (warp > kConsumers) return;
+        // ------------------------------------------------------------ producer: one lane per tile, in turn
+        const int n = (int)(c1 - c0);
+        int issued = 0;
+        bool given_up = false;
+        for (int i0 = 0; i0 < n && !given_up; i0 += 32) {
+            const int i = i0 + lane;
+            int row = -1;
+            if (i < n) {
+                const int b = find(c0 + i);
+                const Span sp = span_of(s_len[b], s_live[b], a.window);
+                const unsigned within = (unsigned)(c0 + i - pre[b]);
+                const int h = (int)(within / (unsigned)sp.n), t = sp.first + (int)(within % (unsigned)sp.n);
+                const int page = __ldcg(a.table + (size_t)b * a.max_pages + t);
+                if (page >= 0 && page < a.n_pages) row = page * a.n_kv + h;
+                else status |= VA_DEV_BAD_PAGE;
+            }
+            for (int l = 0; l < 32 && i0 + l < n; ++l) {
+                if (lane == l) {
+                    const int s = i % NS, use = i / NS;
+                    if (use > 0 && !ptx::mbar_wait(empty0 + 8 * s, (use - 1) & 1, abort, kWaitNs)) {
+                        if (!*abort) status |= VA_DEV_TIMEOUT;
+                        *abort = 1;
+                        given_up = true;
+                    } else {
+                        const uint32_t bar = full0 + 8 * s, dst = ptx::smem_u32(ring + s * kTileBytes);
+                        flags[2 + s] = row >= 0;
+                        if (row >= 0) {
+                            const uint32_t sc = ptx::smem_u32(scales + 8 * s);
+                            ptx::mbar_arrive_expect_tx(bar, kTileBytes + 32);
+                            ptx::tma_load_2d(dst, &map_k, 0, row * kPage, bar);
+                            ptx::tma_load_2d(dst + kHeadBytes, &map_v, 0, row * kPage, bar);
+                            ptx::bulk_load(sc, a.k_scale + (size_t)row * kBlocks, 16, bar);
+                            ptx::bulk_load(sc + 16, a.v_scale + (size_t)row * kBlocks, 16, bar);
+                        } else {
+                            ptx::mbar_arrive(bar);
+                        }
+                        issued = i + 1;
+                        __threadfence_block();
+                        *(volatile int*)(flags + 1) = issued;
+                    }
+                }
+                given_up = __any_sync(0xffffffffu, given_up);
+                if (given_up) break;
+            }
+        }
+        // no CTA ends with copies under way, even if its consumers gave up
+        issued = __reduce_max_sync(0xffffffffu, issued);
+        for (int i = max(0, issued - NS) + lane; i < issued; i += 32)
+            ptx::mbar_wait(full0 + 8 * (i % NS), (i / NS) & 1, nullptr, kWaitNs);
+    } else {
+        // ------------------------------------------------------------ consumers
+        ptx::set_max_regs_inc<kConsumerRegs>();
+        const int team = warp / RG, rg = warp % RG;
+        const int g = lane >> 2, j = lane & 3;
+        const int kperm = (g & ~1) ^ ((g & 1) ? 5 : 0);       // this lane's key row of each eight
+        const int heads = a.n_kv * a.group, cols_used = a.n_rows * a.group, col0 = rg * kCols;
+        float* slot = slots + (size_t)warp * S::kSlotFloats;
+        float2* my_ml = slot_ml + warp * kCols;
+        int uses = 0;                                         // how often this warp has filled its slot
+        int seg = 0;
+        long long x = c0;
+        int b = find(c0);
+        bool given_up = false;
+        while (x < c1 && !given_up) {
+            while (x >= pre[b + 1]) ++b;
+            const int len = s_len[b], live = s_live[b];
+            const Span sp = span_of(len, live, a.window);
+            const unsigned within = (unsigned)(x - pre[b]);
+            const int h = (int)(within / (unsigned)sp.n), t0 = (int)(within % (unsigned)sp.n);
+            const int seg_len = (int)min(c1 - x, (long long)(sp.n - t0));
+            const int i_begin = (int)(x - c0), i_end = i_begin + seg_len;
+            const bool whole = seg_len == sp.n, at_start = x == c0;
+            int i = i_begin + ((team - i_begin) % T + T) % T;
+            x += seg_len;
+            ++seg;
+            if (i >= i_end) continue;
+            // Q, each row brought to f16's upper range by a power of two (exact but for elements 2^-39 of the row's
+            // largest); f turns accumulated scores into base-2 exponents
+            uint32_t qf[RT][8][2];
+            float f[RT][2], m[RT][2], l[RT][2];
+            float o[RT][8][4];
+#pragma unroll
+            for (int n = 0; n < RT; ++n) {
+                const int c = col0 + 8 * n + g;
+                uint4 raw[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) raw[e] = make_uint4(0u, 0u, 0u, 0u);
+                if (c < cols_used && c / a.group < live) {
+                    const uint4* src = reinterpret_cast<const uint4*>(
+                        a.q + (((size_t)b * a.n_rows + c / a.group) * heads + h * a.group + c % a.group) * kD + 16 * j);
+                    raw[0] = __ldg(src);
+                    raw[1] = __ldg(src + 1);
+                    raw[2] = __ldg(src + 8);
+                    raw[3] = __ldg(src + 9);
+                }
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+                uint32_t top = 0;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int up = min(max(268 - (int)(top >> 7), 1), 253);
+                const float by = __uint_as_float((uint32_t)up << 23);
+                const float back = __uint_as_float((uint32_t)(254 - up) << 23) * a.scale_log2;
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t v = w[2 * s + e];
+                        qf[n][s][e] = pack_f16(__uint_as_float(v << 16) * by, __uint_as_float(v & 0xFFFF0000u) * by);
+                    }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f[n][e] = __shfl_sync(0xffffffffu, back, (2 * j + e) * 4);
+                    m[n][e] = -INFINITY;
+                    l[n][e] = 0.0f;
+                }
+#pragma unroll
+                for (int d = 0; d < 8; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[n][d][e] = 0.0f;
+            }
+            float R = 0.0f, inv_r = 0.0f;
+            for (; i < i_end; i += T) {
+                const int st = i % NS;
+                if (!page_wait(flags + 1, i, full0 + 8 * st, (i / NS) & 1, abort, status)) {
+                    given_up = true;
+                    break;
+                }
+                if (flags[2 + st]) {
+                    const unsigned char* kt = ring + st * kTileBytes;
+                    const unsigned char* vt = kt + kHeadBytes;
+                    const float* sc = scales + 8 * st;
+                    const int key0 = (sp.first + t0 + (i - i_begin)) * kPage;
+                    // some row does not see all of the page's keys
+                    const bool edge = key0 + kPage - 1 > len - live || (a.window > 0 && key0 < len - a.window);
+                    float vs[kBlocks];
+#pragma unroll
+                    for (int k = 0; k < kBlocks; ++k) vs[k] = edge && key0 + kBlock * k >= len ? 0.0f : sc[kBlocks + k];
+                    const float vmax = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
+                    if (vmax > R) {
+                        const float up = __uint_as_float(min((__float_as_uint(vmax) + 0x7FFFFFu) & 0x7F800000u, 0x7F000000u));
+                        const float by = R / up;
+                        R = up;
+                        inv_r = 1.0f / up;
+#pragma unroll
+                        for (int n = 0; n < RT; ++n)
+#pragma unroll
+                            for (int d = 0; d < 8; ++d)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[n][d][e] *= by;
+                    }
+#pragma unroll
+                    for (int k0 = 0; k0 < kBlocks; k0 += KB) {
+                        float s[KB][RT][4];
+#pragma unroll
+                        for (int k = 0; k < KB; ++k) {
+#pragma unroll
+                            for (int n = 0; n < RT; ++n)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) s[k][n][e] = 0.0f;
+                            const unsigned char* row = kt + ((k0 + k) * kBlock + kperm) * kD;
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const int at = ((j + 4 * half) ^ kperm) * 16;
+                                const uint4 ra = *reinterpret_cast<const uint4*>(row + at);
+                                const uint4 rb = *reinterpret_cast<const uint4*>(row + 8 * kD + at);
+                                const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+                                for (int w = 0; w < 4; ++w) {
+                                    uint32_t a0, a1, a2, a3;
+                                    widen<kInt8>(wa[w], a0, a2);
+                                    widen<kInt8>(wb[w], a1, a3);
+#pragma unroll
+                                    for (int n = 0; n < RT; ++n)
+                                        mma_f16(s[k][n], a0, a1, a2, a3, qf[n][4 * half + w][0], qf[n][4 * half + w][1]);
+                                }
+                            }
+                        }
+                        // exponents, masks, the step's maxima
+                        float mx[RT][2];
+#pragma unroll
+                        for (int n = 0; n < RT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                mx[n][e] = -INFINITY;
+#pragma unroll
+                                for (int k = 0; k < KB; ++k) {
+                                    const float fk = f[n][e] * sc[k0 + k];
+                                    s[k][n][e] *= fk;
+                                    s[k][n][2 + e] *= fk;
+                                }
+                                if (edge) {
+                                    const int c = col0 + 8 * n + 2 * j + e;
+                                    const int p = len - live + min(c / a.group, live - 1);
+                                    const int lo = a.window > 0 ? p - a.window : -1;
+#pragma unroll
+                                    for (int k = 0; k < KB; ++k)
+#pragma unroll
+                                        for (int u = 0; u < 2; ++u) {
+                                            const int key = key0 + (k0 + k) * kBlock + kperm + 8 * u;
+                                            if (key > p || key <= lo) s[k][n][2 * u + e] = -INFINITY;
+                                        }
+                                }
+#pragma unroll
+                                for (int k = 0; k < KB; ++k) mx[n][e] = fmaxf(mx[n][e], fmaxf(s[k][n][e], s[k][n][2 + e]));
+                            }
+                        bool raise = false;
+#pragma unroll
+                        for (int n = 0; n < RT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], 4));
+                                mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], 8));
+                                mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], 16));
+                                raise = raise || mx[n][e] > m[n][e] + kLazy;
+                            }
+                        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                            for (int n = 0; n < RT; ++n)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float now = fmaxf(m[n][e], mx[n][e]);
+                                    const float by = m[n][e] == -INFINITY ? 0.0f : ptx::ex2(m[n][e] - now);
+                                    m[n][e] = now;
+                                    l[n][e] *= by;
+#pragma unroll
+                                    for (int d = 0; d < 8; ++d) {
+                                        o[n][d][e] *= by;
+                                        o[n][d][2 + e] *= by;
+                                    }
+                                }
+                        }
+                        // weights
+                        uint32_t pf[KB][RT][2];
+#pragma unroll
+                        for (int n = 0; n < RT; ++n) {
+                            const float z0 = (m[n][0] == -INFINITY ? 0.0f : m[n][0]) - kShift;
+                            const float z1 = (m[n][1] == -INFINITY ? 0.0f : m[n][1]) - kShift;
+#pragma unroll
+                            for (int k = 0; k < KB; ++k) {
+                                const float r = vs[k0 + k] * inv_r;
+                                const float p0 = ptx::ex2(s[k][n][0] - z0), p1 = ptx::ex2(s[k][n][1] - z1);
+                                const float p2 = ptx::ex2(s[k][n][2] - z0), p3 = ptx::ex2(s[k][n][3] - z1);
+                                l[n][0] += p0 + p2;
+                                l[n][1] += p1 + p3;
+                                pf[k][n][0] = transpose8(pack_f16(p0 * r, p1 * r));
+                                pf[k][n][1] = transpose8(pack_f16(p2 * r, p3 * r));
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < KB; ++k) {
+                            const int even = 2 * j, odd = (2 * j) ^ 5;
+                            const unsigned char* blk = vt + (k0 + k) * kBlock * kD;
+                            uint4 w0 = *reinterpret_cast<const uint4*>(blk + even * kD + (g ^ even) * 16);
+                            uint4 w1 = *reinterpret_cast<const uint4*>(blk + odd * kD + (g ^ odd) * 16);
+                            uint4 w2 = *reinterpret_cast<const uint4*>(blk + (even + 8) * kD + (g ^ even) * 16);
+                            uint4 w3 = *reinterpret_cast<const uint4*>(blk + (odd + 8) * kD + (g ^ odd) * 16);
+                            if (!kInt8 && edge) {      // what lies past the sequence may be NaN
+                                const int key = key0 + (k0 + k) * kBlock;
+                                const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+                                if (key + even >= len) w0 = none;
+                                if (key + odd >= len) w1 = none;
+                                if (key + even + 8 >= len) w2 = none;
+                                if (key + odd + 8 >= len) w3 = none;
+                            }
+                            const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
+                            const uint32_t u2[4] = {w2.x, w2.y, w2.z, w2.w}, u3[4] = {w3.x, w3.y, w3.z, w3.w};
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                uint32_t a0, a1, a2, a3;
+                                widen<kInt8>(__byte_perm(u0[w], u1[w], 0x5140), a0, a1);
+                                widen<kInt8>(__byte_perm(u2[w], u3[w], 0x5140), a2, a3);
+#pragma unroll
+                                for (int n = 0; n < RT; ++n)
+                                    mma_f16(o[n][2 * w], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
+                                widen<kInt8>(__byte_perm(u0[w], u1[w], 0x7362), a0, a1);
+                                widen<kInt8>(__byte_perm(u2[w], u3[w], 0x7362), a2, a3);
+#pragma unroll
+                                for (int n = 0; n < RT; ++n)
+                                    mma_f16(o[n][2 * w + 1], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(empty0 + 8 * st);
+            }
+            if (given_up) break;
+            // -------------------------------------------------------- the warp's sums into its slot
+            if (uses > 0 && !warp_wait(free0 + 8 * warp, (uses - 1) & 1, abort, status)) break;
+            ++uses;
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float sum = l[n][e];
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                    const int c = 8 * n + 2 * j + e;
+                    if (g == 0) my_ml[c] = make_float2(m[n][e] - kShift, sum);
+                    // dimensions 16 g .. 16 g + 15 of pair c: the lane's eight accumulator pairs in order
+                    float4* dst = reinterpret_cast<float4*>(slot + c * kD);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        dst[4 * g + (w ^ j)] = make_float4(o[n][2 * w][e] * R, o[n][2 * w][2 + e] * R, o[n][2 * w + 1][e] * R,
+                                                           o[n][2 * w + 1][2 + e] * R);
+                }
+            const int active = min(T, seg_len);
+            int last = 0;
+            __threadfence_block();
+            __syncwarp();
+            if (lane == 0) {
+                int* ticket = tickets + rg * kTickets + ((seg - 1) & (kTickets - 1));
+                last = atomicAdd(ticket, 1) == active - 1;
+                if (last) *ticket = 0;
+            }
+            last = __shfl_sync(0xffffffffu, last, 0);
+            if (!last) continue;
+            __threadfence_block();
+            __syncwarp();
+            // -------------------------------------------------------- the last warp of the segment joins them
+            const int first_team = i_begin % T;
+            for (int c = 0; c < kCols && col0 + c < cols_used; ++c) {
+                const int col = col0 + c, r = col / a.group;
+                if (r >= live) break;
+                float top = -INFINITY;
+                for (int t = 0; t < active; ++t)
+                    top = fmaxf(top, slot_ml[(((first_team + t) % T) * RG + rg) * kCols + c].x);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                float sum = 0.0f;
+                const int chunk = (lane & ~3) | ((lane & 3) ^ ((c >> 1) & 3));
+                for (int t = 0; t < active; ++t) {
+                    const int w = ((first_team + t) % T) * RG + rg;
+                    const float2 ml = slot_ml[w * kCols + c];
+                    const float by = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.0f) : exp2f(ml.x - top);
+                    const float4 v = reinterpret_cast<const float4*>(slots + (size_t)w * S::kSlotFloats + c * kD)[chunk];
+                    acc.x += by * v.x;
+                    acc.y += by * v.y;
+                    acc.z += by * v.z;
+                    acc.w += by * v.w;
+                    sum += by * ml.y;
+                }
+                if (whole) {
+                    const int head = h * a.group + col % a.group;
+                    const size_t row = ((size_t)b * a.n_rows + r) * heads + head;
+                    const float lse = finish(acc, top, sum, a.sink, head);
+                    store_row(a.out + row * kD + 4 * lane, acc);
+                    if (lane == 0 && a.out_lse) a.out_lse[row] = lse;
+                } else {
+                    const size_t at = (size_t)(2 * blockIdx.x + (at_start ? 0 : 1)) * kMaxCols + col;
+                    reinterpret_cast<float4*>(a.part_o + at * kD)[lane] = acc;
+                    if (lane == 0) a.part_ml[at] = make_float2(top, sum);
+                }
+            }
+            __syncwarp();
+            if (lane < active) ptx::mbar_arrive(free0 + 8 * (((first_team + lane) % T) * RG + rg));
+        }
+    }
+    if (status && a.dev_status) atomicOr(a.dev_status, status);
+}
+
+// Launch of one shape; rows: 8-pair tiles and warps a team that cover the call's pairs.
+template <bool kInt8, int RT, int RG>
+cudaError_t launch_shape(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+    const cudaError_t e = ensure_smem_attr((const void*)attn_paged_kernel<kInt8, RT, RG>, Shape<RT, RG>::kBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    pdl_config(&cfg, attr, dim3((unsigned)a.n_ctas), dim3(kAttnThreads), Shape<RT, RG>::kBytes, stream);
+    return cudaLaunchKernelEx(&cfg, attn_paged_kernel<kInt8, RT, RG>, a, k, v);
+}
+
+template <bool kInt8>
+cudaError_t launch_format(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+    const int cols = a.n_rows * a.group;
+    if (cols <= 8) return launch_shape<kInt8, 1, 1>(a, k, v, stream);
+    if (cols <= 16) return launch_shape<kInt8, 2, 1>(a, k, v, stream);
+    if (cols <= 24) return launch_shape<kInt8, 3, 1>(a, k, v, stream);
+    if (cols <= 32) return launch_shape<kInt8, 2, 2>(a, k, v, stream);
+    if (cols <= 48) return launch_shape<kInt8, 3, 2>(a, k, v, stream);
+    return launch_shape<kInt8, 2, 4>(a, k, v, stream);
+}
+
+cudaError_t launch_attn_e4m3(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream);
+cudaError_t launch_attn_int8(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream);
+
+}  // namespace paged
+}  // namespace va

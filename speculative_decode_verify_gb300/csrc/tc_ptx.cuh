@@ -84,6 +84,18 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// ----------------------------------------------------------------------------- register split
+// The whole warpgroup gives registers back, or takes some of those that others of its CTA gave back (it waits
+// for them, so the warpgroups' shares must fit into what the CTA was launched with).
+template <int kRegs>
+__device__ __forceinline__ void set_max_regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void set_max_regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // ----------------------------------------------------------------------------- programmatic dependent launch
 // Let the next kernel of the stream start launching; it still waits for this grid in its own
 // griddep_wait before touching memory.
@@ -138,6 +150,13 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
+}
+
+// Untiled load of `bytes` (a multiple of 16; both addresses 16-byte aligned) into shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* gaddr, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(gaddr)), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 // A 4-byte load that asks L2 to fetch the whole 256-byte block around it (LSU path, not the TMA

@@ -56,12 +56,14 @@ def ints(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
-def attention_bounds(out, lse, size, reach):
+def attention_bounds(out, lse, size, reach, top):
     """Largest error of an output and of a log-sum-exp.  Scores are sums of 128 products in fp32 with a few more
     roundings (at most 140 of 2^-24, relative to sum |q k| scale) and enter an exponential that is 2^-21 exact, in a
     total of fp32 sums; weights are rounded to 11 bits (2^-11 each) before the product with V, which is again
-    summed in fp32; the output is rounded once to bf16 (2^-8 relative)."""
+    summed in fp32; the output is rounded once to bf16 (2^-8 relative).  A weight below f16's normal range is rounded to
+    2^-25 of its unit; with the largest at 2^6 units or more and R at most twice the largest scale, n keys of codes up
+    to the top one are off by n 2^-25 2 (scale x top) / 2^6 = 2^-30 n (scale x top) in all."""
     score = (140 * 2.0 ** -24 * reach + 2.0 ** -20)
-    tol_out = 2.0 ** -8 * np.abs(out) + size * (2.0 ** -11 + 2 * score + 2.0 ** -16)[..., None] + 1e-30
+    tol_out = 2.0 ** -8 * np.abs(out) + size * (2.0 ** -11 + 2 * score + 2.0 ** -16)[..., None] + 2.0 ** -30 * np.asarray(top)[..., None]
     tol_lse = score + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0.0)) + 2.0 ** -18
     return tol_out, tol_lse

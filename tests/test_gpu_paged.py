@@ -287,6 +287,45 @@ def test_positions_and_pool_offsets_past_32_bits_of_bytes():
             want, size = w @ v[:n - 1 + r], w @ v[:n - 1 + r].abs()
             reach = SCALE * float((k.abs() @ q[0, r, h].double().abs()).max())
             tol, tol_lse = attention_bounds(want.cpu().numpy(), float(torch.logsumexp(z, 0)), size.cpu().numpy(),
-                                            np.array(reach))
+                                            np.array(reach), np.array(n * 127 * 0.02))
             assert np.all(np.abs(out[0, r, h].double().cpu().numpy() - want.cpu().numpy()) <= tol)
             assert abs(float(lse[0, r, h]) - float(torch.logsumexp(z, 0))) <= tol_lse
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("n,kv,group,rows", [(64 * 152 * 9, 1, 1, 1), (70001, 8, 1, 2), (100000, 1, 6, 3), (64 * 152 * 16, 1, 8, 4),
+                                             (196608, 1, 6, 8), (90000, 2, 7, 8), (64 * 152 * 8 + 1, 3, 4, 3)])
+def test_long_histories_in_which_a_cta_reuses_its_stages(fmt, n, kv, group, rows):
+    need = -(-n // 64)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    if fmt == "int8":
+        codes = [torch.randint(-127, 128, (need, kv, 64, D), generator=g, device="cuda", dtype=torch.int8) for _ in range(2)]
+        value, top = [c.double() for c in codes], 127.0
+    else:
+        f8 = [torch.randn(need, kv, 64, D, generator=g, device="cuda").mul_(80).clamp_(-448, 448).to(torch.float8_e4m3fn)
+              for _ in range(2)]
+        codes, value, top = f8, [c.double() for c in f8], 448.0
+    scale = [torch.rand(need, kv, 4, generator=g, device="cuda") * 2 / top for _ in range(2)]
+    k, v = ((c * s.double().repeat_interleave(16, 2)[..., None]).transpose(0, 1).reshape(kv, -1, D)
+            for c, s in zip(value, scale))
+    table = torch.randperm(need, generator=g, device="cuda").to(torch.int32)
+    codes = [torch.empty_like(c).view(torch.uint8).index_copy_(0, table.long(), c.view(torch.uint8)).view(c.dtype) for c in codes]
+    pool_scale = [torch.empty_like(s).index_copy_(0, table.long(), s) for s in scale]
+    q = torch.randn(1, rows, kv * group, D, generator=g, device="cuda").to(torch.bfloat16)
+    out, lse, status = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda"), ints([0])
+    ws = torch.zeros(va.va_paged_workspace_bytes(1, rows, kv, group), dtype=torch.uint8, device="cuda")
+    va.verify_attn_paged_b8(q, ints([rows]), ints([n]), table[None], *codes, *pool_scale, SCALE, None, ws, out, lse,
+                            dev_status=status)
+    assert int(status.item()) == 0
+    for r in range(rows):
+        p = n - rows + r + 1
+        x = q[0, r].double().view(kv, group, D)
+        z = SCALE * x @ k[:, :p].transpose(1, 2)
+        total = torch.logsumexp(z, -1)
+        w = torch.exp(z - total[..., None])
+        want, size = w @ v[:, :p], w @ v[:, :p].abs()
+        reach = SCALE * (x.abs() @ k[:, :p].abs().transpose(1, 2)).amax(-1)
+        tol, tol_lse = attention_bounds(*(t.cpu().numpy() for t in (want, total, size, reach)),
+                                        np.array(p * 2.0)[None, None])
+        assert np.all(np.abs(out[0, r].double().view(kv, group, D).cpu().numpy() - want.cpu().numpy()) <= tol)
+        assert np.all(np.abs(lse[0, r].double().view(kv, group).cpu().numpy() - total.cpu().numpy()) <= tol_lse)
