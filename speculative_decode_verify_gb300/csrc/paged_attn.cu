@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnPaged
         }
         const int head = h * a.group + col % a.group;
         const size_t row = ((size_t)b * a.n_rows + col / a.group) * heads + head;
-        const float lse = finish(acc, top, sum, a.sink, head);
-        store_row(a.out + row * kD + 4 * lane, acc);
-        if (lane == 0 && a.out_lse) a.out_lse[row] = lse;
+        const Finish f = finish(top, sum, a.sink, head);
+        store_row(a.out + row * kD + 4 * lane, make_float4(acc.x * f.by, acc.y * f.by, acc.z * f.by, acc.w * f.by));
+        if (lane == 0 && a.out_lse) a.out_lse[row] = f.lse;
     }
 }
 

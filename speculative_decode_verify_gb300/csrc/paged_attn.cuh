@@ -75,23 +75,20 @@ __device__ __forceinline__ Span span_of(int len, int live, int window) {
 // CTA c of n takes tiles [cta_begin(c), cta_begin(c + 1)) of `total`; n is at most total.
 __device__ __forceinline__ long long cta_begin(int c, int n, long long total) { return (long long)c * total / n; }
 
-// One output row: the sum over pieces weighted to a common maximum, with the sink, rounded once.
-// o: unnormalised sum, (m, l): reference exponent and sum of 2^(t - m); returns the log-sum-exp.
-__device__ __forceinline__ float finish(float4& o, float m, float l, const float* sink, int head) {
-    const float s2 = sink ? sink[head] * 1.4426950408889634f : -INFINITY;
+// What an unnormalised output row sum 2^(t - m) v is multiplied by, and its log-sum-exp: l is the sum of 2^(t - m),
+// the sink joins the denominator.
+struct Finish {
+    float by, lse;
+};
+__device__ __forceinline__ Finish finish(float m, float l, const float* sink, int head) {
+    Finish f;
+    const float s2 = sink ? __ldg(sink + head) * 1.4426950408889634f : -INFINITY;
     const float seen = l == 0.0f ? -INFINITY : m + log2f(l);
     const float top = fmaxf(seen, s2);
-    if (top == -INFINITY && !(l != l)) {
-        o = make_float4(0.f, 0.f, 0.f, 0.f);
-        return -INFINITY;
-    }
-    const float all = top + log2f(exp2f(seen - top) + exp2f(s2 - top));
-    const float f = l == 0.0f ? 0.0f : exp2f(seen - all) / l;
-    o.x *= f;
-    o.y *= f;
-    o.z *= f;
-    o.w *= f;
-    return (l != l ? l : all) * 0.6931471805599453f;
+    const float all = top == -INFINITY ? -INFINITY : top + log2f(exp2f(seen - top) + exp2f(s2 - top));
+    f.by = l == 0.0f ? 0.0f : (l != l ? l : exp2f(seen - all) / l);
+    f.lse = (l != l ? l : all) * 0.6931471805599453f;
+    return f;
 }
 
 __device__ __forceinline__ void store_row(uint16_t* dst, const float4& o) {
@@ -116,22 +113,33 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Four codes c0..c3 of a word to f16 pairs (c0, c1) and (c2, c3).
+// Codes to f16 pairs, in the integer pipe (cvt.rn.f16x2.e4m3x2 took 8.6 cycles an SM per warp: 1.15 us a tile).
+//   INT8: 0x64xx is 1024 + xx as f16; the biased code (+128) becomes the low byte, and 1152 comes off again.
+//   E4M3: the exponent and mantissa bits, shifted to their places in f16, are the code's value times 2^-8
+//         (subnormals included); that factor is put back in fp32, kUnit below.
+// Of a word c0..c3: INT8 gives (c0, c1), (c2, c3); E4M3 gives (c0, c2), (c1, c3).
 template <bool kInt8>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& x, uint32_t& y) {
     if (kInt8) {
-        // 0x64xx is 1024 + xx: the biased code (+128) becomes the low byte, 1152 comes off again
         const uint32_t u = w ^ 0x80808080u;
         const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
         uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-        const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias), y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
-        lo = *reinterpret_cast<const uint32_t*>(&x);
-        hi = *reinterpret_cast<const uint32_t*>(&y);
+        const __half2 lo = __hsub2(*reinterpret_cast<__half2*>(&a), bias), hi = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+        x = *reinterpret_cast<const uint32_t*>(&lo);
+        y = *reinterpret_cast<const uint32_t*>(&hi);
     } else {
-        asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-            : "=r"(lo), "=r"(hi) : "r"(w));
+        x = ((w << 7) & 0x3F803F80u) | ((w << 8) & 0x80008000u);
+        y = ((w >> 1) & 0x3F803F80u) | (w & 0x80008000u);
     }
 }
+// The same dimension of two keys side by side: words a (one key) and b (the other), dimensions i and i + 1, in the
+// order that widen() takes apart into (a_i, b_i), (a_i+1, b_i+1).
+template <bool kInt8, int kHalf>
+__device__ __forceinline__ uint32_t pair_up(uint32_t a, uint32_t b) {
+    return __byte_perm(a, b, kInt8 ? (kHalf ? 0x7362 : 0x5140) : (kHalf ? 0x7632 : 0x5410));
+}
+template <bool kInt8>
+constexpr float kUnit = kInt8 ? 1.0f : 256.0f;
 
 // A wait that the warp makes as one: every lane leaves it with the same answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int& status) {
@@ -166,7 +174,7 @@ __device__ __forceinline__ bool page_wait(volatile int* issued, int i, uint32_t 
 // RT: 8-pair tiles per warp; RG: warps of a team; kTeams teams; kStages: pages in flight.
 template <int RT, int RG>
 struct Shape {
-    static constexpr int kTeams = kConsumers / RG;
+    static constexpr int kTeams = kConsumers / RG;                       // a power of two, at most 8
     static constexpr int kCols = 8 * RT;                                 // pairs of a warp
     static constexpr int kSlotFloats = kCols * kD;
     static constexpr int kRingAt = 0;
@@ -315,7 +323,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             ptx::mbar_arrive(bar);
                         }
                         issued = i + 1;
-                        __threadfence_block();
+                        // (no fence: what the reader must not miss, the end of the stage's last use, came before
+                        // this lane's wait for the stage, and shared memory has one order)
                         *(volatile int*)(flags + 1) = issued;
                     }
                 }
@@ -337,22 +346,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         float* slot = slots + (size_t)warp * S::kSlotFloats;
         float2* my_ml = slot_ml + warp * kCols;
         int uses = 0;                                         // how often this warp has filled its slot
-        int seg = 0;
-        long long x = c0;
-        int b = find(c0);
+        const int n_tiles = (int)(c1 - c0);
+        int b_next = find(c0), h_next, t_next;                // where the next segment begins
+        {
+            const unsigned within = (unsigned)(c0 - pre[b_next]), n = (unsigned)span_of(s_len[b_next], s_live[b_next], a.window).n;
+            h_next = (int)(within / n);
+            t_next = (int)(within % n);
+        }
         bool given_up = false;
-        while (x < c1 && !given_up) {
-            while (x >= pre[b + 1]) ++b;
+        for (int i_end = 0, seg = 0; i_end < n_tiles && !given_up; ++seg) {
+            const int b = b_next, h = h_next, t0 = t_next, i_begin = i_end;
             const int len = s_len[b], live = s_live[b];
             const Span sp = span_of(len, live, a.window);
-            const unsigned within = (unsigned)(x - pre[b]);
-            const int h = (int)(within / (unsigned)sp.n), t0 = (int)(within % (unsigned)sp.n);
-            const int seg_len = (int)min(c1 - x, (long long)(sp.n - t0));
-            const int i_begin = (int)(x - c0), i_end = i_begin + seg_len;
-            const bool whole = seg_len == sp.n, at_start = x == c0;
-            int i = i_begin + ((team - i_begin) % T + T) % T;
-            x += seg_len;
-            ++seg;
+            const int seg_len = min(n_tiles - i_begin, sp.n - t0);
+            const bool whole = seg_len == sp.n;
+            i_end += seg_len;
+            t_next = 0;
+            if (++h_next == a.n_kv) {
+                h_next = 0;
+                do ++b_next;
+                while (b_next < a.n_seqs && pre[b_next + 1] == pre[b_next]);
+            }
+            int i = i_begin + ((team - i_begin) & (T - 1));
             if (i >= i_end) continue;
             // Q, each row brought to f16's upper range by a power of two (exact but for elements 2^-39 of the row's
             // largest); f turns accumulated scores into base-2 exponents
@@ -381,14 +396,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const int up = min(max(268 - (int)(top >> 7), 1), 253);
                 const float by = __uint_as_float((uint32_t)up << 23);
-                const float back = __uint_as_float((uint32_t)(254 - up) << 23) * a.scale_log2;
+                const float back = __uint_as_float((uint32_t)(254 - up) << 23) * (a.scale_log2 * kUnit<kInt8>);
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t v = w[2 * s + e];
-                        qf[n][s][e] = pack_f16(__uint_as_float(v << 16) * by, __uint_as_float(v & 0xFFFF0000u) * by);
-                    }
+                for (int s = 0; s < 8; ++s) {   // four dimensions, paired as widen() pairs codes
+                    const uint32_t v0 = w[2 * s], v1 = w[2 * s + 1];
+                    const float x0 = __uint_as_float(v0 << 16) * by, x1 = __uint_as_float(v0 & 0xFFFF0000u) * by;
+                    const float x2 = __uint_as_float(v1 << 16) * by, x3 = __uint_as_float(v1 & 0xFFFF0000u) * by;
+                    qf[n][s][0] = kInt8 ? pack_f16(x0, x1) : pack_f16(x0, x2);
+                    qf[n][s][1] = kInt8 ? pack_f16(x2, x3) : pack_f16(x1, x3);
+                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     f[n][e] = __shfl_sync(0xffffffffu, back, (2 * j + e) * 4);
@@ -532,30 +548,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         for (int k = 0; k < KB; ++k) {
                             const int even = 2 * j, odd = (2 * j) ^ 5;
                             const unsigned char* blk = vt + (k0 + k) * kBlock * kD;
-                            uint4 w0 = *reinterpret_cast<const uint4*>(blk + even * kD + (g ^ even) * 16);
-                            uint4 w1 = *reinterpret_cast<const uint4*>(blk + odd * kD + (g ^ odd) * 16);
-                            uint4 w2 = *reinterpret_cast<const uint4*>(blk + (even + 8) * kD + (g ^ even) * 16);
-                            uint4 w3 = *reinterpret_cast<const uint4*>(blk + (odd + 8) * kD + (g ^ odd) * 16);
-                            if (!kInt8 && edge) {      // what lies past the sequence may be NaN
-                                const int key = key0 + (k0 + k) * kBlock;
-                                const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-                                if (key + even >= len) w0 = none;
-                                if (key + odd >= len) w1 = none;
-                                if (key + even + 8 >= len) w2 = none;
-                                if (key + odd + 8 >= len) w3 = none;
-                            }
+                            const uint4 w0 = *reinterpret_cast<const uint4*>(blk + even * kD + (g ^ even) * 16);
+                            const uint4 w1 = *reinterpret_cast<const uint4*>(blk + odd * kD + (g ^ odd) * 16);
+                            const uint4 w2 = *reinterpret_cast<const uint4*>(blk + (even + 8) * kD + (g ^ even) * 16);
+                            const uint4 w3 = *reinterpret_cast<const uint4*>(blk + (odd + 8) * kD + (g ^ odd) * 16);
                             const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
                             const uint32_t u2[4] = {w2.x, w2.y, w2.z, w2.w}, u3[4] = {w3.x, w3.y, w3.z, w3.w};
 #pragma unroll
                             for (int w = 0; w < 4; ++w) {
                                 uint32_t a0, a1, a2, a3;
-                                widen<kInt8>(__byte_perm(u0[w], u1[w], 0x5140), a0, a1);
-                                widen<kInt8>(__byte_perm(u2[w], u3[w], 0x5140), a2, a3);
+                                widen<kInt8>(pair_up<kInt8, 0>(u0[w], u1[w]), a0, a1);
+                                widen<kInt8>(pair_up<kInt8, 0>(u2[w], u3[w]), a2, a3);
 #pragma unroll
                                 for (int n = 0; n < RT; ++n)
                                     mma_f16(o[n][2 * w], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
-                                widen<kInt8>(__byte_perm(u0[w], u1[w], 0x7362), a0, a1);
-                                widen<kInt8>(__byte_perm(u2[w], u3[w], 0x7362), a2, a3);
+                                widen<kInt8>(pair_up<kInt8, 1>(u0[w], u1[w]), a0, a1);
+                                widen<kInt8>(pair_up<kInt8, 1>(u2[w], u3[w]), a2, a3);
 #pragma unroll
                                 for (int n = 0; n < RT; ++n)
                                     mma_f16(o[n][2 * w + 1], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
@@ -567,7 +575,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(empty0 + 8 * st);
             }
             if (given_up) break;
-            // -------------------------------------------------------- the warp's sums into its slot
+            // -------------------------------------------------------- sums of the segment
+            // where row c of this warp goes: the output if the segment is the whole head, else this CTA's part
+            auto emit = [&](int c, const float4& u) {
+                const int col = col0 + c, r = col / a.group;
+                if (whole) {
+                    const size_t row = ((size_t)b * a.n_rows + r) * heads + h * a.group + col % a.group;
+                    store_row(a.out + row * kD + 4 * lane, u);
+                } else {
+                    const size_t at = (size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + col;
+                    reinterpret_cast<float4*>(a.part_o + at * kD)[lane] = u;
+                }
+            };
+            // the same for its reference and sum; returns what the row is multiplied by
+            auto emit_ml = [&](int c, float top, float sum) {
+                const int col = col0 + c, r = col / a.group;
+                if (r >= live) return 0.0f;
+                if (!whole) {
+                    a.part_ml[(size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + col] = make_float2(top, sum);
+                    return 1.0f;
+                }
+                const int head = h * a.group + col % a.group;
+                const Finish f = finish(top, sum, a.sink, head);
+                if (a.out_lse) a.out_lse[((size_t)b * a.n_rows + r) * heads + head] = f.lse;
+                return f.by;
+            };
+            const int active = min(T, seg_len), n_cols = min(kCols, live * a.group - col0);
             if (uses > 0 && !warp_wait(free0 + 8 * warp, (uses - 1) & 1, abort, status)) break;
             ++uses;
 #pragma unroll
@@ -582,60 +615,69 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (g == 0) my_ml[c] = make_float2(m[n][e] - kShift, sum);
                     // dimensions 16 g .. 16 g + 15 of pair c: the lane's eight accumulator pairs in order
                     float4* dst = reinterpret_cast<float4*>(slot + c * kD);
+                    const float by = R * kUnit<kInt8>;
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
-                        dst[4 * g + (w ^ j)] = make_float4(o[n][2 * w][e] * R, o[n][2 * w][2 + e] * R, o[n][2 * w + 1][e] * R,
-                                                           o[n][2 * w + 1][2 + e] * R);
+                        dst[4 * g + (w ^ j)] = make_float4(o[n][2 * w][e] * by, o[n][2 * w][2 + e] * by,
+                                                           o[n][2 * w + 1][e] * by, o[n][2 * w + 1][2 + e] * by);
                 }
-            const int active = min(T, seg_len);
-            int last = 0;
+            int last = 1;
             __threadfence_block();
             __syncwarp();
-            if (lane == 0) {
-                int* ticket = tickets + rg * kTickets + ((seg - 1) & (kTickets - 1));
-                last = atomicAdd(ticket, 1) == active - 1;
-                if (last) *ticket = 0;
+            if (active > 1) {
+                if (lane == 0) {
+                    int* ticket = tickets + rg * kTickets + (seg & (kTickets - 1));
+                    last = atomicAdd(ticket, 1) == active - 1;
+                    if (last) *ticket = 0;
+                }
+                last = __shfl_sync(0xffffffffu, last, 0);
+                if (!last) continue;
+                __threadfence_block();
+                __syncwarp();
             }
-            last = __shfl_sync(0xffffffffu, last, 0);
-            if (!last) continue;
-            __threadfence_block();
-            __syncwarp();
             // -------------------------------------------------------- the last warp of the segment joins them
-            const int first_team = i_begin % T;
-            for (int c = 0; c < kCols && col0 + c < cols_used; ++c) {
-                const int col = col0 + c, r = col / a.group;
-                if (r >= live) break;
-                float top = -INFINITY;
-                for (int t = 0; t < active; ++t)
-                    top = fmaxf(top, slot_ml[(((first_team + t) % T) * RG + rg) * kCols + c].x);
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                float sum = 0.0f;
+            // weights: eight lanes a pair, one for each active team, in the teams' order of tiles
+            const int first_team = i_begin & (T - 1);
+            const int t_mine = lane & 7, w_mine = ((first_team + t_mine) & (T - 1)) * RG + rg;
+            float by[kCols / 4];
+#pragma unroll
+            for (int k = 0; k < kCols / 4; ++k) {
+                const int c = 4 * k + (lane >> 3);
+                float2 ml = make_float2(-INFINITY, 0.0f);
+                if (t_mine < active) ml = slot_ml[w_mine * kCols + c];
+                float top = ml.x;
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                by[k] = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.0f) : exp2f(ml.x - top);
+                float sum = by[k] * ml.y;
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                float all = 0.0f;
+                if (t_mine == 0 && c < n_cols) all = emit_ml(c, top, sum);
+                by[k] *= __shfl_sync(0xffffffffu, all, lane & 24);
+            }
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                if (c >= n_cols) break;
                 const int chunk = (lane & ~3) | ((lane & 3) ^ ((c >> 1) & 3));
-                for (int t = 0; t < active; ++t) {
-                    const int w = ((first_team + t) % T) * RG + rg;
-                    const float2 ml = slot_ml[w * kCols + c];
-                    const float by = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.0f) : exp2f(ml.x - top);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    if (t >= active) break;
+                    const int w = ((first_team + t) & (T - 1)) * RG + rg;
+                    const float f = __shfl_sync(0xffffffffu, by[c / 4], (c & 3) * 8 + t);
                     const float4 v = reinterpret_cast<const float4*>(slots + (size_t)w * S::kSlotFloats + c * kD)[chunk];
-                    acc.x += by * v.x;
-                    acc.y += by * v.y;
-                    acc.z += by * v.z;
-                    acc.w += by * v.w;
-                    sum += by * ml.y;
+                    acc.x += f * v.x;
+                    acc.y += f * v.y;
+                    acc.z += f * v.z;
+                    acc.w += f * v.w;
                 }
-                if (whole) {
-                    const int head = h * a.group + col % a.group;
-                    const size_t row = ((size_t)b * a.n_rows + r) * heads + head;
-                    const float lse = finish(acc, top, sum, a.sink, head);
-                    store_row(a.out + row * kD + 4 * lane, acc);
-                    if (lane == 0 && a.out_lse) a.out_lse[row] = lse;
-                } else {
-                    const size_t at = (size_t)(2 * blockIdx.x + (at_start ? 0 : 1)) * kMaxCols + col;
-                    reinterpret_cast<float4*>(a.part_o + at * kD)[lane] = acc;
-                    if (lane == 0) a.part_ml[at] = make_float2(top, sum);
-                }
+                emit(c, acc);
             }
             __syncwarp();
-            if (lane < active) ptx::mbar_arrive(free0 + 8 * (((first_team + lane) % T) * RG + rg));
+            if (lane < active) ptx::mbar_arrive(free0 + 8 * (((first_team + lane) & (T - 1)) * RG + rg));
         }
     }
     if (status && a.dev_status) atomicOr(a.dev_status, status);
