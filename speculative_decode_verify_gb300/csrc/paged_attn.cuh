@@ -178,7 +178,7 @@ struct Shape {
     static constexpr int kCols = 8 * RT;                                 // pairs of a warp
     static constexpr int kSlotFloats = kCols * kD;
     static constexpr int kRingAt = 0;
-    static constexpr int kFixed = kConsumers * (kSlotFloats + 2 * kCols) * 4   // the warps' slots and their (m, l)
+    static constexpr int kFixed = kConsumers * (kSlotFloats + 10 * kCols) * 4  // the warps' slots, (m, l) and weights
                                   + (VA_PAGED_MAX_SEQS + 1) * 8 + VA_PAGED_MAX_SEQS * 5   // prefix, lengths, live rows
                                   + 2048;                                      // barriers, tickets, scales, alignment
     static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kTileBytes + 32);
@@ -193,13 +193,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                       const __grid_constant__ CUtensorMap map_v) {
     using S = Shape<RT, RG>;
     constexpr int NS = S::kStages, T = S::kTeams, kCols = S::kCols;
-    constexpr int KB = RT >= 3 ? 2 : 4;       // 16-key blocks per softmax step (registers)
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* ring = base;
     float* slots = reinterpret_cast<float*>(ring + NS * kTileBytes);
     float2* slot_ml = reinterpret_cast<float2*>(slots + kConsumers * S::kSlotFloats);
-    long long* pre = reinterpret_cast<long long*>(slot_ml + kConsumers * kCols);
+    float* weights = reinterpret_cast<float*>(slot_ml + kConsumers * kCols);
+    long long* pre = reinterpret_cast<long long*>(weights + kConsumers * kCols * 8);
     int* s_len = reinterpret_cast<int*>(pre + VA_PAGED_MAX_SEQS + 1);
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_len + VA_PAGED_MAX_SEQS + 2);
     float* scales = reinterpret_cast<float*>(bars + 48);
@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // largest); f turns accumulated scores into base-2 exponents
             uint32_t qf[RT][8][2];
             float f[RT][2], m[RT][2], l[RT][2];
+            int p[RT][2];                                     // positions of the columns' rows
             float o[RT][8][4];
 #pragma unroll
             for (int n = 0; n < RT; ++n) {
@@ -410,6 +411,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     f[n][e] = __shfl_sync(0xffffffffu, back, (2 * j + e) * 4);
                     m[n][e] = -INFINITY;
                     l[n][e] = 0.0f;
+                    p[n][e] = len - live + min((col0 + 8 * n + 2 * j + e) / a.group, live - 1);
                 }
 #pragma unroll
                 for (int d = 0; d < 8; ++d)
@@ -430,10 +432,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int key0 = (sp.first + t0 + (i - i_begin)) * kPage;
                     // some row does not see all of the page's keys
                     const bool edge = key0 + kPage - 1 > len - live || (a.window > 0 && key0 < len - a.window);
-                    float vs[kBlocks];
-#pragma unroll
-                    for (int k = 0; k < kBlocks; ++k) vs[k] = edge && key0 + kBlock * k >= len ? 0.0f : sc[kBlocks + k];
-                    const float vmax = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
+                    // the blocks that some row sees
+                    const int k_end = edge ? min(kBlocks, (len - key0 + kBlock - 1) / kBlock) : kBlocks;
+                    const int k_begin = edge && a.window > 0 ? max(0, len - live - a.window + 1 - key0) / kBlock : 0;
+                    float vmax = 0.0f;
+                    for (int k = k_begin; k < k_end; ++k) vmax = fmaxf(vmax, sc[kBlocks + k]);
                     if (vmax > R) {
                         const float up = __uint_as_float(min((__float_as_uint(vmax) + 0x7FFFFFu) & 0x7F800000u, 0x7F000000u));
                         const float by = R / up;
@@ -446,77 +449,73 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) o[n][d][e] *= by;
                     }
+#pragma unroll 1
+                    for (int k = k_begin; k < k_end; ++k) {
+                        // scores of 16 keys, the head dimension in two halves (two shorter chains)
+                        float s[2][RT][4];
 #pragma unroll
-                    for (int k0 = 0; k0 < kBlocks; k0 += KB) {
-                        float s[KB][RT][4];
-#pragma unroll
-                        for (int k = 0; k < KB; ++k) {
+                        for (int u = 0; u < 2; ++u)
 #pragma unroll
                             for (int n = 0; n < RT; ++n)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) s[k][n][e] = 0.0f;
-                            const unsigned char* row = kt + ((k0 + k) * kBlock + kperm) * kD;
+                                for (int e = 0; e < 4; ++e) s[u][n][e] = 0.0f;
+                        const unsigned char* row = kt + (k * kBlock + kperm) * kD;
+                        uint4 ra[2], rb[2];
 #pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const int at = ((j + 4 * half) ^ kperm) * 16;
-                                const uint4 ra = *reinterpret_cast<const uint4*>(row + at);
-                                const uint4 rb = *reinterpret_cast<const uint4*>(row + 8 * kD + at);
-                                const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-#pragma unroll
-                                for (int w = 0; w < 4; ++w) {
-                                    uint32_t a0, a1, a2, a3;
-                                    widen<kInt8>(wa[w], a0, a2);
-                                    widen<kInt8>(wb[w], a1, a3);
-#pragma unroll
-                                    for (int n = 0; n < RT; ++n)
-                                        mma_f16(s[k][n], a0, a1, a2, a3, qf[n][4 * half + w][0], qf[n][4 * half + w][1]);
-                                }
-                            }
+                        for (int u = 0; u < 2; ++u) {
+                            const int at = ((j + 4 * u) ^ kperm) * 16;
+                            ra[u] = *reinterpret_cast<const uint4*>(row + at);
+                            rb[u] = *reinterpret_cast<const uint4*>(row + 8 * kD + at);
                         }
-                        // exponents, masks, the step's maxima
-                        float mx[RT][2];
 #pragma unroll
-                        for (int n = 0; n < RT; ++n)
+                        for (int w = 0; w < 4; ++w)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                mx[n][e] = -INFINITY;
+                            for (int u = 0; u < 2; ++u) {
+                                const uint32_t wa[4] = {ra[u].x, ra[u].y, ra[u].z, ra[u].w};
+                                const uint32_t wb[4] = {rb[u].x, rb[u].y, rb[u].z, rb[u].w};
+                                uint32_t a0, a1, a2, a3;
+                                widen<kInt8>(wa[w], a0, a2);
+                                widen<kInt8>(wb[w], a1, a3);
 #pragma unroll
-                                for (int k = 0; k < KB; ++k) {
-                                    const float fk = f[n][e] * sc[k0 + k];
-                                    s[k][n][e] *= fk;
-                                    s[k][n][2 + e] *= fk;
-                                }
-                                if (edge) {
-                                    const int c = col0 + 8 * n + 2 * j + e;
-                                    const int p = len - live + min(c / a.group, live - 1);
-                                    const int lo = a.window > 0 ? p - a.window : -1;
-#pragma unroll
-                                    for (int k = 0; k < KB; ++k)
-#pragma unroll
-                                        for (int u = 0; u < 2; ++u) {
-                                            const int key = key0 + (k0 + k) * kBlock + kperm + 8 * u;
-                                            if (key > p || key <= lo) s[k][n][2 * u + e] = -INFINITY;
-                                        }
-                                }
-#pragma unroll
-                                for (int k = 0; k < KB; ++k) mx[n][e] = fmaxf(mx[n][e], fmaxf(s[k][n][e], s[k][n][2 + e]));
+                                for (int n = 0; n < RT; ++n)
+                                    mma_f16(s[u][n], a0, a1, a2, a3, qf[n][4 * u + w][0], qf[n][4 * u + w][1]);
                             }
+                        // V, while the scores are on their way
+                        const int even = 2 * j, odd = (2 * j) ^ 5;
+                        const unsigned char* blk = vt + k * kBlock * kD;
+                        const uint4 w0 = *reinterpret_cast<const uint4*>(blk + even * kD + (g ^ even) * 16);
+                        const uint4 w1 = *reinterpret_cast<const uint4*>(blk + odd * kD + (g ^ odd) * 16);
+                        const uint4 w2 = *reinterpret_cast<const uint4*>(blk + (even + 8) * kD + (g ^ even) * 16);
+                        const uint4 w3 = *reinterpret_cast<const uint4*>(blk + (odd + 8) * kD + (g ^ odd) * 16);
+                        // exponents and masks; is some score over its column's reference by more than kLazy?
+                        const float ks = sc[k];
                         bool raise = false;
 #pragma unroll
                         for (int n = 0; n < RT; ++n)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], 4));
-                                mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], 8));
-                                mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], 16));
-                                raise = raise || mx[n][e] > m[n][e] + kLazy;
+                                const float fk = f[n][e] * ks;
+                                float x0 = (s[0][n][e] + s[1][n][e]) * fk, x1 = (s[0][n][2 + e] + s[1][n][2 + e]) * fk;
+                                if (edge) {
+                                    const int key = key0 + k * kBlock + kperm;
+                                    const int lo = a.window > 0 ? p[n][e] - a.window : -1;
+                                    if (key > p[n][e] || key <= lo) x0 = -INFINITY;
+                                    if (key + 8 > p[n][e] || key + 8 <= lo) x1 = -INFINITY;
+                                }
+                                s[0][n][e] = x0;
+                                s[0][n][2 + e] = x1;
+                                raise = raise || fmaxf(x0, x1) - m[n][e] > kLazy;
                             }
                         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                             for (int n = 0; n < RT; ++n)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    const float now = fmaxf(m[n][e], mx[n][e]);
+                                    float now = fmaxf(s[0][n][e], s[0][n][2 + e]);
+                                    now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 4));
+                                    now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 8));
+                                    now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 16));
+                                    now = fmaxf(now, m[n][e]);
                                     const float by = m[n][e] == -INFINITY ? 0.0f : ptx::ex2(m[n][e] - now);
                                     m[n][e] = now;
                                     l[n][e] *= by;
@@ -528,46 +527,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 }
                         }
                         // weights
-                        uint32_t pf[KB][RT][2];
+                        const float r = sc[kBlocks + k] * inv_r;
+                        uint32_t pf[RT][2];
 #pragma unroll
                         for (int n = 0; n < RT; ++n) {
                             const float z0 = (m[n][0] == -INFINITY ? 0.0f : m[n][0]) - kShift;
                             const float z1 = (m[n][1] == -INFINITY ? 0.0f : m[n][1]) - kShift;
-#pragma unroll
-                            for (int k = 0; k < KB; ++k) {
-                                const float r = vs[k0 + k] * inv_r;
-                                const float p0 = ptx::ex2(s[k][n][0] - z0), p1 = ptx::ex2(s[k][n][1] - z1);
-                                const float p2 = ptx::ex2(s[k][n][2] - z0), p3 = ptx::ex2(s[k][n][3] - z1);
-                                l[n][0] += p0 + p2;
-                                l[n][1] += p1 + p3;
-                                pf[k][n][0] = transpose8(pack_f16(p0 * r, p1 * r));
-                                pf[k][n][1] = transpose8(pack_f16(p2 * r, p3 * r));
-                            }
+                            const float p0 = ptx::ex2(s[0][n][0] - z0), p1 = ptx::ex2(s[0][n][1] - z1);
+                            const float p2 = ptx::ex2(s[0][n][2] - z0), p3 = ptx::ex2(s[0][n][3] - z1);
+                            l[n][0] += p0 + p2;
+                            l[n][1] += p1 + p3;
+                            pf[n][0] = transpose8(pack_f16(p0 * r, p1 * r));
+                            pf[n][1] = transpose8(pack_f16(p2 * r, p3 * r));
                         }
+                        const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
+                        const uint32_t u2[4] = {w2.x, w2.y, w2.z, w2.w}, u3[4] = {w3.x, w3.y, w3.z, w3.w};
 #pragma unroll
-                        for (int k = 0; k < KB; ++k) {
-                            const int even = 2 * j, odd = (2 * j) ^ 5;
-                            const unsigned char* blk = vt + (k0 + k) * kBlock * kD;
-                            const uint4 w0 = *reinterpret_cast<const uint4*>(blk + even * kD + (g ^ even) * 16);
-                            const uint4 w1 = *reinterpret_cast<const uint4*>(blk + odd * kD + (g ^ odd) * 16);
-                            const uint4 w2 = *reinterpret_cast<const uint4*>(blk + (even + 8) * kD + (g ^ even) * 16);
-                            const uint4 w3 = *reinterpret_cast<const uint4*>(blk + (odd + 8) * kD + (g ^ odd) * 16);
-                            const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
-                            const uint32_t u2[4] = {w2.x, w2.y, w2.z, w2.w}, u3[4] = {w3.x, w3.y, w3.z, w3.w};
+                        for (int w = 0; w < 4; ++w) {
+                            uint32_t a0, a1, a2, a3;
+                            widen<kInt8>(pair_up<kInt8, 0>(u0[w], u1[w]), a0, a1);
+                            widen<kInt8>(pair_up<kInt8, 0>(u2[w], u3[w]), a2, a3);
 #pragma unroll
-                            for (int w = 0; w < 4; ++w) {
-                                uint32_t a0, a1, a2, a3;
-                                widen<kInt8>(pair_up<kInt8, 0>(u0[w], u1[w]), a0, a1);
-                                widen<kInt8>(pair_up<kInt8, 0>(u2[w], u3[w]), a2, a3);
+                            for (int n = 0; n < RT; ++n) mma_f16(o[n][2 * w], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                            widen<kInt8>(pair_up<kInt8, 1>(u0[w], u1[w]), a0, a1);
+                            widen<kInt8>(pair_up<kInt8, 1>(u2[w], u3[w]), a2, a3);
 #pragma unroll
-                                for (int n = 0; n < RT; ++n)
-                                    mma_f16(o[n][2 * w], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
-                                widen<kInt8>(pair_up<kInt8, 1>(u0[w], u1[w]), a0, a1);
-                                widen<kInt8>(pair_up<kInt8, 1>(u2[w], u3[w]), a2, a3);
-#pragma unroll
-                                for (int n = 0; n < RT; ++n)
-                                    mma_f16(o[n][2 * w + 1], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
-                            }
+                            for (int n = 0; n < RT; ++n) mma_f16(o[n][2 * w + 1], a0, a1, a2, a3, pf[n][0], pf[n][1]);
                         }
                     }
                 }
@@ -576,30 +561,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             if (given_up) break;
             // -------------------------------------------------------- sums of the segment
-            // where row c of this warp goes: the output if the segment is the whole head, else this CTA's part
-            auto emit = [&](int c, const float4& u) {
-                const int col = col0 + c, r = col / a.group;
-                if (whole) {
-                    const size_t row = ((size_t)b * a.n_rows + r) * heads + h * a.group + col % a.group;
-                    store_row(a.out + row * kD + 4 * lane, u);
-                } else {
-                    const size_t at = (size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + col;
-                    reinterpret_cast<float4*>(a.part_o + at * kD)[lane] = u;
-                }
-            };
-            // the same for its reference and sum; returns what the row is multiplied by
-            auto emit_ml = [&](int c, float top, float sum) {
-                const int col = col0 + c, r = col / a.group;
-                if (r >= live) return 0.0f;
-                if (!whole) {
-                    a.part_ml[(size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + col] = make_float2(top, sum);
-                    return 1.0f;
-                }
-                const int head = h * a.group + col % a.group;
-                const Finish f = finish(top, sum, a.sink, head);
-                if (a.out_lse) a.out_lse[((size_t)b * a.n_rows + r) * heads + head] = f.lse;
-                return f.by;
-            };
             const int active = min(T, seg_len), n_cols = min(kCols, live * a.group - col0);
             if (uses > 0 && !warp_wait(free0 + 8 * warp, (uses - 1) & 1, abort, status)) break;
             ++uses;
@@ -636,45 +597,58 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 __syncwarp();
             }
             // -------------------------------------------------------- the last warp of the segment joins them
+            // (loops, not unrolled code: this runs once or twice in a CTA, from a cold instruction cache)
             // weights: eight lanes a pair, one for each active team, in the teams' order of tiles
             const int first_team = i_begin & (T - 1);
-            const int t_mine = lane & 7, w_mine = ((first_team + t_mine) & (T - 1)) * RG + rg;
-            float by[kCols / 4];
-#pragma unroll
-            for (int k = 0; k < kCols / 4; ++k) {
-                const int c = 4 * k + (lane >> 3);
+            const size_t part = (size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + col0;
+            float* by = weights + warp * kCols * 8;
+#pragma unroll 1
+            for (int c = lane >> 3; c < kCols; c += 4) {
+                const int t = lane & 7;
                 float2 ml = make_float2(-INFINITY, 0.0f);
-                if (t_mine < active) ml = slot_ml[w_mine * kCols + c];
+                if (t < active) ml = slot_ml[(((first_team + t) & (T - 1)) * RG + rg) * kCols + c];
                 float top = ml.x;
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                by[k] = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.0f) : exp2f(ml.x - top);
-                float sum = by[k] * ml.y;
+                float one = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.0f) : exp2f(ml.x - top);
+                float sum = one * ml.y;
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                float all = 0.0f;
-                if (t_mine == 0 && c < n_cols) all = emit_ml(c, top, sum);
-                by[k] *= __shfl_sync(0xffffffffu, all, lane & 24);
+                if (c < n_cols) {
+                    if (whole) {     // the output: normalised, with the sink
+                        const int row = (col0 + c) / a.group, head = h * a.group + (col0 + c) % a.group;
+                        const Finish fin = finish(top, sum, a.sink, head);
+                        one *= fin.by;
+                        if (t == 0 && a.out_lse) a.out_lse[((size_t)b * a.n_rows + row) * heads + head] = fin.lse;
+                    } else if (t == 0) {
+                        a.part_ml[part + c] = make_float2(top, sum);
+                    }
+                }
+                by[c * 8 + t] = one;
             }
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-                if (c >= n_cols) break;
+            __syncwarp();
+#pragma unroll 1
+            for (int c = 0; c < n_cols; ++c) {
                 const int chunk = (lane & ~3) | ((lane & 3) ^ ((c >> 1) & 3));
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int t = 0; t < T; ++t) {
-                    if (t >= active) break;
+#pragma unroll 4
+                for (int t = 0; t < active; ++t) {
                     const int w = ((first_team + t) & (T - 1)) * RG + rg;
-                    const float f = __shfl_sync(0xffffffffu, by[c / 4], (c & 3) * 8 + t);
+                    const float one = by[c * 8 + t];
                     const float4 v = reinterpret_cast<const float4*>(slots + (size_t)w * S::kSlotFloats + c * kD)[chunk];
-                    acc.x += f * v.x;
-                    acc.y += f * v.y;
-                    acc.z += f * v.z;
-                    acc.w += f * v.w;
+                    acc.x += one * v.x;
+                    acc.y += one * v.y;
+                    acc.z += one * v.z;
+                    acc.w += one * v.w;
                 }
-                emit(c, acc);
+                if (whole) {
+                    const size_t row = ((size_t)b * a.n_rows + (col0 + c) / a.group) * heads + h * a.group + (col0 + c) % a.group;
+                    store_row(a.out + row * kD + 4 * lane, acc);
+                } else {
+                    reinterpret_cast<float4*>(a.part_o + (part + c) * kD)[lane] = acc;
+                }
             }
             __syncwarp();
             if (lane < active) ptx::mbar_arrive(free0 + 8 * (((first_team + lane) & (T - 1)) * RG + rg));
