@@ -20,36 +20,41 @@ constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 // Few parts: a warp a pair.  Many (a long history over many CTAs): the warps share a pair's parts, each a
 // consecutive run with four chains of its own in order, and join through shared memory; the order is fixed.
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnPagedArgs a) {
-    __shared__ long long sums[2 * kJoinWarps];
+    __shared__ long long sums[3 * kJoinWarps];
     __shared__ float4 acc_s[kJoinWarps][32];
     __shared__ float2 ml_s[kJoinWarps];
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x / a.n_kv, h = blockIdx.x % a.n_kv, heads = a.n_kv * a.group;
-    // tiles before this sequence, and of all
-    long long before = 0, total = 0;
+    // costs before this sequence, and of all; tiles of all (the deal of the split kernel)
+    long long before = 0, total = 0, tiles = 0;
     for (int s = tid; s < a.n_seqs; s += kJoinThreads) {
         const Seq q = load_seq(a.lens, a.n_live, s, a.n_rows, a.max_pages);
-        const long long n = (long long)span_of(q.len, q.live, a.window).n * a.n_kv;
-        total += n;
-        if (s < b) before += n;
+        const int n = span_of(q.len, q.live, a.window).n;
+        const long long cost = n > 0 ? (long long)(n + kSegCost) * a.n_kv : 0;
+        total += cost;
+        tiles += (long long)n * a.n_kv;
+        if (s < b) before += cost;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         before += __shfl_xor_sync(0xffffffffu, before, o);
         total += __shfl_xor_sync(0xffffffffu, total, o);
+        tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
     }
     if (lane == 0) {
         sums[warp] = before;
         sums[kJoinWarps + warp] = total;
+        sums[2 * kJoinWarps + warp] = tiles;
     }
     __syncthreads();
-    before = total = 0;
+    before = total = tiles = 0;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
         before += sums[w];
         total += sums[kJoinWarps + w];
+        tiles += sums[2 * kJoinWarps + w];
     }
     const Seq sq = load_seq(a.lens, a.n_live, b, a.n_rows, a.max_pages);
     const int n_tiles = span_of(sq.len, sq.live, a.window).n;
@@ -60,9 +65,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnPaged
         if (lane == 0 && a.out_lse) a.out_lse[row] = -INFINITY;
     }
     if (n_tiles == 0) return;
-    const int n_ctas = (int)min((long long)a.n_ctas, total);
-    const long long first = before + (long long)h * n_tiles;
-    const int c_first = (int)(((first + 1) * n_ctas - 1) / total), c_last = (int)(((first + n_tiles) * n_ctas - 1) / total);
+    const int n_ctas = (int)min((long long)a.n_ctas, tiles);
+    const long long first = before + (long long)h * (n_tiles + kSegCost);    // this head's first cost
+    auto cta_of = [&](long long y) {
+        return total < (1ll << 24) ? (int)(((unsigned)(y + 1) * (unsigned)n_ctas - 1u) / (unsigned)total)
+                                   : (int)(((y + 1) * n_ctas - 1) / total);
+    };
+    const int c_first = cta_of(first + kSegCost), c_last = cta_of(first + kSegCost + n_tiles - 1);
     if (c_first == c_last) return;   // the split kernel has written the rows
     const int parts = c_last - c_first + 1;
     auto place = [&](int c) {        // the part of CTA c: its first segment's unless the head began inside it

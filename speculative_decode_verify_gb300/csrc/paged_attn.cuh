@@ -72,8 +72,13 @@ __device__ __forceinline__ Span span_of(int len, int live, int window) {
     return s;
 }
 
-// CTA c of n takes tiles [cta_begin(c), cta_begin(c + 1)) of `total`; n is at most total.
-__device__ __forceinline__ long long cta_begin(int c, int n, long long total) { return (long long)c * total / n; }
+// The deal.  A segment costs a CTA kSegCost tiles besides its tiles (its q, its joining), so the tiles are dealt by
+// cost: the tiles of a (sequence, head) of n pages lie at the costs s + kSegCost .. s + kSegCost + n - 1, the next
+// head's at s + kSegCost + n on, and CTA c of C takes the tiles whose cost is in [c W / C, (c + 1) W / C), W the sum.
+constexpr int kSegCost = 2;
+__device__ __forceinline__ long long cta_begin(int c, int n, long long total) {
+    return total < (1ll << 24) ? (long long)((unsigned)c * (unsigned)total / (unsigned)n) : (long long)c * total / n;
+}
 
 // What an unnormalised output row sum 2^(t - m) v is multiplied by, and its log-sum-exp: l is the sum of 2^(t - m),
 // the sink joins the denominator.
@@ -174,12 +179,13 @@ __device__ __forceinline__ bool page_wait(volatile int* issued, int i, uint32_t 
 // RT: 8-pair tiles per warp; RG: warps of a team; kTeams teams; kStages: pages in flight.
 template <int RT, int RG>
 struct Shape {
-    static constexpr int kTeams = kConsumers / RG;                       // a power of two, at most 8
+    static constexpr int kSplit = kConsumers / RG < 4 ? kConsumers / RG : 4;   // warps that share a page's blocks
+    static constexpr int kTeams = kConsumers / (RG * kSplit);                  // a power of two
     static constexpr int kCols = 8 * RT;                                 // pairs of a warp
     static constexpr int kSlotFloats = kCols * kD;
     static constexpr int kRingAt = 0;
     static constexpr int kFixed = kConsumers * (kSlotFloats + 10 * kCols) * 4  // the warps' slots, (m, l) and weights
-                                  + (VA_PAGED_MAX_SEQS + 1) * 8 + VA_PAGED_MAX_SEQS * 5   // prefix, lengths, live rows
+                                  + (VA_PAGED_MAX_SEQS + 1) * 8 + VA_PAGED_MAX_SEQS * 7   // prefixes, lengths, live rows
                                   + 2048;                                      // barriers, tickets, scales, alignment
     static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kTileBytes + 32);
     static constexpr int kStages = kFit < 12 ? kFit : 12;
@@ -192,7 +198,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_paged_kernel(const AttnPagedArgs a, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
     using S = Shape<RT, RG>;
-    constexpr int NS = S::kStages, T = S::kTeams, kCols = S::kCols;
+    constexpr int NS = S::kStages, T = S::kTeams, KG = S::kSplit, kCols = S::kCols;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* ring = base;
@@ -206,6 +212,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int* tickets = reinterpret_cast<int*>(scales + NS * 8);
     int* flags = tickets + RG * kTickets;     // [0] abort, [1] pages issued; from [2] on each stage's validity
     signed char* s_live = reinterpret_cast<signed char*>(flags + 2 + 16);
+    unsigned char* col_row = reinterpret_cast<unsigned char*>(s_live + VA_PAGED_MAX_SEQS);   // row and query head of each pair
+    unsigned char* col_head = col_row + kMaxCols;
+    unsigned short* some = reinterpret_cast<unsigned short*>(col_head + kMaxCols);   // sequences with tiles before each
     const uint32_t full0 = ptx::smem_u32(bars), empty0 = full0 + 8 * 16, free0 = full0 + 8 * 32;
     volatile int* abort = flags;
 
@@ -215,13 +224,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ptx::tma_prefetch_desc(&map_v);
         for (int s = 0; s < NS; ++s) {
             ptx::mbar_init(full0 + 8 * s, 1);
-            ptx::mbar_init(empty0 + 8 * s, RG);
+            ptx::mbar_init(empty0 + 8 * s, RG * KG);
         }
         for (int w = 0; w < kConsumers; ++w) ptx::mbar_init(free0 + 8 * w, 1);
         ptx::mbar_init_fence();
         flags[0] = flags[1] = 0;
     }
     for (int i = tid; i < RG * kTickets; i += kAttnThreads) tickets[i] = 0;
+    if (tid < kMaxCols) {
+        col_row[tid] = (unsigned char)(tid / a.group);
+        col_head[tid] = (unsigned char)(tid % a.group);
+    }
     __syncthreads();
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
@@ -230,8 +243,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int status = 0;
     constexpr int kPer = (VA_PAGED_MAX_SEQS + kAttnThreads - 1) / kAttnThreads;   // sequences per thread
     {
-        long long* sums = reinterpret_cast<long long*>(slots);
-        long long mine[kPer], sum = 0;
+        // per thread: tiles in the low 48 bits, sequences that have any above (at most 1,024)
+        unsigned long long* sums = reinterpret_cast<unsigned long long*>(slots);
+        unsigned long long mine[kPer], sum = 0;
         const int per = (a.n_seqs + kAttnThreads - 1) / kAttnThreads;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -242,27 +256,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 status |= s.status;
                 s_len[b] = s.len;
                 s_live[b] = (signed char)s.live;
-                mine[i] = (long long)span_of(s.len, s.live, a.window).n * a.n_kv;
+                const int n = span_of(s.len, s.live, a.window).n;
+                mine[i] = (unsigned long long)n * a.n_kv + (n > 0 ? 1ull << 48 : 0ull);
                 sum += mine[i];
             }
         }
-        long long upto = sum;
+        unsigned long long upto = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, upto, o);
+            const unsigned long long t = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += t;
         }
         if (lane == 31) sums[warp] = upto;
         __syncthreads();
-        long long before = upto - sum;
+        unsigned long long before = upto - sum;
         for (int w = 0; w < warp; ++w) before += sums[w];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int b = tid * per + i;
             if (i < per && b < a.n_seqs) {
-                pre[b] = before;
+                pre[b] = (long long)(before & 0xFFFFFFFFFFFFull);
+                some[b] = (unsigned short)(before >> 48);
                 before += mine[i];
-                if (b == a.n_seqs - 1) pre[a.n_seqs] = before;
+                if (b == a.n_seqs - 1) {
+                    pre[a.n_seqs] = (long long)(before & 0xFFFFFFFFFFFFull);
+                    some[a.n_seqs] = (unsigned short)(before >> 48);
+                }
             }
         }
         if (status && a.dev_status && blockIdx.x == 0) atomicOr(a.dev_status, status);
@@ -272,16 +291,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const long long total = pre[a.n_seqs];
     const int n_ctas = (int)min((long long)a.n_ctas, total);
     if ((int)blockIdx.x >= n_ctas) return;
-    const long long c0 = cta_begin(blockIdx.x, n_ctas, total), c1 = cta_begin(blockIdx.x + 1, n_ctas, total);
-    auto find = [&](long long x) {             // the sequence whose tiles hold tile x
+    // the last sequence that begins at or before x, in tiles (seg = 0) or in costs (seg = kSegCost x heads)
+    auto find = [&](long long x, int seg) {
         int lo = 0, hi = a.n_seqs;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (pre[mid] <= x) lo = mid;
+            if (pre[mid] + (long long)seg * some[mid] <= x) lo = mid;
             else hi = mid;
         }
         return lo;
     };
+    const int seg_cost = kSegCost * a.n_kv;
+    const long long cost = total + (long long)seg_cost * some[a.n_seqs];
+    auto first_tile = [&](int c) {            // of CTA c
+        const long long y = cta_begin(c, n_ctas, cost);
+        if (y >= cost) return total;
+        const int b = find(y, seg_cost);
+        const unsigned rest = (unsigned)(y - pre[b] - (long long)seg_cost * some[b]);
+        const unsigned n = (unsigned)span_of(s_len[b], s_live[b], a.window).n, per = n + kSegCost;
+        const unsigned h = rest / per, at = rest % per;
+        return pre[b] + (long long)h * n + (at > (unsigned)kSegCost ? at - kSegCost : 0u);
+    };
+    const long long c0 = first_tile(blockIdx.x), c1 = first_tile(blockIdx.x + 1);
 
     if (warp >= kConsumers) {
         ptx::set_max_regs_dec<kProducerRegs>();
@@ -294,7 +325,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int i = i0 + lane;
             int row = -1;
             if (i < n) {
-                const int b = find(c0 + i);
+                const int b = find(c0 + i, 0);
                 const Span sp = span_of(s_len[b], s_live[b], a.window);
                 const unsigned within = (unsigned)(c0 + i - pre[b]);
                 const int h = (int)(within / (unsigned)sp.n), t = sp.first + (int)(within % (unsigned)sp.n);
@@ -339,19 +370,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     } else {
         // ------------------------------------------------------------ consumers
         ptx::set_max_regs_inc<kConsumerRegs>();
-        const int team = warp / RG, rg = warp % RG;
+        const int team = warp / (RG * KG), kg = warp / RG % KG, rg = warp % RG;
         const int g = lane >> 2, j = lane & 3;
         const int kperm = (g & ~1) ^ ((g & 1) ? 5 : 0);       // this lane's key row of each eight
         const int heads = a.n_kv * a.group, cols_used = a.n_rows * a.group, col0 = rg * kCols;
         float* slot = slots + (size_t)warp * S::kSlotFloats;
         float2* my_ml = slot_ml + warp * kCols;
         int uses = 0;                                         // how often this warp has filled its slot
-        const int n_tiles = (int)(c1 - c0);
-        int b_next = find(c0), h_next, t_next;                // where the next segment begins
+        const int n_tiles = (int)(c1 - c0);                   // none where the CTA's costs are all a segment's own
+        int b_next = find(c0, 0), h_next, t_next;                // where the next segment begins
         {
             const unsigned within = (unsigned)(c0 - pre[b_next]), n = (unsigned)span_of(s_len[b_next], s_live[b_next], a.window).n;
-            h_next = (int)(within / n);
-            t_next = (int)(within % n);
+            h_next = n_tiles > 0 ? (int)(within / n) : 0;
+            t_next = n_tiles > 0 ? (int)(within % n) : 0;
         }
         bool given_up = false;
         for (int i_end = 0, seg = 0; i_end < n_tiles && !given_up; ++seg) {
@@ -381,9 +412,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 uint4 raw[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) raw[e] = make_uint4(0u, 0u, 0u, 0u);
-                if (c < cols_used && c / a.group < live) {
+                if (c < cols_used && col_row[c] < live) {
                     const uint4* src = reinterpret_cast<const uint4*>(
-                        a.q + (((size_t)b * a.n_rows + c / a.group) * heads + h * a.group + c % a.group) * kD + 16 * j);
+                        a.q + (((size_t)b * a.n_rows + col_row[c]) * heads + h * a.group + col_head[c]) * kD + 16 * j);
                     raw[0] = __ldg(src);
                     raw[1] = __ldg(src + 1);
                     raw[2] = __ldg(src + 8);
@@ -411,7 +442,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     f[n][e] = __shfl_sync(0xffffffffu, back, (2 * j + e) * 4);
                     m[n][e] = -INFINITY;
                     l[n][e] = 0.0f;
-                    p[n][e] = len - live + min((col0 + 8 * n + 2 * j + e) / a.group, live - 1);
+                    p[n][e] = len - live + min((int)col_row[min(col0 + 8 * n + 2 * j + e, kMaxCols - 1)], live - 1);
                 }
 #pragma unroll
                 for (int d = 0; d < 8; ++d)
@@ -432,9 +463,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int key0 = (sp.first + t0 + (i - i_begin)) * kPage;
                     // some row does not see all of the page's keys
                     const bool edge = key0 + kPage - 1 > len - live || (a.window > 0 && key0 < len - a.window);
-                    // the blocks that some row sees
-                    const int k_end = edge ? min(kBlocks, (len - key0 + kBlock - 1) / kBlock) : kBlocks;
-                    const int k_begin = edge && a.window > 0 ? max(0, len - live - a.window + 1 - key0) / kBlock : 0;
+                    // this warp's blocks, those of them that some row sees
+                    const int k_end = min(edge ? min(kBlocks, (len - key0 + kBlock - 1) / kBlock) : kBlocks, (kg + 1) * (kBlocks / KG));
+                    const int k_begin = max(edge && a.window > 0 ? max(0, len - live - a.window + 1 - key0) / kBlock : 0,
+                                            kg * (kBlocks / KG));
                     float vmax = 0.0f;
                     for (int k = k_begin; k < k_end; ++k) vmax = fmaxf(vmax, sc[kBlocks + k]);
                     if (vmax > R) {
@@ -561,7 +593,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             if (given_up) break;
             // -------------------------------------------------------- sums of the segment
-            const int active = min(T, seg_len), n_cols = min(kCols, live * a.group - col0);
+            const int active = min(T, seg_len) * KG, n_cols = min(kCols, live * a.group - col0);
             if (uses > 0 && !warp_wait(free0 + 8 * warp, (uses - 1) & 1, abort, status)) break;
             ++uses;
 #pragma unroll
@@ -598,15 +630,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             // -------------------------------------------------------- the last warp of the segment joins them
             // (loops, not unrolled code: this runs once or twice in a CTA, from a cold instruction cache)
-            // weights: eight lanes a pair, one for each active team, in the teams' order of tiles
-            const int first_team = i_begin & (T - 1);
+            // weights: eight lanes a pair, one for each active warp, in the order of tiles
+            auto warp_of = [&](int t) { return ((((i_begin & (T - 1)) + t / KG) & (T - 1)) * KG + t % KG) * RG + rg; };
             const size_t part = (size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + col0;
             float* by = weights + warp * kCols * 8;
 #pragma unroll 1
             for (int c = lane >> 3; c < kCols; c += 4) {
                 const int t = lane & 7;
                 float2 ml = make_float2(-INFINITY, 0.0f);
-                if (t < active) ml = slot_ml[(((first_team + t) & (T - 1)) * RG + rg) * kCols + c];
+                if (t < active) ml = slot_ml[warp_of(t) * kCols + c];
                 float top = ml.x;
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -618,7 +650,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                 if (c < n_cols) {
                     if (whole) {     // the output: normalised, with the sink
-                        const int row = (col0 + c) / a.group, head = h * a.group + (col0 + c) % a.group;
+                        const int row = col_row[col0 + c], head = h * a.group + col_head[col0 + c];
                         const Finish fin = finish(top, sum, a.sink, head);
                         one *= fin.by;
                         if (t == 0 && a.out_lse) a.out_lse[((size_t)b * a.n_rows + row) * heads + head] = fin.lse;
@@ -635,7 +667,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
                 for (int t = 0; t < active; ++t) {
-                    const int w = ((first_team + t) & (T - 1)) * RG + rg;
+                    const int w = warp_of(t);
                     const float one = by[c * 8 + t];
                     const float4 v = reinterpret_cast<const float4*>(slots + (size_t)w * S::kSlotFloats + c * kD)[chunk];
                     acc.x += one * v.x;
@@ -644,14 +676,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     acc.w += one * v.w;
                 }
                 if (whole) {
-                    const size_t row = ((size_t)b * a.n_rows + (col0 + c) / a.group) * heads + h * a.group + (col0 + c) % a.group;
+                    const size_t row = ((size_t)b * a.n_rows + col_row[col0 + c]) * heads + h * a.group + col_head[col0 + c];
                     store_row(a.out + row * kD + 4 * lane, acc);
                 } else {
                     reinterpret_cast<float4*>(a.part_o + (part + c) * kD)[lane] = acc;
                 }
             }
             __syncwarp();
-            if (lane < active) ptx::mbar_arrive(free0 + 8 * (((first_team + lane) & (T - 1)) * RG + rg));
+            if (lane < active) ptx::mbar_arrive(free0 + 8 * warp_of(lane));
         }
     }
     if (status && a.dev_status) atomicOr(a.dev_status, status);
