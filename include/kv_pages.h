@@ -13,8 +13,8 @@
  *   codes         [n_pages][n_kv_heads][64][128] bytes, keys and values apart, 16-byte aligned
  *   scales        [n_pages][n_kv_heads][4] fp32, one per block of VA_B8_BLOCK (16) positions and head
  *   format        VA_B8_E4M3 (codes are E4M3, the largest 448) or VA_B8_INT8 (codes are int8 in -127..127),
- *                 for keys and values alike.  An element stands for scale x code.  (E4M3's NaN code 0x7F is
- *                 never written; where it is read it counts as 480.)
+ *                 for keys and values alike.  An element stands for scale x code.  (The append writes no
+ *                 NaN code.)
  * Sequences
  *   table         int32 [n_seqs][max_pages]: entry x is the page of positions 64 x .. 64 x + 63, -1 = none
  *   lens          int32 [n_seqs]: positions of the sequence, its live rows among them

@@ -118,11 +118,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Codes to f16 pairs, in the integer pipe (cvt.rn.f16x2.e4m3x2 took 8.6 cycles an SM per warp: 1.15 us a tile).
-//   INT8: 0x64xx is 1024 + xx as f16; the biased code (+128) becomes the low byte, and 1152 comes off again.
-//   E4M3: the exponent and mantissa bits, shifted to their places in f16, are the code's value times 2^-8
-//         (subnormals included); that factor is put back in fp32, kUnit below.
-// Of a word c0..c3: INT8 gives (c0, c1), (c2, c3); E4M3 gives (c0, c2), (c1, c3).
+// A word's codes c0..c3 to the f16 pairs (c0, c1), (c2, c3), exactly.  E4M3: two conversions, which issue like any
+// integer instruction here (2.2 cycles a warp measured; placing the bits by shifts and masks took seven).  INT8:
+// 0x64xx is 1024 + xx, so the biased code (+128) becomes the low byte and 1152 comes off again.
 template <bool kInt8>
 __device__ __forceinline__ void widen(uint32_t w, uint32_t& x, uint32_t& y) {
     if (kInt8) {
@@ -133,18 +131,10 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& x, uint32_t& y) {
         x = *reinterpret_cast<const uint32_t*>(&lo);
         y = *reinterpret_cast<const uint32_t*>(&hi);
     } else {
-        x = ((w << 7) & 0x3F803F80u) | ((w << 8) & 0x80008000u);
-        y = ((w >> 1) & 0x3F803F80u) | (w & 0x80008000u);
+        asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+            : "=r"(x), "=r"(y) : "r"(w));
     }
 }
-// The same dimension of two keys side by side: words a (one key) and b (the other), dimensions i and i + 1, in the
-// order that widen() takes apart into (a_i, b_i), (a_i+1, b_i+1).
-template <bool kInt8, int kHalf>
-__device__ __forceinline__ uint32_t pair_up(uint32_t a, uint32_t b) {
-    return __byte_perm(a, b, kInt8 ? (kHalf ? 0x7362 : 0x5140) : (kHalf ? 0x7632 : 0x5410));
-}
-template <bool kInt8>
-constexpr float kUnit = kInt8 ? 1.0f : 256.0f;
 
 // A wait that the warp makes as one: every lane leaves it with the same answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int& status) {
@@ -179,7 +169,7 @@ __device__ __forceinline__ bool page_wait(volatile int* issued, int i, uint32_t 
 // RT: 8-pair tiles per warp; RG: warps of a team; kTeams teams; kStages: pages in flight.
 template <int RT, int RG>
 struct Shape {
-    static constexpr int kSplit = kConsumers / RG < 4 ? kConsumers / RG : 4;   // warps that share a page's blocks
+    static constexpr int kSplit = 2;                                           // warps that share a page's blocks
     static constexpr int kTeams = kConsumers / (RG * kSplit);                  // a power of two
     static constexpr int kCols = 8 * RT;                                 // pairs of a warp
     static constexpr int kSlotFloats = kCols * kD;
@@ -198,7 +188,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_paged_kernel(const AttnPagedArgs a, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
     using S = Shape<RT, RG>;
-    constexpr int NS = S::kStages, T = S::kTeams, KG = S::kSplit, kCols = S::kCols;
+    constexpr int NS = S::kStages, T = S::kTeams, KG = S::kSplit, KB = kBlocks / KG, kCols = S::kCols;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* ring = base;
@@ -428,15 +418,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const int up = min(max(268 - (int)(top >> 7), 1), 253);
                 const float by = __uint_as_float((uint32_t)up << 23);
-                const float back = __uint_as_float((uint32_t)(254 - up) << 23) * (a.scale_log2 * kUnit<kInt8>);
+                const float back = __uint_as_float((uint32_t)(254 - up) << 23) * a.scale_log2;
 #pragma unroll
-                for (int s = 0; s < 8; ++s) {   // four dimensions, paired as widen() pairs codes
-                    const uint32_t v0 = w[2 * s], v1 = w[2 * s + 1];
-                    const float x0 = __uint_as_float(v0 << 16) * by, x1 = __uint_as_float(v0 & 0xFFFF0000u) * by;
-                    const float x2 = __uint_as_float(v1 << 16) * by, x3 = __uint_as_float(v1 & 0xFFFF0000u) * by;
-                    qf[n][s][0] = kInt8 ? pack_f16(x0, x1) : pack_f16(x0, x2);
-                    qf[n][s][1] = kInt8 ? pack_f16(x2, x3) : pack_f16(x1, x3);
-                }
+                for (int s = 0; s < 8; ++s)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t v = w[2 * s + e];
+                        qf[n][s][e] = pack_f16(__uint_as_float(v << 16) * by, __uint_as_float(v & 0xFFFF0000u) * by);
+                    }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     f[n][e] = __shfl_sync(0xffffffffu, back, (2 * j + e) * 4);
@@ -463,91 +452,96 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int key0 = (sp.first + t0 + (i - i_begin)) * kPage;
                     // some row does not see all of the page's keys
                     const bool edge = key0 + kPage - 1 > len - live || (a.window > 0 && key0 < len - a.window);
-                    // this warp's blocks, those of them that some row sees
-                    const int k_end = min(edge ? min(kBlocks, (len - key0 + kBlock - 1) / kBlock) : kBlocks, (kg + 1) * (kBlocks / KG));
-                    const int k_begin = max(edge && a.window > 0 ? max(0, len - live - a.window + 1 - key0) / kBlock : 0,
-                                            kg * (kBlocks / KG));
-                    float vmax = 0.0f;
-                    for (int k = k_begin; k < k_end; ++k) vmax = fmaxf(vmax, sc[kBlocks + k]);
-                    if (vmax > R) {
-                        const float up = __uint_as_float(min((__float_as_uint(vmax) + 0x7FFFFFu) & 0x7F800000u, 0x7F000000u));
-                        const float by = R / up;
-                        R = up;
-                        inv_r = 1.0f / up;
+                    // this warp's KB blocks; past: blocks that begin past the sequence, where scales may be anything
+                    const int k0 = kg * KB;
+                    const bool none = edge && (key0 + k0 * kBlock >= len ||
+                                               (a.window > 0 && key0 + (k0 + KB) * kBlock <= len - live - a.window + 1));
+                    if (!none) {
+                        float vs[KB];
+                        float vmax = 0.0f;
 #pragma unroll
-                        for (int n = 0; n < RT; ++n)
-#pragma unroll
-                            for (int d = 0; d < 8; ++d)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) o[n][d][e] *= by;
-                    }
-#pragma unroll 1
-                    for (int k = k_begin; k < k_end; ++k) {
-                        // scores of 16 keys, the head dimension in two halves (two shorter chains)
-                        float s[2][RT][4];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
+                        for (int k = 0; k < KB; ++k) {
+                            vs[k] = edge && key0 + (k0 + k) * kBlock >= len ? 0.0f : sc[kBlocks + k0 + k];
+                            vmax = fmaxf(vmax, vs[k]);
+                        }
+                        if (vmax > R) {
+                            const float up = __uint_as_float(min((__float_as_uint(vmax) + 0x7FFFFFu) & 0x7F800000u, 0x7F000000u));
+                            const float by = R / up;
+                            R = up;
+                            inv_r = 1.0f / up;
 #pragma unroll
                             for (int n = 0; n < RT; ++n)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) s[u][n][e] = 0.0f;
-                        const unsigned char* row = kt + (k * kBlock + kperm) * kD;
-                        uint4 ra[2], rb[2];
+                                for (int d = 0; d < 8; ++d)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[n][d][e] *= by;
+                        }
+                        // scores of 16 KB keys
+                        float s[KB][RT][4];
+#pragma unroll
+                        for (int k = 0; k < KB; ++k)
+#pragma unroll
+                            for (int n = 0; n < RT; ++n)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) s[k][n][e] = 0.0f;
+                        const unsigned char* row = kt + (k0 * kBlock + kperm) * kD;
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const int at = ((j + 4 * u) ^ kperm) * 16;
-                            ra[u] = *reinterpret_cast<const uint4*>(row + at);
-                            rb[u] = *reinterpret_cast<const uint4*>(row + 8 * kD + at);
-                        }
+                            uint4 ra[KB], rb[KB];
 #pragma unroll
-                        for (int w = 0; w < 4; ++w)
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const uint32_t wa[4] = {ra[u].x, ra[u].y, ra[u].z, ra[u].w};
-                                const uint32_t wb[4] = {rb[u].x, rb[u].y, rb[u].z, rb[u].w};
-                                uint32_t a0, a1, a2, a3;
-                                widen<kInt8>(wa[w], a0, a2);
-                                widen<kInt8>(wb[w], a1, a3);
-#pragma unroll
-                                for (int n = 0; n < RT; ++n)
-                                    mma_f16(s[u][n], a0, a1, a2, a3, qf[n][4 * u + w][0], qf[n][4 * u + w][1]);
+                            for (int k = 0; k < KB; ++k) {
+                                ra[k] = *reinterpret_cast<const uint4*>(row + k * kBlock * kD + at);
+                                rb[k] = *reinterpret_cast<const uint4*>(row + (k * kBlock + 8) * kD + at);
                             }
-                        // V, while the scores are on their way
-                        const int even = 2 * j, odd = (2 * j) ^ 5;
-                        const unsigned char* blk = vt + k * kBlock * kD;
-                        const uint4 w0 = *reinterpret_cast<const uint4*>(blk + even * kD + (g ^ even) * 16);
-                        const uint4 w1 = *reinterpret_cast<const uint4*>(blk + odd * kD + (g ^ odd) * 16);
-                        const uint4 w2 = *reinterpret_cast<const uint4*>(blk + (even + 8) * kD + (g ^ even) * 16);
-                        const uint4 w3 = *reinterpret_cast<const uint4*>(blk + (odd + 8) * kD + (g ^ odd) * 16);
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                                for (int k = 0; k < KB; ++k) {
+                                    const uint32_t wa[4] = {ra[k].x, ra[k].y, ra[k].z, ra[k].w};
+                                    const uint32_t wb[4] = {rb[k].x, rb[k].y, rb[k].z, rb[k].w};
+                                    uint32_t a0, a1, a2, a3;
+                                    widen<kInt8>(wa[w], a0, a2);
+                                    widen<kInt8>(wb[w], a1, a3);
+#pragma unroll
+                                    for (int n = 0; n < RT; ++n)
+                                        mma_f16(s[k][n], a0, a1, a2, a3, qf[n][4 * u + w][0], qf[n][4 * u + w][1]);
+                                }
+                        }
                         // exponents and masks; is some score over its column's reference by more than kLazy?
-                        const float ks = sc[k];
                         bool raise = false;
 #pragma unroll
                         for (int n = 0; n < RT; ++n)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float fk = f[n][e] * ks;
-                                float x0 = (s[0][n][e] + s[1][n][e]) * fk, x1 = (s[0][n][2 + e] + s[1][n][2 + e]) * fk;
-                                if (edge) {
-                                    const int key = key0 + k * kBlock + kperm;
-                                    const int lo = a.window > 0 ? p[n][e] - a.window : -1;
-                                    if (key > p[n][e] || key <= lo) x0 = -INFINITY;
-                                    if (key + 8 > p[n][e] || key + 8 <= lo) x1 = -INFINITY;
+                                float top = -INFINITY;
+#pragma unroll
+                                for (int k = 0; k < KB; ++k) {
+                                    const float fk = f[n][e] * sc[k0 + k];
+                                    float x0 = s[k][n][e] * fk, x1 = s[k][n][2 + e] * fk;
+                                    if (edge) {
+                                        const int key = key0 + (k0 + k) * kBlock + kperm;
+                                        const int lo = a.window > 0 ? p[n][e] - a.window : -1;
+                                        if (key > p[n][e] || key <= lo) x0 = -INFINITY;
+                                        if (key + 8 > p[n][e] || key + 8 <= lo) x1 = -INFINITY;
+                                    }
+                                    s[k][n][e] = x0;
+                                    s[k][n][2 + e] = x1;
+                                    top = fmaxf(top, fmaxf(x0, x1));
                                 }
-                                s[0][n][e] = x0;
-                                s[0][n][2 + e] = x1;
-                                raise = raise || fmaxf(x0, x1) - m[n][e] > kLazy;
+                                raise = raise || top - m[n][e] > kLazy;
                             }
                         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                             for (int n = 0; n < RT; ++n)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    float now = fmaxf(s[0][n][e], s[0][n][2 + e]);
+                                    float now = m[n][e];
+#pragma unroll
+                                    for (int k = 0; k < KB; ++k) now = fmaxf(now, fmaxf(s[k][n][e], s[k][n][2 + e]));
                                     now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 4));
                                     now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 8));
                                     now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 16));
-                                    now = fmaxf(now, m[n][e]);
                                     const float by = m[n][e] == -INFINITY ? 0.0f : ptx::ex2(m[n][e] - now);
                                     m[n][e] = now;
                                     l[n][e] *= by;
@@ -559,32 +553,55 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 }
                         }
                         // weights
-                        const float r = sc[kBlocks + k] * inv_r;
-                        uint32_t pf[RT][2];
+                        uint32_t pf[KB][RT][2];
 #pragma unroll
                         for (int n = 0; n < RT; ++n) {
                             const float z0 = (m[n][0] == -INFINITY ? 0.0f : m[n][0]) - kShift;
                             const float z1 = (m[n][1] == -INFINITY ? 0.0f : m[n][1]) - kShift;
-                            const float p0 = ptx::ex2(s[0][n][0] - z0), p1 = ptx::ex2(s[0][n][1] - z1);
-                            const float p2 = ptx::ex2(s[0][n][2] - z0), p3 = ptx::ex2(s[0][n][3] - z1);
-                            l[n][0] += p0 + p2;
-                            l[n][1] += p1 + p3;
-                            pf[n][0] = transpose8(pack_f16(p0 * r, p1 * r));
-                            pf[n][1] = transpose8(pack_f16(p2 * r, p3 * r));
+#pragma unroll
+                            for (int k = 0; k < KB; ++k) {
+                                const float r = vs[k] * inv_r;
+                                const float p0 = ptx::ex2(s[k][n][0] - z0), p1 = ptx::ex2(s[k][n][1] - z1);
+                                const float p2 = ptx::ex2(s[k][n][2] - z0), p3 = ptx::ex2(s[k][n][3] - z1);
+                                l[n][0] += p0 + p2;
+                                l[n][1] += p1 + p3;
+                                pf[k][n][0] = transpose8(pack_f16(p0 * r, p1 * r));
+                                pf[k][n][1] = transpose8(pack_f16(p2 * r, p3 * r));
+                            }
                         }
-                        const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
-                        const uint32_t u2[4] = {w2.x, w2.y, w2.z, w2.w}, u3[4] = {w3.x, w3.y, w3.z, w3.w};
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            uint32_t a0, a1, a2, a3;
-                            widen<kInt8>(pair_up<kInt8, 0>(u0[w], u1[w]), a0, a1);
-                            widen<kInt8>(pair_up<kInt8, 0>(u2[w], u3[w]), a2, a3);
+                        for (int k = 0; k < KB; ++k) {
+                            const int even = 2 * j, odd = (2 * j) ^ 5;
+                            const unsigned char* blk = vt + (k0 + k) * kBlock * kD;
+                            uint4 w0 = *reinterpret_cast<const uint4*>(blk + even * kD + (g ^ even) * 16);
+                            uint4 w1 = *reinterpret_cast<const uint4*>(blk + odd * kD + (g ^ odd) * 16);
+                            uint4 w2 = *reinterpret_cast<const uint4*>(blk + (even + 8) * kD + (g ^ even) * 16);
+                            uint4 w3 = *reinterpret_cast<const uint4*>(blk + (odd + 8) * kD + (g ^ odd) * 16);
+                            if (!kInt8 && edge) {      // what lies past the sequence may be NaN
+                                const int key = key0 + (k0 + k) * kBlock;
+                                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                                if (key + even >= len) w0 = zero;
+                                if (key + odd >= len) w1 = zero;
+                                if (key + even + 8 >= len) w2 = zero;
+                                if (key + odd + 8 >= len) w3 = zero;
+                            }
+                            const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
+                            const uint32_t u2[4] = {w2.x, w2.y, w2.z, w2.w}, u3[4] = {w3.x, w3.y, w3.z, w3.w};
 #pragma unroll
-                            for (int n = 0; n < RT; ++n) mma_f16(o[n][2 * w], a0, a1, a2, a3, pf[n][0], pf[n][1]);
-                            widen<kInt8>(pair_up<kInt8, 1>(u0[w], u1[w]), a0, a1);
-                            widen<kInt8>(pair_up<kInt8, 1>(u2[w], u3[w]), a2, a3);
+                            for (int w = 0; w < 4; ++w) {
+                                // dimensions 4 w, 4 w + 1 of the even and odd keys side by side, then 4 w + 2, 4 w + 3
+                                uint32_t a0, a1, a2, a3;
+                                widen<kInt8>(__byte_perm(u0[w], u1[w], 0x5140), a0, a1);
+                                widen<kInt8>(__byte_perm(u2[w], u3[w], 0x5140), a2, a3);
 #pragma unroll
-                            for (int n = 0; n < RT; ++n) mma_f16(o[n][2 * w + 1], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                                for (int n = 0; n < RT; ++n)
+                                    mma_f16(o[n][2 * w], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
+                                widen<kInt8>(__byte_perm(u0[w], u1[w], 0x7362), a0, a1);
+                                widen<kInt8>(__byte_perm(u2[w], u3[w], 0x7362), a2, a3);
+#pragma unroll
+                                for (int n = 0; n < RT; ++n)
+                                    mma_f16(o[n][2 * w + 1], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
+                            }
                         }
                     }
                 }
@@ -608,7 +625,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (g == 0) my_ml[c] = make_float2(m[n][e] - kShift, sum);
                     // dimensions 16 g .. 16 g + 15 of pair c: the lane's eight accumulator pairs in order
                     float4* dst = reinterpret_cast<float4*>(slot + c * kD);
-                    const float by = R * kUnit<kInt8>;
+                    const float by = R;
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
                         dst[4 * g + (w ^ j)] = make_float4(o[n][2 * w][e] * by, o[n][2 * w][2 + e] * by,
