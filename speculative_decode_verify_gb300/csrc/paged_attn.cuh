@@ -147,14 +147,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return ok;
 }
 
-// The page of tile i is in its stage: first that its loads have been issued (*issued > i), because a barrier's
-// parity alone does not tell the use that is waited for from the one before the last; then that they are done.
-__device__ __forceinline__ bool page_wait(volatile int* issued, int i, uint32_t bar, uint32_t parity, volatile int* abort,
+// A stage's use number `use` has been loaded (bar: its full barrier) or read (its empty barrier): first that the
+// use's loads have been issued (*issued > use), because a barrier's parity alone does not tell the use that is
+// waited for from the one before the last; then the barrier.
+__device__ __forceinline__ bool page_wait(volatile int* issued, int use, uint32_t bar, uint32_t parity, volatile int* abort,
                                           int& status) {
     bool ok = true;
-    if (*issued <= i) {
+    if (*issued <= use) {
         const uint64_t t0 = ptx::globaltimer_ns();
-        while (*issued <= i && ok) ok = !*abort && ptx::globaltimer_ns() - t0 <= kWaitNs;
+        while (*issued <= use && ok) ok = !*abort && ptx::globaltimer_ns() - t0 <= kWaitNs;
     }
     if (!__all_sync(0xffffffffu, ok)) {
         if (!*abort) status |= VA_DEV_TIMEOUT;
@@ -200,8 +201,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_len + VA_PAGED_MAX_SEQS + 2);
     float* scales = reinterpret_cast<float*>(bars + 48);
     int* tickets = reinterpret_cast<int*>(scales + NS * 8);
-    int* flags = tickets + RG * kTickets;     // [0] abort, [1] pages issued; from [2] on each stage's validity
-    signed char* s_live = reinterpret_cast<signed char*>(flags + 2 + 16);
+    int* issued = tickets + RG * kTickets;    // each stage's uses so far
+    int* valid = issued + 16;                 // whether its tile has a page
+    int* flags = valid + 16;                  // [0]: the CTA gives up
+    signed char* s_live = reinterpret_cast<signed char*>(flags + 4);
     unsigned char* col_row = reinterpret_cast<unsigned char*>(s_live + VA_PAGED_MAX_SEQS);   // row and query head of each pair
     unsigned char* col_head = col_row + kMaxCols;
     unsigned short* some = reinterpret_cast<unsigned short*>(col_head + kMaxCols);   // sequences with tiles before each
@@ -218,7 +221,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         for (int w = 0; w < kConsumers; ++w) ptx::mbar_init(free0 + 8 * w, 1);
         ptx::mbar_init_fence();
-        flags[0] = flags[1] = 0;
+        flags[0] = 0;
+        for (int s = 0; s < 16; ++s) issued[s] = 0;
     }
     for (int i = tid; i < RG * kTickets; i += kAttnThreads) tickets[i] = 0;
     if (tid < kMaxCols) {
@@ -286,77 +290,81 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         int lo = 0, hi = a.n_seqs;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (pre[mid] + (long long)seg * some[mid] <= x) lo = mid;
+            if (pre[mid] + seg * (int)some[mid] <= x) lo = mid;
             else hi = mid;
         }
         return lo;
     };
     const int seg_cost = kSegCost * a.n_kv;
-    const long long cost = total + (long long)seg_cost * some[a.n_seqs];
-    auto first_tile = [&](int c) {            // of CTA c
-        const long long y = cta_begin(c, n_ctas, cost);
-        if (y >= cost) return total;
-        const int b = find(y, seg_cost);
-        const unsigned rest = (unsigned)(y - pre[b] - (long long)seg_cost * some[b]);
-        const unsigned n = (unsigned)span_of(s_len[b], s_live[b], a.window).n, per = n + kSegCost;
-        const unsigned h = rest / per, at = rest % per;
-        return pre[b] + (long long)h * n + (at > (unsigned)kSegCost ? at - kSegCost : 0u);
-    };
-    const long long c0 = first_tile(blockIdx.x), c1 = first_tile(blockIdx.x + 1);
+    const long long cost = total + seg_cost * (int)some[a.n_seqs];
+    // where this CTA's tiles begin (even lanes) and the next one's (odd lanes)
+    long long c0 = total, c1;
+    int b_first = 0, h_first = 0, t_first = 0;
+    {
+        const long long y = cta_begin(blockIdx.x + (lane & 1), n_ctas, cost);
+        if (y < cost) {
+            b_first = find(y, seg_cost);
+            const unsigned rest = (unsigned)(y - pre[b_first] - seg_cost * (int)some[b_first]);
+            const unsigned n = (unsigned)span_of(s_len[b_first], s_live[b_first], a.window).n, per = n + kSegCost;
+            h_first = (int)(rest / per);
+            t_first = max((int)(rest % per) - kSegCost, 0);
+            c0 = pre[b_first] + (long long)h_first * n + t_first;
+        }
+        c1 = __shfl_sync(0xffffffffu, c0, 1);
+        c0 = __shfl_sync(0xffffffffu, c0, 0);
+        b_first = __shfl_sync(0xffffffffu, b_first, 0);
+        h_first = __shfl_sync(0xffffffffu, h_first, 0);
+        t_first = __shfl_sync(0xffffffffu, t_first, 0);
+    }
 
     if (warp >= kConsumers) {
         ptx::set_max_regs_dec<kProducerRegs>();
-        if (warp > kConsumers) return;
-        // ------------------------------------------------------------ producer: one lane per tile, in turn
-        const int n = (int)(c1 - c0);
-        int issued = 0;
+        // ------------------------------------------------------------ producers
+        // Four warps take the tiles in turn (one alone issued a tile in 0.5 us, longer than a tile takes to arrive).
+        // A lane looks up a tile's page, 32 at once; then the warp issues them one by one, a copy a lane.
+        const int n = (int)(c1 - c0), pw = warp - kConsumers;
+        int last = -1;
         bool given_up = false;
-        for (int i0 = 0; i0 < n && !given_up; i0 += 32) {
-            const int i = i0 + lane;
+        for (int i0 = pw; i0 < n && !given_up; i0 += 4 * 32) {
             int row = -1;
-            if (i < n) {
-                const int b = find(c0 + i, 0);
+            if (i0 + 4 * lane < n) {
+                const long long x = c0 + i0 + 4 * lane;
+                const int b = find(x, 0);
                 const Span sp = span_of(s_len[b], s_live[b], a.window);
-                const unsigned within = (unsigned)(c0 + i - pre[b]);
+                const unsigned within = (unsigned)(x - pre[b]);
                 const int h = (int)(within / (unsigned)sp.n), t = sp.first + (int)(within % (unsigned)sp.n);
                 const int page = __ldcg(a.table + (size_t)b * a.max_pages + t);
                 if (page >= 0 && page < a.n_pages) row = page * a.n_kv + h;
                 else status |= VA_DEV_BAD_PAGE;
             }
-            for (int l = 0; l < 32 && i0 + l < n; ++l) {
-                if (lane == l) {
-                    const int s = i % NS, use = i / NS;
-                    if (use > 0 && !ptx::mbar_wait(empty0 + 8 * s, (use - 1) & 1, abort, kWaitNs)) {
-                        if (!*abort) status |= VA_DEV_TIMEOUT;
-                        *abort = 1;
-                        given_up = true;
-                    } else {
-                        const uint32_t bar = full0 + 8 * s, dst = ptx::smem_u32(ring + s * kTileBytes);
-                        flags[2 + s] = row >= 0;
-                        if (row >= 0) {
-                            const uint32_t sc = ptx::smem_u32(scales + 8 * s);
-                            ptx::mbar_arrive_expect_tx(bar, kTileBytes + 32);
-                            ptx::tma_load_2d(dst, &map_k, 0, row * kPage, bar);
-                            ptx::tma_load_2d(dst + kHeadBytes, &map_v, 0, row * kPage, bar);
-                            ptx::bulk_load(sc, a.k_scale + (size_t)row * kBlocks, 16, bar);
-                            ptx::bulk_load(sc + 16, a.v_scale + (size_t)row * kBlocks, 16, bar);
-                        } else {
-                            ptx::mbar_arrive(bar);
-                        }
-                        issued = i + 1;
-                        // (no fence: what the reader must not miss, the end of the stage's last use, came before
-                        // this lane's wait for the stage, and shared memory has one order)
-                        *(volatile int*)(flags + 1) = issued;
-                    }
+            for (int l = 0; l < 32 && i0 + 4 * l < n; ++l) {
+                const int i = i0 + 4 * l, s = i % NS, use = i / NS, r = __shfl_sync(0xffffffffu, row, l);
+                if (use > 0 && !page_wait(issued + s, use - 1, empty0 + 8 * s, (use - 1) & 1, abort, status)) {
+                    given_up = true;
+                    break;
                 }
-                given_up = __any_sync(0xffffffffu, given_up);
-                if (given_up) break;
+                const uint32_t bar = full0 + 8 * s, dst = ptx::smem_u32(ring + s * kTileBytes);
+                if (lane == 0) {
+                    valid[s] = r >= 0;
+                    if (r >= 0) ptx::mbar_arrive_expect_tx(bar, kTileBytes + 32);
+                    else ptx::mbar_arrive(bar);
+                    // (no fence: what the reader must not miss, the end of the stage's last use, came before this
+                    // lane's wait for the stage, and shared memory has one order)
+                    *(volatile int*)(issued + s) = use + 1;
+                }
+                __syncwarp();
+                if (r >= 0) {
+                    if (lane < 2)
+                        ptx::tma_load_2d(dst + lane * kHeadBytes, lane ? &map_v : &map_k, 0, r * kPage, bar);
+                    else if (lane < 4)
+                        ptx::bulk_load(ptx::smem_u32(scales + 8 * s) + 16 * (lane - 2),
+                                       (lane == 2 ? a.k_scale : a.v_scale) + (size_t)r * kBlocks, 16, bar);
+                }
+                last = i;
             }
         }
         // no CTA ends with copies under way, even if its consumers gave up
-        issued = __reduce_max_sync(0xffffffffu, issued);
-        for (int i = max(0, issued - NS) + lane; i < issued; i += 32)
-            ptx::mbar_wait(full0 + 8 * (i % NS), (i / NS) & 1, nullptr, kWaitNs);
+        for (; last >= 0 && last > n - 1 - NS; last -= 4) ptx::mbar_wait(full0 + 8 * (last % NS), (last / NS) & 1, nullptr, kWaitNs);
     } else {
         // ------------------------------------------------------------ consumers
         ptx::set_max_regs_inc<kConsumerRegs>();
@@ -368,12 +376,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         float2* my_ml = slot_ml + warp * kCols;
         int uses = 0;                                         // how often this warp has filled its slot
         const int n_tiles = (int)(c1 - c0);                   // none where the CTA's costs are all a segment's own
-        int b_next = find(c0, 0), h_next, t_next;                // where the next segment begins
-        {
-            const unsigned within = (unsigned)(c0 - pre[b_next]), n = (unsigned)span_of(s_len[b_next], s_live[b_next], a.window).n;
-            h_next = n_tiles > 0 ? (int)(within / n) : 0;
-            t_next = n_tiles > 0 ? (int)(within % n) : 0;
-        }
+        int b_next = b_first, h_next = h_first, t_next = t_first;   // where the next segment begins
         bool given_up = false;
         for (int i_end = 0, seg = 0; i_end < n_tiles && !given_up; ++seg) {
             const int b = b_next, h = h_next, t0 = t_next, i_begin = i_end;
@@ -441,11 +444,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             float R = 0.0f, inv_r = 0.0f;
             for (; i < i_end; i += T) {
                 const int st = i % NS;
-                if (!page_wait(flags + 1, i, full0 + 8 * st, (i / NS) & 1, abort, status)) {
+                if (!page_wait(issued + st, i / NS, full0 + 8 * st, (i / NS) & 1, abort, status)) {
                     given_up = true;
                     break;
                 }
-                if (flags[2 + st]) {
+                if (valid[st]) {
                     const unsigned char* kt = ring + st * kTileBytes;
                     const unsigned char* vt = kt + kHeadBytes;
                     const float* sc = scales + 8 * st;
