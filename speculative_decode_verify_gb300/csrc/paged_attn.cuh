@@ -40,6 +40,7 @@ constexpr int kTileBytes = 2 * kHeadBytes;    // K and V codes of a tile
 constexpr uint64_t kWaitNs = 1000000000ull;   // a wait gives up after a second (VA_DEV_TIMEOUT)
 constexpr float kShift = 6.0f;                // p = 2^(t - m + kShift)
 constexpr float kLazy = 8.0f;                 // m is raised when a score passes it by this much
+constexpr float kNoScore = -3.0e38f;          // m before the first score (any score passes it)
 constexpr int kTickets = 64;                  // segments that can be open at once in a CTA are fewer
 
 // Workspace: partial sums of 2 segments a CTA, [2 kMaxCtas][kMaxCols][128] floats, then their (m, l).
@@ -121,12 +122,18 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // A word's codes c0..c3 to the f16 pairs (c0, c1), (c2, c3), exactly.  E4M3: two conversions, which issue like any
 // integer instruction here (2.2 cycles a warp measured; placing the bits by shifts and masks took seven).  INT8:
 // 0x64xx is 1024 + xx, so the biased code (+128) becomes the low byte and 1152 comes off again.
-template <bool kInt8>
+// kBiased leaves the 1152 on (the keys': their scores lose 1152 sum q, one subtraction a score).
+template <bool kInt8, bool kBiased>
 __device__ __forceinline__ void widen(uint32_t w, uint32_t& x, uint32_t& y) {
     if (kInt8) {
         const uint32_t u = w ^ 0x80808080u;
         const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
         uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        if (kBiased) {
+            x = a;
+            y = b;
+            return;
+        }
         const __half2 lo = __hsub2(*reinterpret_cast<__half2*>(&a), bias), hi = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
         x = *reinterpret_cast<const uint32_t*>(&lo);
         y = *reinterpret_cast<const uint32_t*>(&hi);
@@ -175,7 +182,7 @@ struct Shape {
     static constexpr int kCols = 8 * RT;                                 // pairs of a warp
     static constexpr int kSlotFloats = kCols * kD;
     static constexpr int kRingAt = 0;
-    static constexpr int kFixed = kConsumers * (kSlotFloats + 10 * kCols) * 4  // the warps' slots, (m, l) and weights
+    static constexpr int kFixed = kConsumers * (kSlotFloats + 2 * kCols) * 4   // the warps' slots and their (m, l)
                                   + (VA_PAGED_MAX_SEQS + 1) * 8 + VA_PAGED_MAX_SEQS * 7   // prefixes, lengths, live rows
                                   + 2048;                                      // barriers, tickets, scales, alignment
     static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kTileBytes + 32);
@@ -195,8 +202,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     unsigned char* ring = base;
     float* slots = reinterpret_cast<float*>(ring + NS * kTileBytes);
     float2* slot_ml = reinterpret_cast<float2*>(slots + kConsumers * S::kSlotFloats);
-    float* weights = reinterpret_cast<float*>(slot_ml + kConsumers * kCols);
-    long long* pre = reinterpret_cast<long long*>(weights + kConsumers * kCols * 8);
+    long long* pre = reinterpret_cast<long long*>(slot_ml + kConsumers * kCols);
     int* s_len = reinterpret_cast<int*>(pre + VA_PAGED_MAX_SEQS + 1);
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_len + VA_PAGED_MAX_SEQS + 2);
     float* scales = reinterpret_cast<float*>(bars + 48);
@@ -209,6 +215,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     unsigned char* col_head = col_row + kMaxCols;
     unsigned short* some = reinterpret_cast<unsigned short*>(col_head + kMaxCols);   // sequences with tiles before each
     const uint32_t full0 = ptx::smem_u32(bars), empty0 = full0 + 8 * 16, free0 = full0 + 8 * 32;
+    const uint32_t filled = full0 + 8 * 40, joined = full0 + 8 * 41;
     volatile int* abort = flags;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -220,6 +227,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             ptx::mbar_init(empty0 + 8 * s, RG * KG);
         }
         for (int w = 0; w < kConsumers; ++w) ptx::mbar_init(free0 + 8 * w, 1);
+        ptx::mbar_init(filled, kConsumers);
+        ptx::mbar_init(joined, kConsumers);
         ptx::mbar_init_fence();
         flags[0] = 0;
         for (int s = 0; s < 16; ++s) issued[s] = 0;
@@ -374,7 +383,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int heads = a.n_kv * a.group, cols_used = a.n_rows * a.group, col0 = rg * kCols;
         float* slot = slots + (size_t)warp * S::kSlotFloats;
         float2* my_ml = slot_ml + warp * kCols;
-        int uses = 0;                                         // how often this warp has filled its slot
+        // how often the slot has been filled for a single warp's join, and for a common one; which was the last
+        int uses = 0, joins = 0, slot_use = 0;
         const int n_tiles = (int)(c1 - c0);                   // none where the CTA's costs are all a segment's own
         int b_next = b_first, h_next = h_first, t_next = t_first;   // where the next segment begins
         bool given_up = false;
@@ -394,52 +404,67 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             int i = i_begin + ((team - i_begin) & (T - 1));
             if (i >= i_end) continue;
             // Q, each row brought to f16's upper range by a power of two (exact but for elements 2^-39 of the row's
-            // largest); f turns accumulated scores into base-2 exponents
+            // largest); f turns accumulated scores into base-2 exponents, and off takes INT8's bias out of them
             uint32_t qf[RT][8][2];
-            float f[RT][2], m[RT][2], l[RT][2];
+            float f[RT][2], off[RT][2], m[RT][2], l[RT][2];
             int p[RT][2];                                     // positions of the columns' rows
             float o[RT][8][4];
+            {
+                uint4 raw[RT][4];
 #pragma unroll
-            for (int n = 0; n < RT; ++n) {
-                const int c = col0 + 8 * n + g;
-                uint4 raw[4];
+                for (int n = 0; n < RT; ++n) {
+                    const int c = col0 + 8 * n + g;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) raw[e] = make_uint4(0u, 0u, 0u, 0u);
-                if (c < cols_used && col_row[c] < live) {
-                    const uint4* src = reinterpret_cast<const uint4*>(
-                        a.q + (((size_t)b * a.n_rows + col_row[c]) * heads + h * a.group + col_head[c]) * kD + 16 * j);
-                    raw[0] = __ldg(src);
-                    raw[1] = __ldg(src + 1);
-                    raw[2] = __ldg(src + 8);
-                    raw[3] = __ldg(src + 9);
+                    for (int e = 0; e < 4; ++e) raw[n][e] = make_uint4(0u, 0u, 0u, 0u);
+                    if (c < cols_used && col_row[c] < live) {
+                        const uint4* src = reinterpret_cast<const uint4*>(
+                            a.q + (((size_t)b * a.n_rows + col_row[c]) * heads + h * a.group + col_head[c]) * kD + 16 * j);
+                        raw[n][0] = __ldg(src);
+                        raw[n][1] = __ldg(src + 1);
+                        raw[n][2] = __ldg(src + 8);
+                        raw[n][3] = __ldg(src + 9);
+                    }
                 }
-                const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
-                uint32_t top = 0;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int up = min(max(268 - (int)(top >> 7), 1), 253);
-                const float by = __uint_as_float((uint32_t)up << 23);
-                const float back = __uint_as_float((uint32_t)(254 - up) << 23) * a.scale_log2;
+                for (int n = 0; n < RT; ++n) {
+                    const uint32_t* w = reinterpret_cast<const uint32_t*>(raw[n]);
+                    uint32_t top = 0;
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
+                    for (int e = 0; e < 16; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const int up = min(max(268 - (int)(top >> 7), 1), 253);
+                    const float by = __uint_as_float((uint32_t)up << 23);
+                    const float back = __uint_as_float((uint32_t)(254 - up) << 23) * a.scale_log2;
+                    float sum = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t v = w[2 * s + e];
-                        qf[n][s][e] = pack_f16(__uint_as_float(v << 16) * by, __uint_as_float(v & 0xFFFF0000u) * by);
+                    for (int s = 0; s < 8; ++s)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t v = w[2 * s + e];
+                            qf[n][s][e] = pack_f16(__uint_as_float(v << 16) * by, __uint_as_float(v & 0xFFFF0000u) * by);
+                            if (kInt8) {
+                                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&qf[n][s][e]));
+                                sum += x.x + x.y;
+                            }
+                        }
+                    if (kInt8) {
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                     }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    f[n][e] = __shfl_sync(0xffffffffu, back, (2 * j + e) * 4);
-                    m[n][e] = -INFINITY;
-                    l[n][e] = 0.0f;
-                    p[n][e] = len - live + min((int)col_row[min(col0 + 8 * n + 2 * j + e, kMaxCols - 1)], live - 1);
+                    for (int e = 0; e < 2; ++e) {
+                        f[n][e] = __shfl_sync(0xffffffffu, back, (2 * j + e) * 4);
+                        off[n][e] = kInt8 ? 1152.0f * __shfl_sync(0xffffffffu, sum, (2 * j + e) * 4) : 0.0f;
+                        m[n][e] = kNoScore;
+                        l[n][e] = 0.0f;
+                        p[n][e] = len - live + min((int)col_row[min(col0 + 8 * n + 2 * j + e, kMaxCols - 1)], live - 1);
+                    }
+#pragma unroll
+                    for (int d = 0; d < 8; ++d)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][d][e] = 0.0f;
                 }
-#pragma unroll
-                for (int d = 0; d < 8; ++d)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[n][d][e] = 0.0f;
             }
             float R = 0.0f, inv_r = 0.0f;
             for (; i < i_end; i += T) {
@@ -504,24 +529,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                     const uint32_t wa[4] = {ra[k].x, ra[k].y, ra[k].z, ra[k].w};
                                     const uint32_t wb[4] = {rb[k].x, rb[k].y, rb[k].z, rb[k].w};
                                     uint32_t a0, a1, a2, a3;
-                                    widen<kInt8>(wa[w], a0, a2);
-                                    widen<kInt8>(wb[w], a1, a3);
+                                    widen<kInt8, true>(wa[w], a0, a2);
+                                    widen<kInt8, true>(wb[w], a1, a3);
 #pragma unroll
                                     for (int n = 0; n < RT; ++n)
                                         mma_f16(s[k][n], a0, a1, a2, a3, qf[n][4 * u + w][0], qf[n][4 * u + w][1]);
                                 }
                         }
-                        // exponents and masks; is some score over its column's reference by more than kLazy?
+                        // exponents y = t - m + kShift and masks; a column without a score yet counts from 0 and
+                        // gets its reference now, another one when a score has passed the old one by kLazy
                         bool raise = false;
+                        float top[RT][2];
 #pragma unroll
                         for (int n = 0; n < RT; ++n)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                float top = -INFINITY;
+                                const float z = kShift - (m[n][e] == kNoScore ? 0.0f : m[n][e]);
+                                top[n][e] = -INFINITY;
 #pragma unroll
                                 for (int k = 0; k < KB; ++k) {
-                                    const float fk = f[n][e] * sc[k0 + k];
-                                    float x0 = s[k][n][e] * fk, x1 = s[k][n][2 + e] * fk;
+                                    const float fk = f[n][e] * sc[k0 + k], zk = kInt8 ? fmaf(-off[n][e], fk, z) : z;
+                                    float x0 = fmaf(s[k][n][e], fk, zk), x1 = fmaf(s[k][n][2 + e], fk, zk);
                                     if (edge) {
                                         const int key = key0 + (k0 + k) * kBlock + kperm;
                                         const int lo = a.window > 0 ? p[n][e] - a.window : -1;
@@ -530,24 +558,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                     }
                                     s[k][n][e] = x0;
                                     s[k][n][2 + e] = x1;
-                                    top = fmaxf(top, fmaxf(x0, x1));
+                                    top[n][e] = fmaxf(top[n][e], fmaxf(x0, x1));
                                 }
-                                raise = raise || top - m[n][e] > kLazy;
+                                raise = raise || top[n][e] > (m[n][e] == kNoScore ? -INFINITY : kShift + kLazy);
                             }
                         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                             for (int n = 0; n < RT; ++n)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    float now = m[n][e];
-#pragma unroll
-                                    for (int k = 0; k < KB; ++k) now = fmaxf(now, fmaxf(s[k][n][e], s[k][n][2 + e]));
+                                    float now = top[n][e];
                                     now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 4));
                                     now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 8));
                                     now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 16));
-                                    const float by = m[n][e] == -INFINITY ? 0.0f : ptx::ex2(m[n][e] - now);
-                                    m[n][e] = now;
+                                    const bool none_yet = m[n][e] == kNoScore;
+                                    const float up = now == -INFINITY ? 0.0f : (none_yet ? now - kShift : fmaxf(now - kShift, 0.0f));
+                                    if (now > -INFINITY) m[n][e] = (none_yet ? 0.0f : m[n][e]) + up;
+                                    const float by = none_yet ? 1.0f : ptx::ex2(-up);      // (sums of nothing are 0)
                                     l[n][e] *= by;
+#pragma unroll
+                                    for (int k = 0; k < KB; ++k) {
+                                        s[k][n][e] -= up;
+                                        s[k][n][2 + e] -= up;
+                                    }
 #pragma unroll
                                     for (int d = 0; d < 8; ++d) {
                                         o[n][d][e] *= by;
@@ -558,14 +591,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         // weights
                         uint32_t pf[KB][RT][2];
 #pragma unroll
-                        for (int n = 0; n < RT; ++n) {
-                            const float z0 = (m[n][0] == -INFINITY ? 0.0f : m[n][0]) - kShift;
-                            const float z1 = (m[n][1] == -INFINITY ? 0.0f : m[n][1]) - kShift;
+                        for (int k = 0; k < KB; ++k) {
+                            const float r = vs[k] * inv_r;
 #pragma unroll
-                            for (int k = 0; k < KB; ++k) {
-                                const float r = vs[k] * inv_r;
-                                const float p0 = ptx::ex2(s[k][n][0] - z0), p1 = ptx::ex2(s[k][n][1] - z1);
-                                const float p2 = ptx::ex2(s[k][n][2] - z0), p3 = ptx::ex2(s[k][n][3] - z1);
+                            for (int n = 0; n < RT; ++n) {
+                                const float p0 = ptx::ex2(s[k][n][0]), p1 = ptx::ex2(s[k][n][1]);
+                                const float p2 = ptx::ex2(s[k][n][2]), p3 = ptx::ex2(s[k][n][3]);
                                 l[n][0] += p0 + p2;
                                 l[n][1] += p1 + p3;
                                 pf[k][n][0] = transpose8(pack_f16(p0 * r, p1 * r));
@@ -594,13 +625,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             for (int w = 0; w < 4; ++w) {
                                 // dimensions 4 w, 4 w + 1 of the even and odd keys side by side, then 4 w + 2, 4 w + 3
                                 uint32_t a0, a1, a2, a3;
-                                widen<kInt8>(__byte_perm(u0[w], u1[w], 0x5140), a0, a1);
-                                widen<kInt8>(__byte_perm(u2[w], u3[w], 0x5140), a2, a3);
+                                widen<kInt8, false>(__byte_perm(u0[w], u1[w], 0x5140), a0, a1);
+                                widen<kInt8, false>(__byte_perm(u2[w], u3[w], 0x5140), a2, a3);
 #pragma unroll
                                 for (int n = 0; n < RT; ++n)
                                     mma_f16(o[n][2 * w], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
-                                widen<kInt8>(__byte_perm(u0[w], u1[w], 0x7362), a0, a1);
-                                widen<kInt8>(__byte_perm(u2[w], u3[w], 0x7362), a2, a3);
+                                widen<kInt8, false>(__byte_perm(u0[w], u1[w], 0x7362), a0, a1);
+                                widen<kInt8, false>(__byte_perm(u2[w], u3[w], 0x7362), a2, a3);
 #pragma unroll
                                 for (int n = 0; n < RT; ++n)
                                     mma_f16(o[n][2 * w + 1], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
@@ -612,10 +643,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(empty0 + 8 * st);
             }
             if (given_up) break;
-            // -------------------------------------------------------- sums of the segment
-            const int active = min(T, seg_len) * KG, n_cols = min(kCols, live * a.group - col0);
-            if (uses > 0 && !warp_wait(free0 + 8 * warp, (uses - 1) & 1, abort, status)) break;
-            ++uses;
+            // -------------------------------------------------------- sums of the segment, into the warp's slot
+            const int active = min(T, seg_len) * KG;              // warps that have a part of it (for each rg)
+            if (slot_use == 1 && !warp_wait(free0 + 8 * warp, (uses - 1) & 1, abort, status)) break;
+            if (slot_use == 2 && !warp_wait(joined, (joins - 1) & 1, abort, status)) break;
 #pragma unroll
             for (int n = 0; n < RT; ++n)
 #pragma unroll
@@ -625,40 +656,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                     const int c = 8 * n + 2 * j + e;
-                    if (g == 0) my_ml[c] = make_float2(m[n][e] - kShift, sum);
+                    if (g == 0) my_ml[c] = make_float2(m[n][e] == kNoScore ? -INFINITY : m[n][e] - kShift, sum);
                     // dimensions 16 g .. 16 g + 15 of pair c: the lane's eight accumulator pairs in order
                     float4* dst = reinterpret_cast<float4*>(slot + c * kD);
-                    const float by = R;
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
-                        dst[4 * g + (w ^ j)] = make_float4(o[n][2 * w][e] * by, o[n][2 * w][2 + e] * by,
-                                                           o[n][2 * w + 1][e] * by, o[n][2 * w + 1][2 + e] * by);
+                        dst[4 * g + (w ^ j)] = make_float4(o[n][2 * w][e] * R, o[n][2 * w][2 + e] * R, o[n][2 * w + 1][e] * R,
+                                                           o[n][2 * w + 1][2 + e] * R);
                 }
-            int last = 1;
-            __threadfence_block();
-            __syncwarp();
-            if (active > 1) {
-                if (lane == 0) {
-                    int* ticket = tickets + rg * kTickets + (seg & (kTickets - 1));
-                    last = atomicAdd(ticket, 1) == active - 1;
-                    if (last) *ticket = 0;
-                }
-                last = __shfl_sync(0xffffffffu, last, 0);
-                if (!last) continue;
-                __threadfence_block();
-                __syncwarp();
-            }
-            // -------------------------------------------------------- the last warp of the segment joins them
-            // (loops, not unrolled code: this runs once or twice in a CTA, from a cold instruction cache)
-            // weights: eight lanes a pair, one for each active warp, in the order of tiles
-            auto warp_of = [&](int t) { return ((((i_begin & (T - 1)) + t / KG) & (T - 1)) * KG + t % KG) * RG + rg; };
-            const size_t part = (size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + col0;
-            float* by = weights + warp * kCols * 8;
-#pragma unroll 1
-            for (int c = lane >> 3; c < kCols; c += 4) {
-                const int t = lane & 7;
+            // Column c of row group r: the sum over the active warps, in the order of their tiles, to the output if the
+            // segment is the whole head, else to this CTA's part of it.
+            auto join = [&](int r, int c) {
+                auto warp_of = [&](int t) { return ((((i_begin & (T - 1)) + t / KG) & (T - 1)) * KG + t % KG) * RG + r; };
+                const int col = r * kCols + c, chunk = (lane & ~3) | ((lane & 3) ^ ((c >> 1) & 3)), t_mine = lane & 7;
                 float2 ml = make_float2(-INFINITY, 0.0f);
-                if (t < active) ml = slot_ml[warp_of(t) * kCols + c];
+                if (t_mine < active) ml = slot_ml[warp_of(t_mine) * kCols + c];
+                float4 v[8];
+#pragma unroll
+                for (int t = 0; t < T * KG; ++t)
+                    if (t < active)
+                        v[t] = reinterpret_cast<const float4*>(slots + (size_t)warp_of(t) * S::kSlotFloats + c * kD)[chunk];
                 float top = ml.x;
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -668,42 +685,65 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                if (c < n_cols) {
-                    if (whole) {     // the output: normalised, with the sink
-                        const int row = col_row[col0 + c], head = h * a.group + col_head[col0 + c];
-                        const Finish fin = finish(top, sum, a.sink, head);
-                        one *= fin.by;
-                        if (t == 0 && a.out_lse) a.out_lse[((size_t)b * a.n_rows + row) * heads + head] = fin.lse;
-                    } else if (t == 0) {
-                        a.part_ml[part + c] = make_float2(top, sum);
-                    }
-                }
-                by[c * 8 + t] = one;
-            }
-            __syncwarp();
-#pragma unroll 1
-            for (int c = 0; c < n_cols; ++c) {
-                const int chunk = (lane & ~3) | ((lane & 3) ^ ((c >> 1) & 3));
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                for (int t = 0; t < active; ++t) {
-                    const int w = warp_of(t);
-                    const float one = by[c * 8 + t];
-                    const float4 v = reinterpret_cast<const float4*>(slots + (size_t)w * S::kSlotFloats + c * kD)[chunk];
-                    acc.x += one * v.x;
-                    acc.y += one * v.y;
-                    acc.z += one * v.z;
-                    acc.w += one * v.w;
-                }
+                const size_t part = (size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + col;
+                const int head = h * a.group + col_head[col];
+                const size_t row = ((size_t)b * a.n_rows + col_row[col]) * heads + head;
                 if (whole) {
-                    const size_t row = ((size_t)b * a.n_rows + col_row[col0 + c]) * heads + h * a.group + col_head[col0 + c];
-                    store_row(a.out + row * kD + 4 * lane, acc);
-                } else {
-                    reinterpret_cast<float4*>(a.part_o + (part + c) * kD)[lane] = acc;
+                    const Finish fin = finish(top, sum, a.sink, head);
+                    one *= fin.by;
+                    if (lane == 0 && a.out_lse) a.out_lse[row] = fin.lse;
+                } else if (lane == 0) {
+                    a.part_ml[part] = make_float2(top, sum);
                 }
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int t = 0; t < T * KG; ++t)
+                    if (t < active) {
+                        const float w = __shfl_sync(0xffffffffu, one, t);
+                        acc.x += w * v[t].x;
+                        acc.y += w * v[t].y;
+                        acc.z += w * v[t].z;
+                        acc.w += w * v[t].w;
+                    }
+                if (whole) store_row(a.out + row * kD + 4 * lane, acc);
+                else reinterpret_cast<float4*>(a.part_o + part * kD)[lane] = acc;
+            };
+            // (rolled loops: this runs a few times in a CTA, from a cold instruction cache)
+            if (seg_len >= T) {
+                // every warp has a part: they meet, and share the columns
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(filled);
+                if (!warp_wait(filled, joins & 1, abort, status)) break;
+#pragma unroll 1
+                for (int q = warp; q < RG * kCols; q += kConsumers)
+                    if (q < cols_used && col_row[q] < live) join(q / kCols, q % kCols);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(joined);
+                ++joins;
+                slot_use = 2;
+            } else {
+                // the last of the active warps joins their columns; the others go on
+                int last = 1;
+                __threadfence_block();
+                __syncwarp();
+                if (lane == 0) {
+                    int* ticket = tickets + rg * kTickets + (seg & (kTickets - 1));
+                    last = atomicAdd(ticket, 1) == active - 1;
+                    if (last) *ticket = 0;
+                }
+                last = __shfl_sync(0xffffffffu, last, 0);
+                ++uses;
+                slot_use = 1;
+                if (!last) continue;
+                __threadfence_block();
+                __syncwarp();
+#pragma unroll 1
+                for (int c = 0; c < kCols; ++c)
+                    if (col0 + c < cols_used && col_row[col0 + c] < live) join(rg, c);
+                __syncwarp();
+                if (lane < active)
+                    ptx::mbar_arrive(free0 + 8 * (((((i_begin & (T - 1)) + lane / KG) & (T - 1)) * KG + lane % KG) * RG + rg));
             }
-            __syncwarp();
-            if (lane < active) ptx::mbar_arrive(free0 + 8 * warp_of(lane));
         }
     }
     if (status && a.dev_status) atomicOr(a.dev_status, status);
