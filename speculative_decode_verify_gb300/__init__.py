@@ -57,6 +57,8 @@ def lib_path(variant: str = "") -> str:
 
 def lib(variant: str = "") -> ctypes.CDLL:
     """The loaded CUDA library (built by ``speculative_decode_verify_gb300.build``)."""
+    if variant in _lib:
+        return _lib[variant]
     with _lock:
         if variant in _lib:
             return _lib[variant]
@@ -323,52 +325,78 @@ def verify_attn_q8_step(q, k_new, v_new, n_live: int, k_codes, v_codes, k_scale,
 
 
 # ----------------------------------------------------------------------------- paged 8-bit cache of many sequences
-def _addr(*tensors):
-    """Addresses of dense tensors (None: a null pointer); the C ABI takes no strides."""
-    for t in tensors:
-        if t is not None and not t.is_contiguous():
-            raise ValueError("the paged cache's calls take contiguous tensors")
-    return [None if t is None else t.data_ptr() for t in tensors]
-
-
+# (these calls are made many times a step: the checks below look at each tensor once and do little else)
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
 
 
+def _at(t, count: int, size: int, what: str) -> int:
+    """Address of a dense tensor of `count` elements of `size` bytes (the C ABI takes no strides)."""
+    if t.numel() != count or t.itemsize != size or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous tensor of {count} elements of {size} bytes")
+    return t.data_ptr()
+
+
+def _bytes(t):
+    if not t.is_contiguous():
+        raise ValueError("the workspace: a contiguous tensor")
+    return t.data_ptr(), t.numel() * t.itemsize
+
+
+def _opt(t, count: int, size: int, what: str):
+    return None if t is None else _at(t, count, size, what)
+
+
+def _launch(fn: str, call, t, stream, *args) -> None:
+    """Call an entry point on the stream given, or on the current one of t's device, with that device current."""
+    import torch
+    index = t.get_device()
+    if index >= 0 and index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            status = call(*args, _stream(stream))
+    elif stream is None and index >= 0:
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        status = call(*args, _stream(stream))
+    if status != VA_OK:
+        raise VerifyAttnError(fn, status)
+
+
 def _pool(k_codes, v_codes, k_scale, v_scale):
-    """(layers, pages, kv heads, format, addresses) of pools [pages, heads, 64, 128] or [layers, pages, ...]."""
-    shape = k_codes.shape
-    _need(len(shape) in (4, 5) and shape[-2] == TILE and shape[-1] == HEAD_DIM and v_codes.shape == shape
-          and k_codes.dtype == v_codes.dtype and k_codes.element_size() == 1,
-          "codes are [..., pages, heads, 64, 128] of one 8-bit type")
-    want = (*shape[:-2], TILE // B8_BLOCK)
-    _need(tuple(k_scale.shape) == want and tuple(v_scale.shape) == want and k_scale.element_size() == 4
-          and v_scale.element_size() == 4, "scales are float32 [..., pages, heads, 4]")
-    fmt = B8_INT8 if str(k_codes.dtype) == "torch.int8" else B8_E4M3
-    return (1 if len(shape) == 4 else int(shape[0]), int(shape[-4]), int(shape[-3]), fmt,
-            _addr(k_codes, v_codes, k_scale, v_scale))
+    """(layers, pages, kv heads, format, four addresses) of pools [pages, heads, 64, 128] or [layers, pages, ...]."""
+    import torch
+    *outer, heads, page, d = k_codes.shape
+    if not (len(outer) in (1, 2) and page == TILE and d == HEAD_DIM and v_codes.shape == k_codes.shape
+            and v_codes.dtype is k_codes.dtype and k_scale.shape == v_scale.shape
+            and tuple(k_scale.shape) == (*outer, heads, TILE // B8_BLOCK)):
+        raise ValueError("pools are codes [..., pages, heads, 64, 128] of one 8-bit type and scales [..., pages, heads, 4]")
+    n, ns = k_codes.numel(), k_scale.numel()
+    return (outer[0] if len(outer) == 2 else 1, outer[-1], heads, B8_INT8 if k_codes.dtype is torch.int8 else B8_E4M3,
+            _at(k_codes, n, 1, "codes"), _at(v_codes, n, 1, "codes"), _at(k_scale, ns, 4, "scales"),
+            _at(v_scale, ns, 4, "scales"))
 
 
-def _counts(n: int, what: str, *tensors):
-    for t in tensors:
-        _need(t.numel() == n and t.element_size() == 4, what)
+def _table(table, n: int):
+    if table.dim() != 2 or table.shape[0] != n:
+        raise ValueError("the table is int32 [n_seqs, max_pages]")
+    width = table.shape[1]
+    return width, _at(table, n * width, 4, "the table")
 
 
 def kv_page_append_b8(k_new, v_new, n_live, lens, table, k_codes, v_codes, k_scale, v_scale, dev_status=None,
                       stream=None, variant: str = "") -> None:
     """Code the live rows' K/V ([n_seqs, n_rows, n_kv_heads, 128] bf16) into the sequences' pages.  The pool's
     format goes by its dtype: int8, or E4M3 (float8_e4m3fn or uint8)."""
-    layers, pages, heads, fmt, pool = _pool(k_codes, v_codes, k_scale, v_scale)
-    n, rows = int(k_new.shape[0]), int(k_new.shape[1])
-    _need(layers == 1 and k_new.shape == v_new.shape and tuple(k_new.shape) == (n, rows, heads, HEAD_DIM)
-          and k_new.element_size() == 2 and v_new.element_size() == 2, "new rows are [n_seqs, n_rows, n_kv_heads, 128]")
-    _need(table.dim() == 2 and table.shape[0] == n and table.element_size() == 4, "the table is int32 [n_seqs, max_pages]")
-    _counts(n, "one int32 a sequence", n_live, lens)
-    kn, vn, live, ln, tb, ds = _addr(k_new, v_new, n_live, lens, table, dev_status)
-    st = lib(variant).kv_page_append_b8(kn, vn, n, rows, heads, live, ln, tb, int(table.shape[1]), *pool, pages, fmt, ds,
-                                        _stream(stream))
-    _check("kv_page_append_b8", st)
+    layers, pages, heads, fmt, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
+    n, rows, h, d = k_new.shape
+    _need(layers == 1 and h == heads and d == HEAD_DIM and v_new.shape == k_new.shape,
+          "new rows are [n_seqs, n_rows, n_kv_heads, 128], the pool one layer's")
+    width, tb = _table(table, n)
+    count = n * rows * heads * HEAD_DIM
+    _launch("kv_page_append_b8", lib(variant).kv_page_append_b8, k_codes, stream, _at(k_new, count, 2, "k_new"),
+            _at(v_new, count, 2, "v_new"), n, rows, heads, _at(n_live, n, 4, "n_live"), _at(lens, n, 4, "lens"), tb, width,
+            kc, vc, ks, vs, pages, fmt, _opt(dev_status, 1, 4, "dev_status"))
 
 
 def va_paged_workspace_bytes(n_seqs: int, n_rows: int, n_kv_heads: int, group: int) -> int:
@@ -380,21 +408,17 @@ def verify_attn_paged_b8(q, n_live, lens, table, k_codes, v_codes, k_scale, v_sc
     """Verify attention of every sequence's live rows (q [n_seqs, n_rows, heads, 128] bf16) over its pages; writes
     out (as q) and out_lse [n_seqs, n_rows, heads].  ``workspace``: a device byte tensor of
     va_paged_workspace_bytes(...) bytes, zeroed once."""
-    layers, pages, kv, fmt, pool = _pool(k_codes, v_codes, k_scale, v_scale)
-    n, rows, heads, d = (int(x) for x in q.shape)
-    _need(layers == 1 and d == HEAD_DIM and heads % kv == 0 and out.shape == q.shape and q.element_size() == 2
-          and out.element_size() == 2, "q and out are [n_seqs, n_rows, n_kv_heads * group, 128] bf16")
-    _need(table.dim() == 2 and table.shape[0] == n and table.element_size() == 4, "the table is int32 [n_seqs, max_pages]")
-    _counts(n, "one int32 a sequence", n_live, lens)
-    if sink is not None:
-        _counts(heads, "one float32 sink a query head", sink)
-    if out_lse is not None:
-        _counts(n * rows * heads, "out_lse is float32 [n_seqs, n_rows, heads]", out_lse)
-    qa, live, ln, tb, sk, ws, o, lse, ds = _addr(q, n_live, lens, table, sink, workspace, out, out_lse, dev_status)
-    st = lib(variant).verify_attn_paged_b8(qa, n, rows, kv, heads // kv, live, ln, tb, int(table.shape[1]), *pool, pages,
-                                           fmt, int(window), float(scale), sk, ws,
-                                           workspace.numel() * workspace.element_size(), o, lse, ds, _stream(stream))
-    _check("verify_attn_paged_b8", st)
+    layers, pages, kv, fmt, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
+    n, rows, heads, d = q.shape
+    _need(layers == 1 and d == HEAD_DIM and heads % kv == 0 and out.shape == q.shape,
+          "q and out are [n_seqs, n_rows, n_kv_heads * group, 128], the pool one layer's")
+    width, tb = _table(table, n)
+    pairs = n * rows * heads
+    ws, size = _bytes(workspace)
+    _launch("verify_attn_paged_b8", lib(variant).verify_attn_paged_b8, k_codes, stream, _at(q, pairs * HEAD_DIM, 2, "q"), n,
+            rows, kv, heads // kv, _at(n_live, n, 4, "n_live"), _at(lens, n, 4, "lens"), tb, width, kc, vc, ks, vs, pages,
+            fmt, int(window), float(scale), _opt(sink, heads, 4, "sink"), ws, size, _at(out, pairs * HEAD_DIM, 2, "out"),
+            _opt(out_lse, pairs, 4, "out_lse"), _opt(dev_status, 1, 4, "dev_status"))
 
 
 def va_page_ops_workspace_bytes(n_seqs: int, max_pages: int, n_pages: int) -> int:
@@ -405,44 +429,41 @@ def kv_page_extend(table, lens, n_new, refs, k_codes, v_codes, k_scale, v_scale,
                    variant: str = "") -> None:
     """Pages for n_new[b] more tokens of every sequence (copy on write); lens grows by n_new.  Pools of all layers:
     [layers, pages, heads, 64, 128]."""
-    layers, pages, heads, _, pool = _pool(k_codes, v_codes, k_scale, v_scale)
-    n, width = (int(x) for x in table.shape)
-    _counts(n, "one int32 a sequence", lens, n_new)
-    _counts(pages, "one int32 reference count a page", refs)
-    tb, ln, new, rf, ws, ds = _addr(table, lens, n_new, refs, workspace, dev_status)
-    st = lib(variant).kv_page_extend(tb, ln, new, n, width, rf, pages, layers, heads, *pool, ws,
-                                     workspace.numel() * workspace.element_size(), ds, _stream(stream))
-    _check("kv_page_extend", st)
+    layers, pages, heads, _, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
+    n = table.shape[0]
+    width, tb = _table(table, n)
+    ws, size = _bytes(workspace)
+    _launch("kv_page_extend", lib(variant).kv_page_extend, k_codes, stream, tb, _at(lens, n, 4, "lens"),
+            _at(n_new, n, 4, "n_new"), n, width, _at(refs, pages, 4, "refs"), pages, layers, heads, kc, vc, ks, vs, ws, size,
+            _opt(dev_status, 1, 4, "dev_status"))
 
 
 def kv_page_reorder(table, lens, src, refs, group: int = 0, dev_status=None, stream=None, variant: str = "") -> None:
     """Slot j takes the sequence of slot src[j] of its group (j: kept, another: forked, -1: freed)."""
-    n, width = (int(x) for x in table.shape)
-    _counts(n, "one int32 a sequence", lens, src)
-    tb, ln, s, rf, ds = _addr(table, lens, src, refs, dev_status)
-    st = lib(variant).kv_page_reorder(tb, ln, n, width, s, int(group), rf, int(refs.numel()), ds, _stream(stream))
-    _check("kv_page_reorder", st)
+    n, pages = table.shape[0], refs.numel()
+    width, tb = _table(table, n)
+    _launch("kv_page_reorder", lib(variant).kv_page_reorder, table, stream, tb, _at(lens, n, 4, "lens"), n, width,
+            _at(src, n, 4, "src"), int(group), _at(refs, pages, 4, "refs"), pages, _opt(dev_status, 1, 4, "dev_status"))
 
 
 def kv_page_copy(src, dst, k_codes, v_codes, k_scale, v_scale, dev_status=None, stream=None, variant: str = "") -> None:
     """Page dst[i] becomes a copy of page src[i], in all layers."""
-    layers, pages, heads, _, pool = _pool(k_codes, v_codes, k_scale, v_scale)
-    _counts(int(src.numel()), "as many destinations as sources, int32", src, dst)
-    s, d, ds = _addr(src, dst, dev_status)
-    st = lib(variant).kv_page_copy(s, d, int(src.numel()), pages, layers, heads, *pool, ds, _stream(stream))
-    _check("kv_page_copy", st)
+    layers, pages, heads, _, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
+    n = src.numel()
+    _launch("kv_page_copy", lib(variant).kv_page_copy, k_codes, stream, _at(src, n, 4, "src"), _at(dst, n, 4, "dst"), n,
+            pages, layers, heads, kc, vc, ks, vs, _opt(dev_status, 1, 4, "dev_status"))
 
 
 def kv_page_compact(table, refs, k_codes, v_codes, k_scale, v_scale, moved_to, n_live_pages, workspace, dev_status=None,
                     stream=None, variant: str = "") -> None:
     """Move the live pages to the lowest numbers; moved_to [pages] tells where, n_live_pages [1] how many there are."""
-    layers, pages, heads, _, pool = _pool(k_codes, v_codes, k_scale, v_scale)
-    n, width = (int(x) for x in table.shape)
-    _counts(pages, "one int32 a page", refs, moved_to)
-    tb, rf, mv, nl, ws, ds = _addr(table, refs, moved_to, n_live_pages, workspace, dev_status)
-    st = lib(variant).kv_page_compact(tb, n, width, rf, pages, layers, heads, *pool, mv, nl, ws,
-                                      workspace.numel() * workspace.element_size(), ds, _stream(stream))
-    _check("kv_page_compact", st)
+    layers, pages, heads, _, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
+    n = table.shape[0]
+    width, tb = _table(table, n)
+    ws, size = _bytes(workspace)
+    _launch("kv_page_compact", lib(variant).kv_page_compact, k_codes, stream, tb, n, width, _at(refs, pages, 4, "refs"),
+            pages, layers, heads, kc, vc, ks, vs, _at(moved_to, pages, 4, "moved_to"), _at(n_live_pages, 1, 4, "n_live_pages"),
+            ws, size, _opt(dev_status, 1, 4, "dev_status"))
 
 
 # ----------------------------------------------------------------------------- beam search
@@ -455,17 +476,18 @@ def va_beam_select(logits, scores, n_beams: int, parents, tokens, out_scores, wo
     """The best n_out continuations of each request's n_beams hypotheses: logits [n_groups * n_beams, vocab] (float32
     or bfloat16, rows at any stride that keeps them 16-byte aligned), scores [n_groups * n_beams]; writes parents,
     tokens and out_scores [n_groups, n_out].  ``workspace``: va_beam_workspace_bytes(...) bytes, zeroed once."""
-    rows, vocab = (int(x) for x in logits.shape)
-    groups, n_out = (int(x) for x in parents.shape)
-    _need(groups * int(n_beams) == rows and (vocab == 1 or logits.stride(1) == 1)
-          and str(logits.dtype) in ("torch.float32", "torch.bfloat16"), "logits are [n_groups * n_beams, vocab]")
-    _counts(rows, "one score (and flag) a hypothesis", scores, *([] if finished is None else [finished]))
-    _counts(groups * n_out, "outputs are [n_groups, n_out]", parents, tokens, out_scores)
-    sc, fin, pa, tk, os_, ws = _addr(scores, finished, parents, tokens, out_scores, workspace)
-    st = lib(variant).va_beam_select(logits.data_ptr(), 0 if logits.element_size() == 4 else 1, int(logits.stride(0)),
-                                     groups, int(n_beams), vocab, sc, fin, int(end_token), n_out, pa, tk, os_, ws,
-                                     workspace.numel() * workspace.element_size(), _stream(stream))
-    _check("va_beam_select", st)
+    import torch
+    rows, vocab = logits.shape
+    groups, n_out = parents.shape
+    stride, inner = logits.stride()
+    bf16 = logits.dtype is torch.bfloat16
+    _need(groups * n_beams == rows and (vocab == 1 or inner == 1) and (bf16 or logits.dtype is torch.float32),
+          "logits are float32 or bfloat16 [n_groups * n_beams, vocab]")
+    count = groups * n_out
+    ws, size = _bytes(workspace)
+    _launch("va_beam_select", lib(variant).va_beam_select, logits, stream, logits.data_ptr(), 1 if bf16 else 0, stride, groups,
+            int(n_beams), vocab, _at(scores, rows, 4, "scores"), _opt(finished, rows, 4, "finished"), int(end_token), n_out,
+            _at(parents, count, 4, "parents"), _at(tokens, count, 4, "tokens"), _at(out_scores, count, 4, "out_scores"), ws, size)
 
 
 # ----------------------------------------------------------------------------- self-test

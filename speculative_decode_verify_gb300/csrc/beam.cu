@@ -1,13 +1,15 @@
 // va_beam_select: beam search's selection over beams and vocabulary.
 //
 // One launch, three levels.  A CTA per (8,192-logit tile, row) reads its logits once: it forms the tile's maximum
-// m and sum of exp(l - m) and collects the tile's k best keys as the sampler does.  The last CTA of a row to
+// m and sum of exp(l - m) and collects the tile's k best keys as the sampler does, but forms keys only of the few
+// logits at or above a bound (a 64-bit key of every logit took ten times the loads: 117 us for 32 x 8 x 151,669).  The last CTA of a row to
 // arrive merges the tiles: log-sum-exp in 64 bits from the tiles' (m, sum), the row's k best keys, and their
 // scores in 64 bits.  The last row of a request to arrive merges the hypotheses.  Every order is fixed by the
 // keys, so the arrivals' order changes nothing.
 // Bytes: the logits once; what a tile hands on (k keys) is 1/1000 of that.
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -31,10 +33,9 @@ constexpr int kWarps = kThreads / 32;
 
 struct BeamSmem {
     uint64_t cand[kMaxMerge];   // tile: its candidates; row and request: the candidates that are ranked
-    uint64_t lists[kThreads];
     uint64_t red[kWarps];
     uint32_t wmin[kWarps];
-    float fred[kWarps];
+    float fred[kWarps], fsum[kWarps];
     uint64_t all[kMaxMerge];    // row: every tile's keys; request: every hypothesis' score keys
     int32_t tok[kMaxFinal];     // request: their tokens
     int16_t who[kMaxFinal];     // request: which candidate a ranked key is
@@ -85,7 +86,7 @@ __device__ __forceinline__ bool arrive_last(unsigned* counter, int n, int* flag)
 }
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs a) {
     __shared__ BeamSmem sm;
     constexpr int kVec = kBf16 ? 8 : 4, kBytes = kBf16 ? 2 : 4;   // logits per 16 bytes
     const int tile = blockIdx.x, row = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
                 raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-        float mx = -INFINITY;
+        float mine = -INFINITY;      // the thread's largest (NaN is passed over)
 #pragma unroll
         for (int i = 0; i < kPerThread / kVec; ++i) {
             const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -140,37 +141,109 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
                 const float x = kBf16 ? __uint_as_float((c & 1) ? (w[c / 2] & 0xFFFF0000u) : (w[c / 2] << 16))
                                       : __uint_as_float(w[c & 3]);
                 f[i * kVec + c] = x;
-                mx = fmaxf(mx, x);      // a NaN is passed over
+                mine = fmaxf(mine, x);
             }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (lane == 0) sm.fred[warp] = mx;
+        // The tile's maximum, and tau, a lower bound of its k-th largest logit: with f warps whose 32 threads all hold
+        // logits and j = ceil(k / f), the smallest over those warps of the warp's j-th largest distinct thread maximum
+        // (one warp-wide maximum a round).  Fewer than 32 threads of logits: every logit is a candidate.
+        const int full_warps = min(kThreads, (n_in + kVec - 1) / kVec) / 32;
+        const int rounds = full_warps > 0 ? (k + full_warps - 1) / full_warps : 1;
+        uint32_t v = ord_bits(mine), low = 0u;
+        for (int r = 0; r < rounds; ++r) {
+            low = __reduce_max_sync(0xffffffffu, v);
+            if (r == 0 && lane == 0) sm.fred[warp] = ord_to_float(low);
+            v = v == low ? 0u : v;
+        }
+        if (lane == 0) sm.wmin[warp] = warp < full_warps ? low : 0xFFFFFFFFu;
+        if (tid == 0) sm.n_cand = 0;
         __syncthreads();
-        mx = sm.fred[0];
+        float mx = sm.fred[0];
+        uint32_t tau_bits = sm.wmin[0];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sm.fred[w]);
-        float sum = 0.0f;
-        uint64_t key[kPerThread];
+        for (int w = 1; w < kWarps; ++w) {
+            mx = fmaxf(mx, sm.fred[w]);
+            tau_bits = min(tau_bits, sm.wmin[w]);
+        }
+        if (full_warps == 0) tau_bits = 0u;
+        // candidates are at or above tau and above -inf (tau_bits 0 and NaN's image: all that are above -inf)
+        const float tau = tau_bits > ord_bits(-INFINITY) ? ord_to_float(tau_bits) : -FLT_MAX;
+        // exp(l - mx) as 2^(l log2 e + off): within 2^-22 for the terms that weigh anything, but for the rounding of
+        // off, which all share and which is taken out of their sum.  (A maximum that is infinite or so large that
+        // off would not hold its digits: the difference first.)
+        const float l2e = 1.4426950408889634f;
+        const bool plain = fabsf(mx) < 1024.0f;
+        const float off = plain ? -mx * l2e : 0.0f, shared_error = plain ? fmaf(mx, l2e, off) : 0.0f;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        unsigned bits = 0;
+        if (plain) {
 #pragma unroll
-        for (int e = 0; e < kPerThread; ++e) {
-            const bool real = f[e] > -INFINITY;      // neither -inf nor NaN
-            if (real) sum += f[e] == mx ? 1.0f : expf(f[e] - mx);
-            key[e] = real ? make_key(f[e], first + ((e / kVec) * kThreads + tid) * kVec + e % kVec) : 0ull;
+            for (int e = 0; e < kPerThread; ++e)
+                if (f[e] == f[e]) sum[e & 3] += ptx::ex2(fmaf(f[e], l2e, off));
+        } else if (mx > -INFINITY) {
+#pragma unroll
+            for (int e = 0; e < kPerThread; ++e)
+                if (f[e] == f[e]) sum[e & 3] += f[e] == mx ? 1.0f : ptx::ex2((f[e] - mx) * l2e);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int e = 0; e < kPerThread; ++e) bits |= f[e] >= tau ? 1u << e : 0u;
+        float part = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        if (lane == 0) sm.fsum[warp] = part;
+        // compaction: a warp's candidates take consecutive places; their values are read again (few are)
+        const int cnt = __popc(bits);
+        int incl = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        int slot = 0;
+        if (lane == 31 && incl > 0) slot = atomicAdd(&sm.n_cand, incl);
+        slot = __shfl_sync(0xffffffffu, slot, 31) + incl - cnt;
+        for (unsigned rest = bits; rest != 0; rest &= rest - 1) {
+            const int e = __ffs(rest) - 1;
+            const int at = first + ((e / kVec) * kThreads + tid) * kVec + e % kVec;
+            const float x = kBf16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src)[at] << 16)
+                                  : reinterpret_cast<const float*>(src)[at];
+            if (slot < kMaxCand) sm.cand[slot] = make_key(x, at);
+            ++slot;
+        }
         __syncthreads();
-        if (lane == 0) sm.fred[warp] = sum;
-        __syncthreads();
+        const int n_cand = sm.n_cand;
         if (tid == 0) {
-            sum = 0.0f;
+            float all = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) sum += sm.fred[w];
-            a.tile_stats[(size_t)row * n_tiles + tile] = make_float2(mx, sum);
+            for (int w = 0; w < kWarps; ++w) all += sm.fsum[w];
+            a.tile_stats[(size_t)row * n_tiles + tile] = make_float2(mx, mx > -INFINITY ? fmaf(all, -0.69314718f * shared_error, all) : 0.0f);
         }
-        collect_tile(key, min(kThreads, (n_in + kVec - 1) / kVec) / 32, k, sm,
-                     a.tile_keys + ((size_t)row * n_tiles + tile) * k);
+        uint64_t* keys_out = a.tile_keys + ((size_t)row * n_tiles + tile) * k;
+        if (n_cand <= kMaxCand) {
+            // rank by counting: a candidate goes to the place of the number of larger ones, if that is below k
+            for (int c = tid; c < n_cand; c += kThreads) {
+                const uint64_t kc = sm.cand[c];
+                int rank = 0;
+#pragma unroll 8
+                for (int o = 0; o < n_cand; ++o) rank += sm.cand[o] > kc;
+                if (rank < k) keys_out[rank] = kc;
+            }
+            for (int r = n_cand + tid; r < k; r += kThreads) keys_out[r] = 0ull;
+        } else {
+            // many equal logits at the bound: k rounds of block-wide maximum over every logit
+            uint64_t taken = ~0ull;
+            for (int r = 0; r < k; ++r) {
+                uint64_t best = 0;
+#pragma unroll
+                for (int e = 0; e < kPerThread; ++e) {
+                    const uint64_t kv = f[e] > -INFINITY ? make_key(f[e], first + ((e / kVec) * kThreads + tid) * kVec + e % kVec) : 0ull;
+                    best = kv < taken && kv > best ? kv : best;
+                }
+                best = block_max_u64(best, sm.red);
+                if (tid == 0) keys_out[r] = best;
+                taken = best;
+            }
+        }
         if (!arrive_last(a.row_count + row, n_tiles, &sm.last)) return;
         // -------------------------------------------------------- row
         const uint64_t* rw = a.tile_keys + (size_t)row * n_tiles * k;
@@ -196,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
             float top = st.x;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            double s = st.x == -INFINITY ? 0.0 : (st.x == top ? (double)st.y : (double)st.y * exp((double)st.x - (double)top));
+            double s = st.x == -INFINITY ? 0.0 : (st.x == top ? (double)st.y : (double)(st.y * expf(st.x - top)));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             if (lane == 0) {

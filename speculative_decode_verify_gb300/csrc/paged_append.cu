@@ -23,28 +23,45 @@ struct AppendArgs {
     int n_seqs, n_rows, n_kv, max_pages, n_pages, n_blocks;   // n_blocks: most blocks that one sequence's rows touch
 };
 
-// Eight floats to eight codes, each rn(x / s) with one rounding of the quotient.
+// Eight quotients to eight codes.
 template <bool kInt8>
-__device__ __forceinline__ uint2 code8(const float (&x)[8], float s) {
+__device__ __forceinline__ uint2 round8(const float (&q)[8]) {
     uint32_t w[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        float q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = s > 0.0f ? __fdiv_rn(x[4 * h + i], s) : 0.0f;
         if (kInt8) {
             w[h] = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                w[h] |= ((uint32_t)__float2int_rn(fminf(fmaxf(q[i], -127.0f), 127.0f)) & 0xFFu) << (8 * i);
+                w[h] |= ((uint32_t)__float2int_rn(fminf(fmaxf(q[4 * h + i], -127.0f), 127.0f)) & 0xFFu) << (8 * i);
         } else {
             uint16_t lo, hi;
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(q[1]), "f"(q[0]));
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(q[3]), "f"(q[2]));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(q[4 * h + 1]), "f"(q[4 * h]));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(q[4 * h + 3]), "f"(q[4 * h + 2]));
             w[h] = (uint32_t)lo | ((uint32_t)hi << 16);
         }
     }
     return make_uint2(w[0], w[1]);
+}
+
+// Eight floats to the codes of their correctly rounded quotients x / s.  x (1 / s) is within three units of the
+// quotient's last place, so it has the quotient's code unless a value halfway between two codes is that near: such
+// values (and the codes themselves) have no more than eight leading bits in E4M3 and INT8, so that the last 15 of the
+// 23 tell.  Those eight are then divided (one in a thousand is).
+template <bool kInt8>
+__device__ __forceinline__ uint2 code8(const float (&x)[8], float s, float inv) {
+    float q[8];
+    uint32_t near = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        q[i] = x[i] * inv;
+        near = min(near, (__float_as_uint(q[i]) + 4u) & 0x7FFFu);
+    }
+    if (near < 8u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = s > 0.0f ? __fdiv_rn(x[i], s) : 0.0f;
+    }
+    return round8<kInt8>(q);
 }
 
 template <bool kInt8>
@@ -86,30 +103,35 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendA
                 if (p >= start && p < sq.len)
                     raw[r] = __ldcs(reinterpret_cast<const uint4*>(src + (size_t)(p - start) * a.n_kv * kD));
             }
-            // the block's largest finite magnitude; NaN becomes 0
+            // the block's largest magnitude, two elements at a time
             uint32_t top = 0;
-            bool odd = false;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                uint32_t* w = reinterpret_cast<uint32_t*>(&raw[r]);
+            for (int r = 0; r < 8; ++r)
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[r].x & 0x7FFF7FFFu, raw[r].y & 0x7FFF7FFFu),
+                                             __vmaxu2(raw[r].z & 0x7FFF7FFFu, raw[r].w & 0x7FFF7FFFu)));
+            top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xFFFFu));
+            if (top >= 0x7F80u) {
+                // an infinity or NaN somewhere: the largest finite one instead, and NaN becomes 0
+                status |= VA_DEV_NONFINITE;
+                top = 0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int r = 0; r < 8; ++r) {
+                    uint32_t* w = reinterpret_cast<uint32_t*>(&raw[r]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t m = (w[c] >> (16 * e)) & 0x7FFFu;
-                        if (m >= 0x7F80u) {
-                            odd = true;
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t m = (w[c] >> (16 * e)) & 0x7FFFu;
                             if (m > 0x7F80u) w[c] &= e ? 0x0000FFFFu : 0xFFFF0000u;
-                        } else {
-                            top = max(top, m);
+                            if (m < 0x7F80u) top = max(top, m);
                         }
-                    }
                 }
+                top = __reduce_max_sync(0xffffffffu, top);
             }
-            top = __reduce_max_sync(0xffffffffu, top);
-            if (__any_sync(0xffffffffu, odd)) status |= VA_DEV_NONFINITE;
             const float fresh = __fdiv_rn(__uint_as_float(top << 16), top_code(kInt8));
             const float s = older ? fmaxf(fresh, was) : fresh;
+            // (below 2^-100 the reciprocal comes near its range's end: 0 sends all eight to the division)
+            const float inv = s > 7.9e-31f ? __frcp_rn(s) : 0.0f;
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 const int p = p0 + 2 * r + half;
@@ -122,7 +144,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendA
                         x[2 * c] = __uint_as_float(w[c] << 16);
                         x[2 * c + 1] = __uint_as_float(w[c] & 0xFFFF0000u);
                     }
-                    *dst = code8<kInt8>(x, s);
+                    *dst = code8<kInt8>(x, s, inv);
                 } else if (p < start && s > was) {
                     const uint2 c = *dst;
                     float lo[4], hi[4], x[8];
@@ -133,7 +155,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendA
                         x[e] = __fmul_rn(lo[e], was);
                         x[4 + e] = __fmul_rn(hi[e], was);
                     }
-                    *dst = code8<kInt8>(x, s);
+                    *dst = code8<kInt8>(x, s, inv);
                 }
             }
             if (lane == 0) *scale = s;
