@@ -1,8 +1,8 @@
-// verify_attn_paged_b8: the call, and the second of its two launches, which merges what the split kernel
-// (paged_attn.cuh) left in parts and writes the rows that see nothing.
+// verify_attn_paged_b8: the call, and the second of its two launches, which merges what the split kernels
+// (paged_attn.cuh, paged_attn_tc.cuh) left in parts and writes the rows that see nothing.
 #include <cmath>
 
-#include "paged_attn.cuh"
+#include "paged_plan.cuh"
 
 namespace va {
 namespace tc {
@@ -14,11 +14,17 @@ EncodeTiledFn encode_fn();   // attn_tc.cu
 
 namespace paged {
 
+cudaError_t launch_attn_e4m3(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, const uint8_t* k_codes,
+                             const uint8_t* v_codes, cudaStream_t stream);
+cudaError_t launch_attn_int8(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, const uint8_t* k_codes,
+                             const uint8_t* v_codes, cudaStream_t stream);
+
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kMost = kMaxCtas / kJoinWarps;   // most parts of a warp
 
 // CTA (unit, y): unit = (sequence, KV head); its (row, query head) pairs y, y + gridDim.y, ..
 // Few parts: a warp a pair.  Many (a long history over many CTAs): the warps share a pair's parts, each a
-// consecutive run with four chains of its own in order, and join through shared memory; the order is fixed.
+// consecutive run, and join through shared memory; the order is fixed.
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnPagedArgs a) {
     __shared__ long long sums[3 * kJoinWarps];
     __shared__ float4 acc_s[kJoinWarps][32];
@@ -74,16 +80,20 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnPaged
     const int c_first = cta_of(first + kSegCost), c_last = cta_of(first + kSegCost + n_tiles - 1);
     if (c_first == c_last) return;   // the split kernel has written the rows
     const int parts = c_last - c_first + 1;
-    auto place = [&](int c) {        // the part of CTA c: its first segment's unless the head began inside it
-        return (size_t)(2 * c + (cta_begin(c, n_ctas, total) >= first ? 0 : 1)) * kMaxCols;
-    };
-    const bool shared = parts > 16;
+    // the part of a CTA is its first segment's, but for the head's first CTA if the head begins inside it
+    const size_t first_place = (size_t)(2 * c_first + (cta_begin(c_first, n_ctas, total) >= first ? 0 : 1)) * kMaxCols;
+    auto place = [&](int p) { return p == 0 ? first_place : (size_t)(2 * (c_first + p)) * kMaxCols; };
+    const bool shared = parts > kMost;
     const int n_cols = sq.live * a.group, step = shared ? (int)gridDim.y : (int)gridDim.y * kJoinWarps;
     for (int col = shared ? (int)blockIdx.y : (int)blockIdx.y * kJoinWarps + warp; col < n_cols; col += step) {
         const int p0 = shared ? parts * warp / kJoinWarps : 0, p1 = shared ? parts * (warp + 1) / kJoinWarps : parts;
-        // the parts' references and sums, one a lane (a warp has at most 32: 160 / 8, or 16)
+        // all of the warp's parts in flight at once: their sums, and (one a lane) their references
+        float4 v[kMost];
+#pragma unroll
+        for (int i = 0; i < kMost; ++i)
+            if (p0 + i < p1) v[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (place(p0 + i) + col) * kD) + lane);
         float2 ml = make_float2(-INFINITY, 0.0f);
-        if (lane < p1 - p0) ml = __ldcg(a.part_ml + place(c_first + p0 + lane) + col);
+        if (lane < p1 - p0) ml = __ldcg(a.part_ml + place(p0 + lane) + col);
         float top = ml.x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -92,15 +102,15 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnPaged
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 10
-        for (int p = p0; p < p1; ++p) {
-            const float w = __shfl_sync(0xffffffffu, by, p - p0);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (place(c_first + p) + col) * kD) + lane);
-            acc.x += w * v.x;
-            acc.y += w * v.y;
-            acc.z += w * v.z;
-            acc.w += w * v.w;
-        }
+#pragma unroll
+        for (int i = 0; i < kMost; ++i)
+            if (p0 + i < p1) {
+                const float w = __shfl_sync(0xffffffffu, by, i);
+                acc.x += w * v[i].x;
+                acc.y += w * v[i].y;
+                acc.z += w * v[i].z;
+                acc.w += w * v[i].w;
+            }
         if (shared) {
             __syncthreads();
             acc_s[warp][lane] = acc;
@@ -185,8 +195,8 @@ va_status verify_attn_paged_b8(const va_bf16* q, int n_seqs, int n_rows, int n_k
     CUtensorMap mk, mv;
     const long long rows = (long long)n_pages * n_kv_heads * kPage;
     if (!encode_pool(&mk, k_codes, rows) || !encode_pool(&mv, v_codes, rows)) return VA_CUDA_ERROR;
-    st = launched(format == VA_B8_INT8 ? launch_attn_int8(a, mk, mv, (cudaStream_t)stream)
-                                       : launch_attn_e4m3(a, mk, mv, (cudaStream_t)stream));
+    st = launched((format == VA_B8_INT8 ? launch_attn_int8 : launch_attn_e4m3)(
+        a, mk, mv, static_cast<const uint8_t*>(k_codes), static_cast<const uint8_t*>(v_codes), (cudaStream_t)stream));
     if (st != VA_OK) return st;
     // about one CTA an SM: a unit each where there are enough, else its pairs are shared out
     const int units = n_seqs * n_kv_heads, pairs = n_rows * group;

@@ -20,87 +20,18 @@
 // scales go into p relative to R, the largest so far (a power of two), which f16 would not hold by themselves.
 #pragma once
 
-#include <cuda.h>
-#include <cuda_bf16.h>
-
-#include "paged.cuh"
-#include "tc_ptx.cuh"
+#include "paged_attn_tc.cuh"
+#include "paged_plan.cuh"
 
 namespace va {
 namespace paged {
 
-constexpr int kMaxCtas = 160;                 // CTAs of one call (one an SM)
-constexpr int kMaxCols = VA_MAX_ROWS * VA_PAGED_MAX_GROUP;   // 64 (row, query head) pairs of a KV head
 constexpr int kConsumers = 8;                 // consumer warps of a CTA
 // Three warpgroups of 168 registers a thread at launch (64,512 in all); the consumers' two then hold 232, the
 // producer's one 40 (59,392 + 5,120).
 constexpr int kAttnThreads = 32 * (kConsumers + 4);
 constexpr int kConsumerRegs = 232, kProducerRegs = 40;
-constexpr int kTileBytes = 2 * kHeadBytes;    // K and V codes of a tile
-constexpr uint64_t kWaitNs = 1000000000ull;   // a wait gives up after a second (VA_DEV_TIMEOUT)
-constexpr float kShift = 6.0f;                // p = 2^(t - m + kShift)
-constexpr float kLazy = 8.0f;                 // m is raised when a score passes it by this much
-constexpr float kNoScore = -3.0e38f;          // m before the first score (any score passes it)
 constexpr int kTickets = 64;                  // segments that can be open at once in a CTA are fewer
-
-// Workspace: partial sums of 2 segments a CTA, [2 kMaxCtas][kMaxCols][128] floats, then their (m, l).
-constexpr size_t kPartFloats = (size_t)2 * kMaxCtas * kMaxCols * kD;
-constexpr size_t kWorkspaceBytes = sizeof(float) * (kPartFloats + (size_t)2 * kMaxCtas * kMaxCols * 2);
-
-struct AttnPagedArgs {
-    const uint16_t* q;
-    const int32_t *n_live, *lens, *table;
-    const float *k_scale, *v_scale;
-    const float* sink;
-    float* part_o;
-    float2* part_ml;
-    uint16_t* out;
-    float* out_lse;
-    int32_t* dev_status;
-    float scale_log2;                         // scale x log2 e
-    int n_seqs, n_rows, n_kv, group, max_pages, n_pages, window, n_ctas;
-};
-
-// The visible pages of a sequence: [first, first + n).
-struct Span {
-    int first, n;
-};
-__device__ __forceinline__ Span span_of(int len, int live, int window) {
-    Span s;
-    const int lo = window > 0 ? max(0, len - live - window + 1) : 0;
-    s.first = lo / kPage;
-    s.n = live > 0 ? (len + kPage - 1) / kPage - s.first : 0;
-    return s;
-}
-
-// The deal.  A segment costs a CTA kSegCost tiles besides its tiles (its q, its joining), so the tiles are dealt by
-// cost: the tiles of a (sequence, head) of n pages lie at the costs s + kSegCost .. s + kSegCost + n - 1, the next
-// head's at s + kSegCost + n on, and CTA c of C takes the tiles whose cost is in [c W / C, (c + 1) W / C), W the sum.
-constexpr int kSegCost = 2;
-__device__ __forceinline__ long long cta_begin(int c, int n, long long total) {
-    return total < (1ll << 24) ? (long long)((unsigned)c * (unsigned)total / (unsigned)n) : (long long)c * total / n;
-}
-
-// What an unnormalised output row sum 2^(t - m) v is multiplied by, and its log-sum-exp: l is the sum of 2^(t - m),
-// the sink joins the denominator.
-struct Finish {
-    float by, lse;
-};
-__device__ __forceinline__ Finish finish(float m, float l, const float* sink, int head) {
-    Finish f;
-    const float s2 = sink ? __ldg(sink + head) * 1.4426950408889634f : -INFINITY;
-    const float seen = l == 0.0f ? -INFINITY : m + log2f(l);
-    const float top = fmaxf(seen, s2);
-    const float all = top == -INFINITY ? -INFINITY : top + log2f(exp2f(seen - top) + exp2f(s2 - top));
-    f.by = l == 0.0f ? 0.0f : (l != l ? l : exp2f(seen - all) / l);
-    f.lse = (l != l ? l : all) * 0.6931471805599453f;
-    return f;
-}
-
-__device__ __forceinline__ void store_row(uint16_t* dst, const float4& o) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
-    *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
 
 // ----------------------------------------------------------------------------- fragments
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -143,17 +74,6 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& x, uint32_t& y) {
     }
 }
 
-// A wait that the warp makes as one: every lane leaves it with the same answer.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int& status) {
-    const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, kWaitNs));
-    if (!ok) {
-        if (!*abort) status |= VA_DEV_TIMEOUT;
-        __syncwarp();
-        *abort = 1;
-    }
-    return ok;
-}
-
 // A stage's use number `use` has been loaded (bar: its full barrier) or read (its empty barrier): first that the
 // use's loads have been issued (*issued > use), because a barrier's parity alone does not tell the use that is
 // waited for from the one before the last; then the barrier.
@@ -183,8 +103,7 @@ struct Shape {
     static constexpr int kSlotFloats = kCols * kD;
     static constexpr int kRingAt = 0;
     static constexpr int kFixed = kConsumers * (kSlotFloats + 2 * kCols) * 4   // the warps' slots and their (m, l)
-                                  + (VA_PAGED_MAX_SEQS + 1) * 8 + VA_PAGED_MAX_SEQS * 7   // prefixes, lengths, live rows
-                                  + 2048;                                      // barriers, tickets, scales, alignment
+                                  + (int)sizeof(Plan) + 2048;                  // barriers, tickets, alignment
     static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kTileBytes + 32);
     static constexpr int kStages = kFit < 12 ? kFit : 12;
     static constexpr int kBytes = 1024 + kFixed + kStages * (kTileBytes + 32);
@@ -202,18 +121,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     unsigned char* ring = base;
     float* slots = reinterpret_cast<float*>(ring + NS * kTileBytes);
     float2* slot_ml = reinterpret_cast<float2*>(slots + kConsumers * S::kSlotFloats);
-    long long* pre = reinterpret_cast<long long*>(slot_ml + kConsumers * kCols);
-    int* s_len = reinterpret_cast<int*>(pre + VA_PAGED_MAX_SEQS + 1);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(s_len + VA_PAGED_MAX_SEQS + 2);
+    Plan& plan = *reinterpret_cast<Plan*>(slot_ml + kConsumers * kCols);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(&plan + 1);
     float* scales = reinterpret_cast<float*>(bars + 48);
     int* tickets = reinterpret_cast<int*>(scales + NS * 8);
     int* issued = tickets + RG * kTickets;    // each stage's uses so far
     int* valid = issued + 16;                 // whether its tile has a page
     int* flags = valid + 16;                  // [0]: the CTA gives up
-    signed char* s_live = reinterpret_cast<signed char*>(flags + 4);
-    unsigned char* col_row = reinterpret_cast<unsigned char*>(s_live + VA_PAGED_MAX_SEQS);   // row and query head of each pair
-    unsigned char* col_head = col_row + kMaxCols;
-    unsigned short* some = reinterpret_cast<unsigned short*>(col_head + kMaxCols);   // sequences with tiles before each
     const uint32_t full0 = ptx::smem_u32(bars), empty0 = full0 + 8 * 16, free0 = full0 + 8 * 32;
     const uint32_t filled = full0 + 8 * 40, joined = full0 + 8 * 41;
     volatile int* abort = flags;
@@ -234,118 +148,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int s = 0; s < 16; ++s) issued[s] = 0;
     }
     for (int i = tid; i < RG * kTickets; i += kAttnThreads) tickets[i] = 0;
-    if (tid < kMaxCols) {
-        col_row[tid] = (unsigned char)(tid / a.group);
-        col_head[tid] = (unsigned char)(tid % a.group);
-    }
     __syncthreads();
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
 
-    // ---------------------------------------------------------------- plan: tiles before each sequence
     int status = 0;
-    constexpr int kPer = (VA_PAGED_MAX_SEQS + kAttnThreads - 1) / kAttnThreads;   // sequences per thread
-    {
-        // per thread: tiles in the low 48 bits, sequences that have any above (at most 1,024)
-        unsigned long long* sums = reinterpret_cast<unsigned long long*>(slots);
-        unsigned long long mine[kPer], sum = 0;
-        const int per = (a.n_seqs + kAttnThreads - 1) / kAttnThreads;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int b = tid * per + i;
-            mine[i] = 0;
-            if (i < per && b < a.n_seqs) {
-                const Seq s = load_seq(a.lens, a.n_live, b, a.n_rows, a.max_pages);
-                status |= s.status;
-                s_len[b] = s.len;
-                s_live[b] = (signed char)s.live;
-                const int n = span_of(s.len, s.live, a.window).n;
-                mine[i] = (unsigned long long)n * a.n_kv + (n > 0 ? 1ull << 48 : 0ull);
-                sum += mine[i];
-            }
-        }
-        unsigned long long upto = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long t = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += t;
-        }
-        if (lane == 31) sums[warp] = upto;
-        __syncthreads();
-        unsigned long long before = upto - sum;
-        for (int w = 0; w < warp; ++w) before += sums[w];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int b = tid * per + i;
-            if (i < per && b < a.n_seqs) {
-                pre[b] = (long long)(before & 0xFFFFFFFFFFFFull);
-                some[b] = (unsigned short)(before >> 48);
-                before += mine[i];
-                if (b == a.n_seqs - 1) {
-                    pre[a.n_seqs] = (long long)(before & 0xFFFFFFFFFFFFull);
-                    some[a.n_seqs] = (unsigned short)(before >> 48);
-                }
-            }
-        }
-        if (status && a.dev_status && blockIdx.x == 0) atomicOr(a.dev_status, status);
-        status = 0;
-    }
-    __syncthreads();
-    const long long total = pre[a.n_seqs];
-    const int n_ctas = (int)min((long long)a.n_ctas, total);
-    if ((int)blockIdx.x >= n_ctas) return;
-    // the last sequence that begins at or before x, in tiles (seg = 0) or in costs (seg = kSegCost x heads)
-    auto find = [&](long long x, int seg) {
-        int lo = 0, hi = a.n_seqs;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (pre[mid] + seg * (int)some[mid] <= x) lo = mid;
-            else hi = mid;
-        }
-        return lo;
-    };
-    const int seg_cost = kSegCost * a.n_kv;
-    const long long cost = total + seg_cost * (int)some[a.n_seqs];
-    // where this CTA's tiles begin (even lanes) and the next one's (odd lanes)
-    long long c0 = total, c1;
-    int b_first = 0, h_first = 0, t_first = 0;
-    {
-        const long long y = cta_begin(blockIdx.x + (lane & 1), n_ctas, cost);
-        if (y < cost) {
-            b_first = find(y, seg_cost);
-            const unsigned rest = (unsigned)(y - pre[b_first] - seg_cost * (int)some[b_first]);
-            const unsigned n = (unsigned)span_of(s_len[b_first], s_live[b_first], a.window).n, per = n + kSegCost;
-            h_first = (int)(rest / per);
-            t_first = max((int)(rest % per) - kSegCost, 0);
-            c0 = pre[b_first] + (long long)h_first * n + t_first;
-        }
-        c1 = __shfl_sync(0xffffffffu, c0, 1);
-        c0 = __shfl_sync(0xffffffffu, c0, 0);
-        b_first = __shfl_sync(0xffffffffu, b_first, 0);
-        h_first = __shfl_sync(0xffffffffu, h_first, 0);
-        t_first = __shfl_sync(0xffffffffu, t_first, 0);
-    }
+    const Share share = make_plan<kAttnThreads>(plan, a);
+    if ((int)blockIdx.x >= share.n_ctas) return;
 
     if (warp >= kConsumers) {
         ptx::set_max_regs_dec<kProducerRegs>();
         // ------------------------------------------------------------ producers
         // Four warps take the tiles in turn (one alone issued a tile in 0.5 us, longer than a tile takes to arrive).
         // A lane looks up a tile's page, 32 at once; then the warp issues them one by one, a copy a lane.
-        const int n = (int)(c1 - c0), pw = warp - kConsumers;
+        const int n = share.n, pw = warp - kConsumers;
         int last = -1;
         bool given_up = false;
         for (int i0 = pw; i0 < n && !given_up; i0 += 4 * 32) {
             int row = -1;
-            if (i0 + 4 * lane < n) {
-                const long long x = c0 + i0 + 4 * lane;
-                const int b = find(x, 0);
-                const Span sp = span_of(s_len[b], s_live[b], a.window);
-                const unsigned within = (unsigned)(x - pre[b]);
-                const int h = (int)(within / (unsigned)sp.n), t = sp.first + (int)(within % (unsigned)sp.n);
-                const int page = __ldcg(a.table + (size_t)b * a.max_pages + t);
-                if (page >= 0 && page < a.n_pages) row = page * a.n_kv + h;
-                else status |= VA_DEV_BAD_PAGE;
-            }
+            if (i0 + 4 * lane < n) row = tile_row(plan, a, share.c0 + i0 + 4 * lane, status);
             for (int l = 0; l < 32 && i0 + 4 * l < n; ++l) {
                 const int i = i0 + 4 * l, s = i % NS, use = i / NS, r = __shfl_sync(0xffffffffu, row, l);
                 if (use > 0 && !page_wait(issued + s, use - 1, empty0 + 8 * s, (use - 1) & 1, abort, status)) {
@@ -385,22 +206,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         float2* my_ml = slot_ml + warp * kCols;
         // how often the slot has been filled for a single warp's join, and for a common one; which was the last
         int uses = 0, joins = 0, slot_use = 0;
-        const int n_tiles = (int)(c1 - c0);                   // none where the CTA's costs are all a segment's own
-        int b_next = b_first, h_next = h_first, t_next = t_first;   // where the next segment begins
         bool given_up = false;
-        for (int i_end = 0, seg = 0; i_end < n_tiles && !given_up; ++seg) {
-            const int b = b_next, h = h_next, t0 = t_next, i_begin = i_end;
-            const int len = s_len[b], live = s_live[b];
-            const Span sp = span_of(len, live, a.window);
-            const int seg_len = min(n_tiles - i_begin, sp.n - t0);
-            const bool whole = seg_len == sp.n;
-            i_end += seg_len;
-            t_next = 0;
-            if (++h_next == a.n_kv) {
-                h_next = 0;
-                do ++b_next;
-                while (b_next < a.n_seqs && pre[b_next + 1] == pre[b_next]);
-            }
+        Walk walk(share);
+        while (!given_up && walk.next(plan, a, share.n)) {
+            const int b = walk.b, h = walk.h, len = walk.len, live = walk.live, i_begin = walk.begin, i_end = walk.end;
+            const int seg = walk.seg, seg_len = i_end - i_begin;
+            const bool whole = walk.whole;
             int i = i_begin + ((team - i_begin) & (T - 1));
             if (i >= i_end) continue;
             // Q, each row brought to f16's upper range by a power of two (exact but for elements 2^-39 of the row's
@@ -416,9 +227,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int c = col0 + 8 * n + g;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) raw[n][e] = make_uint4(0u, 0u, 0u, 0u);
-                    if (c < cols_used && col_row[c] < live) {
+                    if (c < cols_used && plan.col_row[c] < live) {
                         const uint4* src = reinterpret_cast<const uint4*>(
-                            a.q + (((size_t)b * a.n_rows + col_row[c]) * heads + h * a.group + col_head[c]) * kD + 16 * j);
+                            a.q + (((size_t)b * a.n_rows + plan.col_row[c]) * heads + h * a.group + plan.col_head[c]) * kD + 16 * j);
                         raw[n][0] = __ldg(src);
                         raw[n][1] = __ldg(src + 1);
                         raw[n][2] = __ldg(src + 8);
@@ -458,7 +269,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         off[n][e] = kInt8 ? 1152.0f * __shfl_sync(0xffffffffu, sum, (2 * j + e) * 4) : 0.0f;
                         m[n][e] = kNoScore;
                         l[n][e] = 0.0f;
-                        p[n][e] = len - live + min((int)col_row[min(col0 + 8 * n + 2 * j + e, kMaxCols - 1)], live - 1);
+                        p[n][e] = len - live + min((int)plan.col_row[min(col0 + 8 * n + 2 * j + e, kMaxCols - 1)], live - 1);
                     }
 #pragma unroll
                     for (int d = 0; d < 8; ++d)
@@ -477,7 +288,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const unsigned char* kt = ring + st * kTileBytes;
                     const unsigned char* vt = kt + kHeadBytes;
                     const float* sc = scales + 8 * st;
-                    const int key0 = (sp.first + t0 + (i - i_begin)) * kPage;
+                    const int key0 = (walk.page0 + (i - i_begin)) * kPage;
                     // some row does not see all of the page's keys
                     const bool edge = key0 + kPage - 1 > len - live || (a.window > 0 && key0 < len - a.window);
                     // this warp's KB blocks; past: blocks that begin past the sequence, where scales may be anything
@@ -686,8 +497,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                 const size_t part = (size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + col;
-                const int head = h * a.group + col_head[col];
-                const size_t row = ((size_t)b * a.n_rows + col_row[col]) * heads + head;
+                const int head = h * a.group + plan.col_head[col];
+                const size_t row = ((size_t)b * a.n_rows + plan.col_row[col]) * heads + head;
                 if (whole) {
                     const Finish fin = finish(top, sum, a.sink, head);
                     one *= fin.by;
@@ -716,7 +527,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!warp_wait(filled, joins & 1, abort, status)) break;
 #pragma unroll 1
                 for (int q = warp; q < RG * kCols; q += kConsumers)
-                    if (q < cols_used && col_row[q] < live) join(q / kCols, q % kCols);
+                    if (q < cols_used && plan.col_row[q] < live) join(q / kCols, q % kCols);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(joined);
                 ++joins;
@@ -739,7 +550,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 __syncwarp();
 #pragma unroll 1
                 for (int c = 0; c < kCols; ++c)
-                    if (col0 + c < cols_used && col_row[col0 + c] < live) join(rg, c);
+                    if (col0 + c < cols_used && plan.col_row[col0 + c] < live) join(rg, c);
                 __syncwarp();
                 if (lane < active)
                     ptx::mbar_arrive(free0 + 8 * (((((i_begin & (T - 1)) + lane / KG) & (T - 1)) * KG + lane % KG) * RG + rg));
@@ -760,19 +571,17 @@ cudaError_t launch_shape(const AttnPagedArgs& a, const CUtensorMap& k, const CUt
     return cudaLaunchKernelEx(&cfg, attn_paged_kernel<kInt8, RT, RG>, a, k, v);
 }
 
+// By the (row, query head) pairs of a KV head: up to 16 here, more on tcgen05 (paged_attn_tc.cuh).
 template <bool kInt8>
-cudaError_t launch_format(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+cudaError_t launch_format(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, const uint8_t* k_codes,
+                          const uint8_t* v_codes, cudaStream_t stream) {
     const int cols = a.n_rows * a.group;
     if (cols <= 8) return launch_shape<kInt8, 1, 1>(a, k, v, stream);
     if (cols <= 16) return launch_shape<kInt8, 2, 1>(a, k, v, stream);
-    if (cols <= 24) return launch_shape<kInt8, 3, 1>(a, k, v, stream);
-    if (cols <= 32) return launch_shape<kInt8, 2, 2>(a, k, v, stream);
-    if (cols <= 48) return launch_shape<kInt8, 3, 2>(a, k, v, stream);
-    return launch_shape<kInt8, 2, 4>(a, k, v, stream);
+    if (cols <= 32) return tcg::launch<kInt8, 32>(a, k_codes, v_codes, stream);
+    if (cols <= 48) return tcg::launch<kInt8, 48>(a, k_codes, v_codes, stream);
+    return tcg::launch<kInt8, 64>(a, k_codes, v_codes, stream);
 }
-
-cudaError_t launch_attn_e4m3(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream);
-cudaError_t launch_attn_int8(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream);
 
 }  // namespace paged
 }  // namespace va

@@ -1,10 +1,11 @@
-// The split kernel of verify_attn_paged_b8 over INT8 codes.
+// The split kernels of verify_attn_paged_b8 over INT8 codes.
 #include "paged_attn.cuh"
 
 namespace va {
 namespace paged {
-cudaError_t launch_attn_int8(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
-    return launch_format<true>(a, k, v, stream);
+cudaError_t launch_attn_int8(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, const uint8_t* k_codes,
+                             const uint8_t* v_codes, cudaStream_t stream) {
+    return launch_format<true>(a, k, v, k_codes, v_codes, stream);
 }
 }  // namespace paged
 }  // namespace va
