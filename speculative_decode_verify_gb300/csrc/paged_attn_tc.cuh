@@ -5,8 +5,8 @@
 // with keys as the matrix rows: S^T[128 keys x NC pairs] = K Q^T and O^T[128 dimensions x NC pairs] += V^T P^T, f16
 // operands in shared memory (exact for both code formats), f32 accumulators in TMEM, S double-buffered.
 //   producer   pages' codes and scales into a ring by bulk copies
-//   wideners   eight warps: a tile's K, then its V, from codes to swizzled f16 (one buffer each: K's is free when the
-//              scores are done, V's when the products are)
+//   wideners   eight warps: a tile's K, then its V, from codes to swizzled f16 (K's buffer is free when the scores
+//              are done, V's two when the products of the tile before the last are)
 //   issuer     one thread: the scores of tile i + 1 before the products of tile i
 //   softmax    eight warps, a key a thread, half the pairs each: as in paged_attn.cuh (base 2, a reference that is
 //              raised when a score passes it by 2^8, V's scales relative to the largest so far), with one reference a
@@ -28,9 +28,9 @@ constexpr int kThreads = 32 * (kSoftWarps + kWideWarps + 4);
 constexpr int kSoftRegs = 136, kWideRegs = 72, kLastRegs = 56;
 constexpr int kKeys = 128;                         // keys of a tile
 constexpr uint32_t kHalf = kKeys * 128;            // one half of the dimensions of a tile in f16
-constexpr uint32_t kOffK = 0, kOffV = 2 * kHalf, kOffP = 4 * kHalf;
+constexpr uint32_t kOffK = 0, kOffV = 2 * kHalf, kOffP = 6 * kHalf;   // one K buffer, two of V
 constexpr uint32_t kPBytes = kKeys * 128;          // a tile's weights: a key a row of 64 pairs
-constexpr uint32_t kOffQ = kOffP + 2 * kPBytes;
+constexpr uint32_t kOffQ = kOffP + kPBytes;        // P and Q together hold NC x 128 floats at a segment's end
 constexpr uint32_t kTmemCols = 256, kColS = 0, kColO = 128;   // S at 0 and 64
 
 struct Misc {
@@ -41,12 +41,13 @@ struct Misc {
     float ref[kSoftWarps][32];
     float red[4][kMaxCols], vmax[4];
     alignas(8) uint64_t raw_full[6], raw_empty[6];
-    uint64_t k_ready, v_ready, s_full[2], s_free[2], p_ready[2], pv_done[2], q_ready, o_done, o_free, vote[2], join, drain;
+    uint64_t k_ready, v_ready[2], s_full[2], s_free[2], p_ready[2], pv_done[2], q_ready, o_done, o_free, vote[2], join, drain;
     int prow[kMaxCols];                            // positions of the pairs' rows
     int ring_ok[6], ok[4];
     alignas(8) unsigned char flag[2][kSoftWarps];
     uint32_t tmem;
     int abort;
+    alignas(16) float2 ub[kSoftWarps][32];         // raising: what comes off a pair's exponents, its sums' factor
 };
 
 template <int NC>
@@ -122,8 +123,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
             ptx::mbar_init(bar(ms.raw_empty[s]), kWideWarps);
         }
         ptx::mbar_init(bar(ms.k_ready), kWideWarps);
-        ptx::mbar_init(bar(ms.v_ready), kWideWarps);
         for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(bar(ms.v_ready[s]), kWideWarps);
             ptx::mbar_init(bar(ms.s_full[s]), 1);
             ptx::mbar_init(bar(ms.s_free[s]), kSoftWarps);
             ptx::mbar_init(bar(ms.p_ready[s]), kSoftWarps);
@@ -213,12 +214,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                 ptx::mma_commit(bar(ms.s_full[t & 1]));
             };
             auto products = [&](int t, int n_keys16, bool first, bool end, int seg) {
-                if (!wait(ms.v_ready, t) || !wait(ms.p_ready[t & 1], t >> 1)) return;
+                if (!wait(ms.v_ready[t & 1], t >> 1) || !wait(ms.p_ready[t & 1], t >> 1)) return;
                 if (first && seg > 0 && !wait(ms.o_free, seg - 1)) return;
                 ptx::tc_fence_after();
                 for (int k = 0; k < n_keys16; ++k)
-                    ptx::mma_bf16(tmem + kColO, ptx::smem_desc(base_s + kOffV + k * 2048, kHalf, 1024),
-                                  ptx::smem_desc(base_s + kOffP + (t & 1) * kPBytes + k * 2048, 8192, 1024), id_o,
+                    ptx::mma_bf16(tmem + kColO, ptx::smem_desc(base_s + kOffV + (t & 1) * 2 * kHalf + k * 2048, kHalf, 1024),
+                                  ptx::smem_desc(base_s + kOffP + k * 2048, 8192, 1024), id_o,
                                   !first || k > 0);
                 ptx::mma_commit(bar(ms.pv_done[t & 1]));
                 if (end) ptx::mma_commit(bar(ms.o_done));
@@ -256,9 +257,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                 const int key0 = (walk.page0 + p0 - walk.begin) * kPage;
 #pragma unroll
                 for (int is_v = 0; is_v < 2; ++is_v) {
-                    // K's buffer is free once the scores of the tile before are done, V's once its products are
-                    if (t > 0 && !warp_wait(is_v ? bar(ms.pv_done[(t - 1) & 1]) : bar(ms.s_full[(t - 1) & 1]),
-                                            ((t - 1) >> 1) & 1, abort, status)) {
+                    // K's buffer is free once the scores of the tile before are done, V's once the products of the
+                    // one before that are
+                    if (t > is_v && !warp_wait(is_v ? bar(ms.pv_done[t & 1]) : bar(ms.s_full[(t - 1) & 1]),
+                                               (is_v ? (t >> 1) - 1 : (t - 1) >> 1) & 1, abort, status)) {
                         ok = false;
                         break;
                     }
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                             // (what lies past the sequence or in no page may be NaN, and would stay it with weight 0)
                             if (is_v && (!page_ok || key0 + key >= walk.len)) x = make_uint4(0u, 0u, 0u, 0u);
                             widen16<kInt8>(x, y[0], y[1]);
-                            unsigned char* dst = base + (is_v ? kOffV : kOffK) + (c >> 2) * kHalf + key * 128;
+                            unsigned char* dst = base + (is_v ? kOffV + (t & 1) * 2 * kHalf : kOffK) + (c >> 2) * kHalf + key * 128;
                             *reinterpret_cast<uint4*>(dst + ((first ^ (key & 7)) * 16)) = c & 4 ? y[1] : y[0];
                             *reinterpret_cast<uint4*>(dst + ((second ^ (key & 7)) * 16)) = c & 4 ? y[0] : y[1];
                         }
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                     if (!ok) break;
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(is_v ? bar(ms.v_ready) : bar(ms.k_ready));
+                    if (lane == 0) ptx::mbar_arrive(is_v ? bar(ms.v_ready[t & 1]) : bar(ms.k_ready));
                     if (is_v && lane < n_pages) ptx::mbar_arrive(bar(ms.raw_empty[(p0 + lane) % NR]));
                 }
             }
@@ -410,10 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                     // columns' maxima over the tile's keys, by warp, then over the four warps that share them
 #pragma unroll
                     for (int c = 0; c < NH; ++c) {
-                        // (order-preserving integers; NaN lowest)
-                        const uint32_t u = __float_as_uint(y[c]);
-                        const uint32_t m = __reduce_max_sync(0xffffffffu, y[c] == y[c] ? ((u >> 31) ? ~u : u | 0x80000000u) : 0u);
-                        const float top = m == 0u ? -INFINITY : __uint_as_float((m >> 31) ? m & 0x7FFFFFFFu : ~m);
+                        const float top = ptx::redux_max(y[c]);
                         if (lane == 0) ms.red[q][n0 + c] = top;
                     }
                     if (!meet()) break;
@@ -431,36 +430,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                         tmem_ld<NH>(tl + kColO + n0, o);
                     }
                     // lane c finds pair n0 + c's new reference
-                    float up_mine = 0.0f, by_mine = 1.0f;
                     if (lane < NH) {
                         const int c = n0 + lane;
                         const float now = fmaxf(fmaxf(ms.red[0][c], ms.red[1][c]), fmaxf(ms.red[2][c], ms.red[3][c]));
                         const float was = ref[lane];
                         const bool none_yet = was == kNoScore;
-                        up_mine = now == -INFINITY ? 0.0f : (none_yet ? now - kShift : fmaxf(now - kShift, 0.0f));
-                        by_mine = none_yet ? 1.0f : ptx::ex2(-up_mine);
+                        const float up = now == -INFINITY ? 0.0f : (none_yet ? now - kShift : fmaxf(now - kShift, 0.0f));
+                        ms.ub[warp][lane] = make_float2(up, none_yet ? 1.0f : ptx::ex2(-up));
                         if (now > -INFINITY) {
-                            const float m = (none_yet ? 0.0f : was) + up_mine;
+                            const float m = (none_yet ? 0.0f : was) + up;
                             ref[lane] = m;
                             fz[lane].y = kShift - m;
                         }
                     }
                     __syncwarp();
+                    const float4* ub = reinterpret_cast<const float4*>(ms.ub[warp]);
 #pragma unroll
-                    for (int c = 0; c < NH; ++c) {
-                        const float up = __shfl_sync(0xffffffffu, up_mine, c), by = __shfl_sync(0xffffffffu, by_mine, c);
-                        y[c] -= up;
-                        l[c] *= by;
-                        if (i > 0) o[c] *= by * r_by;
+                    for (int c = 0; c < NH; c += 2) {
+                        const float4 w = ub[c / 2];
+                        y[c] -= w.x;
+                        l[c] *= w.y;
+                        y[c + 1] -= w.z;
+                        l[c + 1] *= w.w;
+                        if (i > 0) {
+                            o[c] *= w.y * r_by;
+                            o[c + 1] *= w.w * r_by;
+                        }
                     }
                     if (i > 0) tmem_st<NH>(tl + kColO + n0, o);
                     ptx::tc_fence_before();
                     all_set = __all_sync(0xffffffffu, lane >= NH || ref[lane] != kNoScore);
                 }
-                // weights into P, in the place that the products of tile t - 2 have left
-                if (t >= 2 && !(ok = warp_wait(bar(ms.pv_done[t & 1]), ((t >> 1) - 1) & 1, abort, status))) break;
+                // weights into P, which the products of the tile before have left
+                if (t > 0 && !(ok = warp_wait(bar(ms.pv_done[(t - 1) & 1]), ((t - 1) >> 1) & 1, abort, status))) break;
                 const float r = vs * inv_r;
-                unsigned char* dst = base + kOffP + (t & 1) * kPBytes + me * 128;
+                unsigned char* dst = base + kOffP + me * 128;
 #pragma unroll
                 for (int c8 = 0; c8 < NH / 8; ++c8) {
                     uint32_t w[4];
@@ -479,56 +483,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                 if (lane == 0) ptx::mbar_arrive(bar(ms.p_ready[t & 1]));
             }
             if (!ok) break;
-            // -------------------------------------------------------- the segment's sums: thread = dimension
-#pragma unroll
-            for (int c = 0; c < NH; ++c) {
-                float sum = l[c];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-                if (lane == 0) ms.red[q][n0 + c] = sum;
-            }
-            if (!meet()) break;
-            // lane c of each warp ends pair n0 + c
-            float by = 0.0f;
-            const size_t part = (size_t)(2 * blockIdx.x + (walk.begin == 0 ? 0 : 1)) * kMaxCols;
-            if (lane < NH) {
-                const int col = n0 + lane;
-                const float sum = (ms.red[0][col] + ms.red[1][col]) + (ms.red[2][col] + ms.red[3][col]);
-                const float m = ref[lane] == kNoScore ? -INFINITY : ref[lane] - kShift;
-                if (col < n_cols && ms.plan.col_row[col] < live) {
-                    if (walk.whole) {
-                        const int head = h * a.group + ms.plan.col_head[col];
-                        const Finish fin = finish(m, sum, a.sink, head);
-                        by = fin.by * R;
-                        if (q == 0 && a.out_lse) a.out_lse[((size_t)b * a.n_rows + ms.plan.col_row[col]) * heads + head] = fin.lse;
-                    } else {
-                        by = R;
-                        if (q == 0) a.part_ml[part + col] = make_float2(m, sum);
-                    }
-                }
-            }
+            // -------------------------------------------------------- the segment's sums
+            // In rolled loops over shared memory (P's and Q's place, now free): this runs once or twice in a CTA, from a
+            // cold instruction cache, where a line of code costs as much as a load.
             if (!(ok = warp_wait(bar(ms.o_done), walk.seg & 1, abort, status))) break;
             ptx::tc_fence_after();
+            float* stage = reinterpret_cast<float*>(base + kOffP);
+#pragma unroll
+            for (int c = 0; c < NH; ++c) stage[(n0 + c) * kKeys + me] = l[c];
             float o[NH];
             tmem_ld<NH>(tl + kColO + n0, o);
             ptx::tc_fence_before();
-            __syncwarp();
+            if (!meet()) break;
             if (lane == 0) ptx::mbar_arrive(bar(ms.o_free));
+            const size_t part = (size_t)(2 * blockIdx.x + (walk.begin == 0 ? 0 : 1)) * kMaxCols;
+#pragma unroll 1
+            for (int c = warp; c < NC; c += kSoftWarps) {
+                const float4 v = reinterpret_cast<const float4*>(stage + c * kKeys)[lane];
+                float sum = (v.x + v.y) + (v.z + v.w);
 #pragma unroll
-            for (int c = 0; c < NH; ++c) {
-                const int col = n0 + c;
-                const float v = o[c] * __shfl_sync(0xffffffffu, by, c);
-                if (col < n_cols && ms.plan.col_row[col] < live) {
-                    if (walk.whole)
-                        a.out[(((size_t)b * a.n_rows + ms.plan.col_row[col]) * heads + h * a.group + ms.plan.col_head[col]) * kD + me] =
-                            __bfloat16_as_ushort(__float2bfloat16_rn(v));
-                    else
-                        a.part_o[(part + col) * kD + me] = v;
+                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                const float at = c < NH ? ms.ref[0][c] : ms.ref[kSoftWarps / 2][c - NH];
+                const float m = at == kNoScore ? -INFINITY : at - kShift;
+                float by = 0.0f;
+                if (c < n_cols && ms.plan.col_row[c] < live) {
+                    by = R;
+                    if (walk.whole) {
+                        const int head = h * a.group + ms.plan.col_head[c];
+                        const Finish fin = finish(m, sum, a.sink, head);
+                        by *= fin.by;
+                        if (lane == 0 && a.out_lse) a.out_lse[((size_t)b * a.n_rows + ms.plan.col_row[c]) * heads + head] = fin.lse;
+                    } else if (lane == 0) {
+                        a.part_ml[part + c] = make_float2(m, sum);
+                    }
                 }
+                if (lane == 0) ms.red[0][c] = by;
             }
+            if (!meet()) break;
+#pragma unroll
+            for (int c = 0; c < NH; ++c) stage[(n0 + c) * kKeys + me] = o[c];
+            if (!meet()) break;
+#pragma unroll 1
+            for (int c = warp; c < NC; c += kSoftWarps) {
+                if (c >= n_cols || ms.plan.col_row[c] >= live) continue;
+                float4 v = reinterpret_cast<const float4*>(stage + c * kKeys)[lane];
+                const float by = ms.red[0][c];
+                v.x *= by;
+                v.y *= by;
+                v.z *= by;
+                v.w *= by;
+                if (walk.whole)
+                    store_row(a.out + (((size_t)b * a.n_rows + ms.plan.col_row[c]) * heads + h * a.group + ms.plan.col_head[c]) * kD + 4 * lane, v);
+                else
+                    reinterpret_cast<float4*>(a.part_o + (part + c) * kD)[lane] = v;
+            }
+            if (!meet()) break;
         }
     }
     if (status && a.dev_status) atomicOr(a.dev_status, status);
