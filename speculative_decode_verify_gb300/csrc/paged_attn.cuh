@@ -102,7 +102,7 @@ struct Shape {
     static constexpr int kCols = 8 * RT;                                 // pairs of a warp
     static constexpr int kSlotFloats = kCols * kD;
     static constexpr int kRingAt = 0;
-    static constexpr int kFixed = kConsumers * (kSlotFloats + 2 * kCols) * 4   // the warps' slots and their (m, l)
+    static constexpr int kFixed = kConsumers * (kSlotFloats + 10 * kCols) * 4  // the warps' slots, (m, l) and weights
                                   + (int)sizeof(Plan) + 2048;                  // barriers, tickets, alignment
     static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kTileBytes + 32);
     static constexpr int kStages = kFit < 12 ? kFit : 12;
@@ -121,7 +121,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     unsigned char* ring = base;
     float* slots = reinterpret_cast<float*>(ring + NS * kTileBytes);
     float2* slot_ml = reinterpret_cast<float2*>(slots + kConsumers * S::kSlotFloats);
-    Plan& plan = *reinterpret_cast<Plan*>(slot_ml + kConsumers * kCols);
+    float* weights = reinterpret_cast<float*>(slot_ml + kConsumers * kCols);
+    Plan& plan = *reinterpret_cast<Plan*>(weights + kConsumers * kCols * 8);
     uint64_t* bars = reinterpret_cast<uint64_t*>(&plan + 1);
     float* scales = reinterpret_cast<float*>(bars + 48);
     int* tickets = reinterpret_cast<int*>(scales + NS * 8);
@@ -548,9 +549,56 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!last) continue;
                 __threadfence_block();
                 __syncwarp();
+                // weights first: eight lanes a column, one for each active warp; then the columns' rows
+                auto warp_of = [&](int t) { return ((((i_begin & (T - 1)) + t / KG) & (T - 1)) * KG + t % KG) * RG + rg; };
+                float* by = weights + warp * kCols * 8;
+                const size_t part = (size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + col0;
+                const int n_here = min(kCols, live * a.group - col0);
 #pragma unroll 1
-                for (int c = 0; c < kCols; ++c)
-                    if (col0 + c < cols_used && plan.col_row[col0 + c] < live) join(rg, c);
+                for (int c = lane >> 3; c < kCols; c += 4) {
+                    const int t = lane & 7;
+                    float2 ml = make_float2(-INFINITY, 0.0f);
+                    if (t < active) ml = slot_ml[warp_of(t) * kCols + c];
+                    float top = ml.x;
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    float one = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.0f) : exp2f(ml.x - top);
+                    float sum = one * ml.y;
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                    if (c < n_here) {
+                        if (whole) {
+                            const int head = h * a.group + plan.col_head[col0 + c];
+                            const Finish fin = finish(top, sum, a.sink, head);
+                            one *= fin.by;
+                            if (t == 0 && a.out_lse) a.out_lse[((size_t)b * a.n_rows + plan.col_row[col0 + c]) * heads + head] = fin.lse;
+                        } else if (t == 0) {
+                            a.part_ml[part + c] = make_float2(top, sum);
+                        }
+                    }
+                    by[c * 8 + t] = one;
+                }
+                __syncwarp();
+#pragma unroll 2
+                for (int c = 0; c < n_here; ++c) {
+                    const int chunk = (lane & ~3) | ((lane & 3) ^ ((c >> 1) & 3));
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                    for (int t = 0; t < active; ++t) {
+                        const float one = by[c * 8 + t];
+                        const float4 v = reinterpret_cast<const float4*>(slots + (size_t)warp_of(t) * S::kSlotFloats + c * kD)[chunk];
+                        acc.x += one * v.x;
+                        acc.y += one * v.y;
+                        acc.z += one * v.z;
+                        acc.w += one * v.w;
+                    }
+                    if (whole)
+                        store_row(a.out + (((size_t)b * a.n_rows + plan.col_row[col0 + c]) * heads + h * a.group + plan.col_head[col0 + c]) * kD + 4 * lane, acc);
+                    else
+                        reinterpret_cast<float4*>(a.part_o + (part + c) * kD)[lane] = acc;
+                }
                 __syncwarp();
                 if (lane < active)
                     ptx::mbar_arrive(free0 + 8 * (((((i_begin & (T - 1)) + lane / KG) & (T - 1)) * KG + lane % KG) * RG + rg));
