@@ -65,7 +65,7 @@ __device__ __forceinline__ uint2 code8(const float (&x)[8], float s, float inv) 
 }
 
 template <bool kInt8>
-__global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(32 * kAppendWarps, 8) append_kernel(const AppendArgs a) {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31, half = lane >> 4, li = lane & 15;
@@ -84,6 +84,16 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendA
     const int p0 = block * kBlock;
     int status = sq.status;
     if (sq.live > 0 && p0 < sq.len) {
+        // the rows on their way before the page is known
+        const uint16_t* src = (is_v ? a.v_new : a.k_new) + ((size_t)b * a.n_rows * a.n_kv + h) * kD + 8 * li;
+        uint4 raw[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const int p = p0 + 2 * r + half;
+            raw[r] = make_uint4(0u, 0u, 0u, 0u);
+            if (p >= start && p < sq.len)
+                raw[r] = __ldcs(reinterpret_cast<const uint4*>(src + (size_t)(p - start) * a.n_kv * kD));
+        }
         const int page = __ldcg(a.table + b * a.max_pages + block / kBlocks);
         if (page < 0 || page >= a.n_pages) {
             status |= VA_DEV_BAD_PAGE;
@@ -92,17 +102,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendA
             const size_t head = (size_t)page * a.n_kv + h;
             uint8_t* codes = (is_v ? a.v_codes : a.k_codes) + head * kHeadBytes + part * kBlock * kD + 8 * li;
             float* scale = (is_v ? a.v_scale : a.k_scale) + head * kBlocks + part;
-            const uint16_t* src = (is_v ? a.v_new : a.k_new) + ((size_t)b * a.n_rows * a.n_kv + h) * kD + 8 * li;
             const bool older = p0 < start;
             const float was = older ? __ldcg(scale) : 0.0f;
-            uint4 raw[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const int p = p0 + 2 * r + half;
-                raw[r] = make_uint4(0u, 0u, 0u, 0u);
-                if (p >= start && p < sq.len)
-                    raw[r] = __ldcs(reinterpret_cast<const uint4*>(src + (size_t)(p - start) * a.n_kv * kD));
-            }
             // the block's largest magnitude, two elements at a time
             uint32_t top = 0;
 #pragma unroll
