@@ -1,12 +1,16 @@
 // va_beam_select: beam search's selection over beams and vocabulary.
 //
-// One launch, three levels.  A CTA per (8,192-logit tile, row) reads its logits once: it forms the tile's maximum
-// m and sum of exp(l - m) and collects the tile's k best keys as the sampler does, but forms keys only of the few
-// logits at or above a bound (a 64-bit key of every logit took ten times the loads: 117 us for 32 x 8 x 151,669).  The last CTA of a row to
-// arrive merges the tiles: log-sum-exp in 64 bits from the tiles' (m, sum), the row's k best keys, and their
-// scores in 64 bits.  The last row of a request to arrive merges the hypotheses.  Every order is fixed by the
-// keys, so the arrivals' order changes nothing.
-// Bytes: the logits once; what a tile hands on (k keys) is 1/1000 of that.
+// One launch, three levels.  The (row, 8,192-logit tile) units are dealt evenly to three CTAs an SM; a run is a CTA's
+// consecutive tiles of one row.  A CTA reads a tile's logits once (the next tile's are on their way into L2):
+//   sums        every thread keeps its own maximum m and sum of exp(l - m) over the run
+//   candidates  the run's k best keys so far are kept sorted in shared memory.  The first tile collects against a lower
+//               bound of its k-th logit, as the sampler does; a later one only the logits above the k-th so far (its
+//               indices are higher, so equal ones lose), few of which are left to rank.
+// The last run of a row to arrive merges the runs: log-sum-exp in 64 bits, the row's k best keys and their scores in
+// 64 bits.  The last row of a request merges the hypotheses.  Every order is fixed by the keys and by the deal, so the
+// arrivals' order changes nothing.
+// Bytes: the logits once; what a run hands on (k keys) is a thousandth of that.  A 64-bit key for every logit took
+// 117 us for 32 x 8 x 151,669 bf16 logits, keys and a ranking for every tile's candidates 56 us.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -32,7 +36,8 @@ constexpr int kMaxFinal = kMaxK * VA_BEAM_MAX_BEAMS;                  // a reque
 constexpr int kWarps = kThreads / 32;
 
 struct BeamSmem {
-    uint64_t cand[kMaxMerge];   // tile: its candidates; row and request: the candidates that are ranked
+    uint64_t cand[kMaxMerge];   // run: its best so far, then a tile's candidates; row and request: what is ranked
+    uint64_t best[kMaxK];       // run: the new best
     uint64_t red[kWarps];
     uint32_t wmin[kWarps];
     float fred[kWarps], fsum[kWarps];
@@ -53,11 +58,11 @@ struct BeamArgs {
     int32_t *parents, *tokens;
     float* out_scores;
     unsigned *row_count, *group_count;
-    uint64_t* tile_keys;       // [rows][tiles][k]
-    float2* tile_stats;        // [rows][tiles] (maximum, sum of exp(l - maximum))
+    uint64_t* run_keys;        // [rows][tiles][k]: the rows' runs in order (at most as many as tiles)
+    float2* run_stats;         // [rows][tiles] (maximum, sum of exp(l - maximum))
     uint64_t* row_keys;        // [rows][k] order-preserving images of the scores, 0 = none
     int32_t* row_tokens;       // [rows][k]
-    int vocab, n_beams, k, end_token;
+    int vocab, n_beams, k, end_token, n_tiles, n_rows;
 };
 
 // Order-preserving image of a score: 0 for -inf and NaN (no candidate).
@@ -71,14 +76,14 @@ __device__ __forceinline__ double key_score(uint64_t k) {
     return __longlong_as_double((long long)((k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k));
 }
 
-// One arrival (release of the block's stores before it, acquire of the others'); every thread learns whether it
-// was the last of n.  The last one resets the counter.
-__device__ __forceinline__ bool arrive_last(unsigned* counter, int n, int* flag) {
+// `mine` arrivals of n (release of the block's stores before them, acquire of the others'); every thread learns
+// whether they were the last.  The last one resets the counter.
+__device__ __forceinline__ bool arrive_last(unsigned* counter, int mine, int n, int* flag) {
     __syncthreads();
     if (threadIdx.x == 0) {
         unsigned prev;
-        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(counter) : "memory");
-        *flag = prev == (unsigned)(n - 1);
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(prev) : "l"(counter), "r"(mine) : "memory");
+        *flag = prev + (unsigned)mine == (unsigned)n;
         if (*flag) *counter = 0u;
     }
     __syncthreads();
@@ -89,172 +94,286 @@ template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs a) {
     __shared__ BeamSmem sm;
     constexpr int kVec = kBf16 ? 8 : 4, kBytes = kBf16 ? 2 : 4;   // logits per 16 bytes
-    const int tile = blockIdx.x, row = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n_tiles = gridDim.x, k = a.k, first = tile * kTileLogits;
-    const unsigned char* src = static_cast<const unsigned char*>(a.logits) + (size_t)row * a.stride * kBytes;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n_tiles = a.n_tiles, k = a.k;
+    // this CTA's share of the (row, tile) units, in order
+    const unsigned units = (unsigned)a.n_rows * n_tiles;      // at most 2^20, by fewer than 2^11 CTAs
+    const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+    auto row_at = [&](int row) { return static_cast<const unsigned char*>(a.logits) + (size_t)row * a.stride * kBytes; };
+    auto prefetch = [&](int u) {
+        if (tid == 0 && u < u1) {
+            const int first = u % n_tiles * kTileLogits, n = min(kTileLogits, a.vocab - first) * kBytes & ~15;
+            if (n > 0) ptx::bulk_prefetch_l2(row_at(u / n_tiles) + (size_t)first * kBytes, (uint32_t)n);
+        }
+    };
     ptx::griddep_launch_dependents();
-    if (tid == 0) {   // pulled into L2 before the dependency resolves, as in the sampler
-        const int n = min(kTileLogits, a.vocab - first) * kBytes & ~15;
-        if (n > 0) ptx::bulk_prefetch_l2(src + (size_t)first * kBytes, (uint32_t)n);
-    }
+    prefetch(u0);          // pulled into L2 before the dependency resolves, as in the sampler
     ptx::griddep_wait();
-    const bool done = a.finished && __ldcg(a.finished + row) != 0;
-    if (done && tile > 0) return;
-    const float base = __ldcg(a.scores + row);
-    if (!done) {
-        // ------------------------------------------------------------ tile
-        float f[kPerThread];
-        const int n_in = min(kTileLogits, a.vocab - first);
-        uint4 raw[kPerThread / kVec];
+    const float l2e = 1.4426950408889634f;
+    int run = 0;                            // tiles of the run so far
+    float m = -INFINITY, sum = 0.0f;        // this thread's maximum of them, and its sum of exp(l - m)
+    for (int u = u0; u < u1; ++u) {
+        const int row = u / n_tiles, tile = u % n_tiles, first = tile * kTileLogits;
+        const unsigned char* src = row_at(row);
+        prefetch(u + 1);
+        const bool done = a.finished && __ldcg(a.finished + row) != 0;
+        const float base = __ldcg(a.scores + row);
+        if (!done) {
+            // -------------------------------------------------------- tile
+            float f[kPerThread];
+            const int n_in = min(kTileLogits, a.vocab - first);
 #pragma unroll
-        for (int i = 0; i < kPerThread / kVec; ++i) {
-            const int at = (i * kThreads + tid) * kVec;
-            if (at + kVec <= n_in) {
-                raw[i] = __ldcs(reinterpret_cast<const uint4*>(src + (size_t)(first + at) * kBytes));
-            } else {   // the row's end: entry by entry, -inf behind it
+            for (int i = 0; i < kPerThread / kVec; ++i) {
+                const int at = (i * kThreads + tid) * kVec;
                 uint32_t w[4];
+                if (at + kVec <= n_in) {
+                    const uint4 raw = __ldcs(reinterpret_cast<const uint4*>(src + (size_t)(first + at) * kBytes));
+                    w[0] = raw.x;
+                    w[1] = raw.y;
+                    w[2] = raw.z;
+                    w[3] = raw.w;
+                } else {   // the row's end: entry by entry, -inf behind it
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (kBf16) {
-                        uint32_t v = 0;
+                    for (int c = 0; c < 4; ++c) {
+                        if (kBf16) {
+                            uint32_t v = 0;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int x = at + 2 * c + e;
-                            v |= (x < n_in ? (uint32_t)*reinterpret_cast<const uint16_t*>(src + (size_t)(first + x) * 2) : 0xFF80u)
-                                 << (16 * e);
+                            for (int e = 0; e < 2; ++e) {
+                                const int x = at + 2 * c + e;
+                                v |= (x < n_in ? (uint32_t)*reinterpret_cast<const uint16_t*>(src + (size_t)(first + x) * 2) : 0xFF80u)
+                                     << (16 * e);
+                            }
+                            w[c] = v;
+                        } else {
+                            const int x = at + c;
+                            w[c] = x < n_in ? *reinterpret_cast<const uint32_t*>(src + (size_t)(first + x) * 4) : 0xFF800000u;
                         }
-                        w[c] = v;
-                    } else {
-                        const int x = at + c;
-                        w[c] = x < n_in ? *reinterpret_cast<const uint32_t*>(src + (size_t)(first + x) * 4) : 0xFF800000u;
                     }
                 }
-                raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    const float x = kBf16 ? __uint_as_float((c & 1) ? (w[c / 2] & 0xFFFF0000u) : (w[c / 2] << 16))
+                                          : __uint_as_float(w[c & 3]);
+                    f[i * kVec + c] = fmaxf(x, -INFINITY);      // a NaN is no candidate: -inf
+                }
             }
-        }
-        float mine = -INFINITY;      // the thread's largest (NaN is passed over)
+            float mine = -INFINITY;      // the thread's largest
 #pragma unroll
-        for (int i = 0; i < kPerThread / kVec; ++i) {
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            for (int e = 0; e < kPerThread; ++e) mine = fmaxf(mine, f[e]);
+            // sums, as 2^(l log2 e + off); a maximum for which off has no digits takes the careful way
+            if (mine > -INFINITY) {
+                const float up = fmaxf(m, mine), off = -up * l2e;
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                const float x = kBf16 ? __uint_as_float((c & 1) ? (w[c / 2] & 0xFFFF0000u) : (w[c / 2] << 16))
-                                      : __uint_as_float(w[c & 3]);
-                f[i * kVec + c] = x;
-                mine = fmaxf(mine, x);
+                for (int e = 0; e < kPerThread; ++e) part[e & 3] += ptx::ex2(fmaf(f[e], l2e, off));
+                float add = (part[0] + part[1]) + (part[2] + part[3]);
+                if (!(fabsf(up) < 1024.0f)) {
+                    add = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < kPerThread; ++e) add += f[e] == up ? 1.0f : ptx::ex2((f[e] - up) * l2e);
+                }
+                sum = (m == up ? sum : (m == -INFINITY ? 0.0f : sum * ptx::ex2((m - up) * l2e))) + add;
+                m = up;
             }
-        }
-        // The tile's maximum, and tau, a lower bound of its k-th largest logit: with f warps whose 32 threads all hold
-        // logits and j = ceil(k / f), the smallest over those warps of the warp's j-th largest distinct thread maximum
-        // (one warp-wide maximum a round).  Fewer than 32 threads of logits: every logit is a candidate.
-        const int full_warps = min(kThreads, (n_in + kVec - 1) / kVec) / 32;
-        const int rounds = full_warps > 0 ? (k + full_warps - 1) / full_warps : 1;
-        uint32_t v = ord_bits(mine), low = 0u;
-        for (int r = 0; r < rounds; ++r) {
-            low = __reduce_max_sync(0xffffffffu, v);
-            if (r == 0 && lane == 0) sm.fred[warp] = ord_to_float(low);
-            v = v == low ? 0u : v;
-        }
-        if (lane == 0) sm.wmin[warp] = warp < full_warps ? low : 0xFFFFFFFFu;
-        if (tid == 0) sm.n_cand = 0;
-        __syncthreads();
-        float mx = sm.fred[0];
-        uint32_t tau_bits = sm.wmin[0];
+            // the bound that candidates have to pass
+            const int held = run > 0 ? k : 0;
+            float tau;
+            if (run > 0) {
+                const uint64_t kth = sm.cand[k - 1];
+                tau = kth != 0ull ? ord_to_float((uint32_t)(kth >> 32) + 1u) : -FLT_MAX;   // the next larger float
+            } else {
+                // A lower bound of the tile's k-th largest logit: with f warps whose 32 threads all hold logits and
+                // j = ceil(k / f), the smallest over those warps of the warp's j-th largest distinct thread maximum
+                // (one warp-wide maximum a round).  Fewer than 32 threads of logits: every logit is a candidate.
+                const int full_warps = min(kThreads, (n_in + kVec - 1) / kVec) / 32;
+                const int rounds = full_warps > 0 ? (k + full_warps - 1) / full_warps : 1;
+                uint32_t v = ord_bits(mine), low = 0u;
+                for (int r = 0; r < rounds; ++r) {
+                    low = __reduce_max_sync(0xffffffffu, v);
+                    v = v == low ? 0u : v;
+                }
+                if (lane == 0) sm.wmin[warp] = warp < full_warps ? low : 0xFFFFFFFFu;
+                __syncthreads();
+                uint32_t least = sm.wmin[0];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            mx = fmaxf(mx, sm.fred[w]);
-            tau_bits = min(tau_bits, sm.wmin[w]);
-        }
-        if (full_warps == 0) tau_bits = 0u;
-        // candidates are at or above tau and above -inf (tau_bits 0 and NaN's image: all that are above -inf)
-        const float tau = tau_bits > ord_bits(-INFINITY) ? ord_to_float(tau_bits) : -FLT_MAX;
-        // exp(l - mx) as 2^(l log2 e + off): within 2^-22 for the terms that weigh anything, but for the rounding of
-        // off, which all share and which is taken out of their sum.  (A maximum that is infinite or so large that
-        // off would not hold its digits: the difference first.)
-        const float l2e = 1.4426950408889634f;
-        const bool plain = fabsf(mx) < 1024.0f;
-        const float off = plain ? -mx * l2e : 0.0f, shared_error = plain ? fmaf(mx, l2e, off) : 0.0f;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        unsigned bits = 0;
-        if (plain) {
+                for (int w = 1; w < kWarps; ++w) least = min(least, sm.wmin[w]);
+                if (full_warps == 0) least = 0u;
+                tau = least > ord_bits(-INFINITY) ? ord_to_float(least) : -FLT_MAX;
+            }
+            unsigned bits = 0;
+            if (mine >= tau) {
 #pragma unroll
-            for (int e = 0; e < kPerThread; ++e)
-                if (f[e] == f[e]) sum[e & 3] += ptx::ex2(fmaf(f[e], l2e, off));
-        } else if (mx > -INFINITY) {
+                for (int e = 0; e < kPerThread; ++e) bits |= f[e] >= tau ? 1u << e : 0u;
+            }
+            if (tid == 0) sm.n_cand = held;
+            if (__syncthreads_or(bits != 0)) {
+                // compaction behind the best so far: a warp's candidates take consecutive places; the values are read
+                // again (few are)
+                const int cnt = __popc(bits);
+                int incl = cnt;
 #pragma unroll
-            for (int e = 0; e < kPerThread; ++e)
-                if (f[e] == f[e]) sum[e & 3] += f[e] == mx ? 1.0f : ptx::ex2((f[e] - mx) * l2e);
-        }
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int t = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += t;
+                }
+                int slot = 0;
+                if (lane == 31 && incl > 0) slot = atomicAdd(&sm.n_cand, incl);
+                slot = __shfl_sync(0xffffffffu, slot, 31) + incl - cnt;
+                for (unsigned rest = bits; rest != 0; rest &= rest - 1) {
+                    const int e = __ffs(rest) - 1;
+                    const int at = first + ((e / kVec) * kThreads + tid) * kVec + e % kVec;
+                    const float x = kBf16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src)[at] << 16)
+                                          : reinterpret_cast<const float*>(src)[at];
+                    if (slot < held + kMaxCand) sm.cand[slot] = make_key(x, at);
+                    ++slot;
+                }
+                if (tid < k) sm.best[tid] = 0ull;
+                __syncthreads();
+                int n = sm.n_cand;
+                if (n > held + kMaxCand) {
+                    // many equal logits at the bound: the tile's k best by k rounds of block-wide maximum
+                    uint64_t taken = ~0ull;
+                    for (int r = 0; r < k; ++r) {
+                        uint64_t best = 0;
 #pragma unroll
-        for (int e = 0; e < kPerThread; ++e) bits |= f[e] >= tau ? 1u << e : 0u;
-        float part = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        for (int e = 0; e < kPerThread; ++e) {
+                            const uint64_t kv = f[e] >= tau ? make_key(f[e], first + ((e / kVec) * kThreads + tid) * kVec + e % kVec) : 0ull;
+                            best = kv < taken && kv > best ? kv : best;
+                        }
+                        best = block_max_u64(best, sm.red);
+                        if (tid == 0) sm.cand[held + r] = best;
+                        taken = best;
+                    }
+                    n = held + k;
+                    __syncthreads();
+                }
+                // rank by counting: a key goes to the place of the number of larger ones, if that is below k
+                for (int c = tid; c < n; c += kThreads) {
+                    const uint64_t kc = sm.cand[c];
+                    int rank = 0;
+#pragma unroll 8
+                    for (int o = 0; o < n; ++o) rank += sm.cand[o] > kc;
+                    if (rank < k && kc != 0ull) sm.best[rank] = kc;
+                }
+                __syncthreads();
+                if (tid < k) sm.cand[tid] = sm.best[tid];
+            } else if (run == 0 && tid < k) {
+                sm.cand[tid] = 0ull;
+            }
+            __syncthreads();
+            ++run;
+            if (tile != n_tiles - 1 && u + 1 != u1) continue;
+            // -------------------------------------------------------- the run's end
+            const int c_first = (int)(((unsigned)(row * n_tiles + 1) * gridDim.x - 1u) / units);
+            const int c_last = (int)(((unsigned)((row + 1) * n_tiles) * gridDim.x - 1u) / units);
+            const int n_runs = c_last - c_first + 1;
+            float top = m;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-        if (lane == 0) sm.fsum[warp] = part;
-        // compaction: a warp's candidates take consecutive places; their values are read again (few are)
-        const int cnt = __popc(bits);
-        int incl = cnt;
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (lane == 0) sm.fred[warp] = top;
+            __syncthreads();
+            top = sm.fred[0];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += t;
-        }
-        int slot = 0;
-        if (lane == 31 && incl > 0) slot = atomicAdd(&sm.n_cand, incl);
-        slot = __shfl_sync(0xffffffffu, slot, 31) + incl - cnt;
-        for (unsigned rest = bits; rest != 0; rest &= rest - 1) {
-            const int e = __ffs(rest) - 1;
-            const int at = first + ((e / kVec) * kThreads + tid) * kVec + e % kVec;
-            const float x = kBf16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src)[at] << 16)
-                                  : reinterpret_cast<const float*>(src)[at];
-            if (slot < kMaxCand) sm.cand[slot] = make_key(x, at);
-            ++slot;
-        }
-        __syncthreads();
-        const int n_cand = sm.n_cand;
-        if (tid == 0) {
-            float all = 0.0f;
+            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm.fred[w]);
+            float all = m == top ? (top > -INFINITY ? sum : 0.0f) : (m == -INFINITY ? 0.0f : sum * ptx::ex2((m - top) * l2e));
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) all += sm.fsum[w];
-            a.tile_stats[(size_t)row * n_tiles + tile] = make_float2(mx, mx > -INFINITY ? fmaf(all, -0.69314718f * shared_error, all) : 0.0f);
-        }
-        uint64_t* keys_out = a.tile_keys + ((size_t)row * n_tiles + tile) * k;
-        if (n_cand <= kMaxCand) {
-            // rank by counting: a candidate goes to the place of the number of larger ones, if that is below k
-            for (int c = tid; c < n_cand; c += kThreads) {
+            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+            if (lane == 0) sm.fsum[warp] = all;
+            __syncthreads();
+            const size_t place = (size_t)row * n_tiles + (blockIdx.x - c_first);
+            if (tid == 0) {
+                all = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) all += sm.fsum[w];
+                a.run_stats[place] = make_float2(top, all);
+            }
+            if (tid < k) a.run_keys[place * k + tid] = sm.cand[tid];
+            run = 0;
+            m = -INFINITY;
+            sum = 0.0f;
+            if (!arrive_last(a.row_count + row, 1, n_runs, &sm.last)) continue;
+            // -------------------------------------------------------- row
+            const uint64_t* rw = a.run_keys + (size_t)row * n_tiles * k;
+            const int total = n_runs * k;
+            for (int e = tid; e < total; e += kThreads) sm.all[e] = __ldcg(rw + e);
+            __syncthreads();
+            if (warp == 0) {
+                // a lower bound of the row's k-th key: the smallest of every run's ceil(k / runs)-th
+                const int m = min(k, (k + n_runs - 1) / n_runs);
+                uint64_t b = ~0ull;
+                if (lane < n_runs) b = sm.all[lane * k + m - 1];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const uint64_t w = __shfl_xor_sync(0xffffffffu, b, o);
+                    b = w < b ? w : b;
+                }
+                if (lane == 0) {
+                    sm.tau = b;
+                    sm.n_cand = 0;
+                }
+                // log-sum-exp over the runs, one a lane
+                const float2 st = lane < n_runs ? __ldcg(a.run_stats + (size_t)row * n_tiles + lane) : make_float2(-INFINITY, 0.0f);
+                float top = st.x;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                double s = st.x == -INFINITY ? 0.0 : (st.x == top ? (double)st.y : (double)(st.y * expf(st.x - top)));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane == 0) {
+                    sm.max = (double)top;
+                    sm.log_sum = log(s);
+                }
+            } else if (warp == 1) {
+                sm.top[lane] = 0ull;
+            }
+            __syncthreads();
+            const uint64_t lb = sm.tau;
+            for (int e = tid; e < total; e += kThreads) {
+                const uint64_t kv = sm.all[e];
+                if (kv >= lb && kv != 0ull) sm.cand[atomicAdd(&sm.n_cand, 1)] = kv;
+            }
+            __syncthreads();
+            const int nc = sm.n_cand;
+            for (int c = tid; c < nc; c += kThreads) {
                 const uint64_t kc = sm.cand[c];
                 int rank = 0;
 #pragma unroll 8
-                for (int o = 0; o < n_cand; ++o) rank += sm.cand[o] > kc;
-                if (rank < k) keys_out[rank] = kc;
+                for (int o = 0; o < nc; ++o) rank += sm.cand[o] > kc;
+                if (rank < k) sm.top[rank] = kc;
             }
-            for (int r = n_cand + tid; r < k; r += kThreads) keys_out[r] = 0ull;
-        } else {
-            // many equal logits at the bound: k rounds of block-wide maximum over every logit
-            uint64_t taken = ~0ull;
-            for (int r = 0; r < k; ++r) {
-                uint64_t best = 0;
-#pragma unroll
-                for (int e = 0; e < kPerThread; ++e) {
-                    const uint64_t kv = f[e] > -INFINITY ? make_key(f[e], first + ((e / kVec) * kThreads + tid) * kVec + e % kVec) : 0ull;
-                    best = kv < taken && kv > best ? kv : best;
+            __syncthreads();
+            if (tid < k) {
+                const uint64_t kv = sm.top[tid];
+                uint64_t sk = 0ull;
+                if (kv != 0ull) {
+                    const double l = (double)ord_to_float((uint32_t)(kv >> 32));
+                    const double above = l == sm.max ? 0.0 : l - sm.max;
+                    sk = score_key((double)base + (above - sm.log_sum));
                 }
-                best = block_max_u64(best, sm.red);
-                if (tid == 0) keys_out[r] = best;
-                taken = best;
+                a.row_keys[(size_t)row * k + tid] = sk;
+                a.row_tokens[(size_t)row * k + tid] = key_index(kv);
+            }
+        } else {
+            // a finished hypothesis: the CTA that has its last tile speaks for it
+            if (tile != n_tiles - 1) continue;
+            if (tid < k) {
+                a.row_keys[(size_t)row * k + tid] = tid == 0 ? score_key((double)base) : 0ull;
+                a.row_tokens[(size_t)row * k + tid] = a.end_token;
             }
         }
-        if (!arrive_last(a.row_count + row, n_tiles, &sm.last)) return;
-        // -------------------------------------------------------- row
-        const uint64_t* rw = a.tile_keys + (size_t)row * n_tiles * k;
-        const int total = n_tiles * k;
-        for (int e = tid; e < total; e += kThreads) sm.all[e] = __ldcg(rw + e);
+        // ---------------------------------------------------------------- request
+        const int group = row / a.n_beams;
+        if (!arrive_last(a.group_count + group, 1, a.n_beams, &sm.last)) continue;
+        const int total = a.n_beams * k;
+        const size_t at = (size_t)group * total;
+        for (int e = tid; e < total; e += kThreads) {
+            sm.all[e] = __ldcg(a.row_keys + at + e);
+            sm.tok[e] = __ldcg(a.row_tokens + at + e);
+        }
         __syncthreads();
-        if (warp == 0) {
-            // a lower bound of the row's k-th key: the smallest of every tile's ceil(k / tiles)-th
-            const int m = min(k, (k + n_tiles - 1) / n_tiles);
-            uint64_t b = ~0ull;
-            if (lane < n_tiles) b = sm.all[lane * k + m - 1];
+        if (warp == 0) {   // a lower bound of the k-th score: the smallest of every hypothesis' ceil(k / beams)-th
+            const int m = (k + a.n_beams - 1) / a.n_beams;
+            uint64_t b = lane < a.n_beams ? sm.all[lane * k + m - 1] : ~0ull;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 const uint64_t w = __shfl_xor_sync(0xffffffffu, b, o);
@@ -264,104 +383,38 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs
                 sm.tau = b;
                 sm.n_cand = 0;
             }
-            // log-sum-exp over the tiles, one a lane
-            const float2 st = lane < n_tiles ? __ldcg(a.tile_stats + (size_t)row * n_tiles + lane) : make_float2(-INFINITY, 0.0f);
-            float top = st.x;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            double s = st.x == -INFINITY ? 0.0 : (st.x == top ? (double)st.y : (double)(st.y * expf(st.x - top)));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == 0) {
-                sm.max = (double)top;
-                sm.log_sum = log(s);
-            }
-        } else if (warp == 1) {
-            sm.top[lane] = 0ull;
         }
         __syncthreads();
         const uint64_t lb = sm.tau;
         for (int e = tid; e < total; e += kThreads) {
             const uint64_t kv = sm.all[e];
-            if (kv >= lb && kv != 0ull) sm.cand[atomicAdd(&sm.n_cand, 1)] = kv;
+            if (kv >= lb && kv != 0ull) {
+                const int i = atomicAdd(&sm.n_cand, 1);
+                sm.cand[i] = kv;
+                sm.who[i] = (int16_t)e;
+            }
         }
         __syncthreads();
         const int nc = sm.n_cand;
+        const size_t out = (size_t)group * k;
         for (int c = tid; c < nc; c += kThreads) {
             const uint64_t kc = sm.cand[c];
+            const int e = sm.who[c];
             int rank = 0;
-#pragma unroll 8
-            for (int o = 0; o < nc; ++o) rank += sm.cand[o] > kc;
-            if (rank < k) sm.top[rank] = kc;
+#pragma unroll 4
+            for (int o = 0; o < nc; ++o) rank += sm.cand[o] > kc || (sm.cand[o] == kc && sm.who[o] < e);
+            if (rank < k) {
+                a.parents[out + rank] = e / k;
+                a.tokens[out + rank] = sm.tok[e];
+                a.out_scores[out + rank] = (float)key_score(kc);
+            }
+        }
+        for (int r = nc + tid; r < k; r += kThreads) {
+            a.parents[out + r] = -1;
+            a.tokens[out + r] = -1;
+            a.out_scores[out + r] = -INFINITY;
         }
         __syncthreads();
-        if (tid < k) {
-            const uint64_t kv = sm.top[tid];
-            uint64_t sk = 0ull;
-            if (kv != 0ull) {
-                const double l = (double)ord_to_float((uint32_t)(kv >> 32));
-                const double above = l == sm.max ? 0.0 : l - sm.max;
-                sk = score_key((double)base + (above - sm.log_sum));
-            }
-            a.row_keys[(size_t)row * k + tid] = sk;
-            a.row_tokens[(size_t)row * k + tid] = key_index(kv);
-        }
-    } else if (tid < k) {
-        a.row_keys[(size_t)row * k + tid] = tid == 0 ? score_key((double)base) : 0ull;
-        a.row_tokens[(size_t)row * k + tid] = a.end_token;
-    }
-    // ---------------------------------------------------------------- request
-    const int group = row / a.n_beams;
-    if (!arrive_last(a.group_count + group, a.n_beams, &sm.last)) return;
-    const int total = a.n_beams * k;
-    const size_t at = (size_t)group * total;
-    for (int e = tid; e < total; e += kThreads) {
-        sm.all[e] = __ldcg(a.row_keys + at + e);
-        sm.tok[e] = __ldcg(a.row_tokens + at + e);
-    }
-    __syncthreads();
-    if (warp == 0) {   // a lower bound of the k-th score: the smallest of every hypothesis' ceil(k / beams)-th
-        const int m = (k + a.n_beams - 1) / a.n_beams;
-        uint64_t b = lane < a.n_beams ? sm.all[lane * k + m - 1] : ~0ull;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const uint64_t w = __shfl_xor_sync(0xffffffffu, b, o);
-            b = w < b ? w : b;
-        }
-        if (lane == 0) {
-            sm.tau = b;
-            sm.n_cand = 0;
-        }
-    }
-    __syncthreads();
-    const uint64_t lb = sm.tau;
-    for (int e = tid; e < total; e += kThreads) {
-        const uint64_t kv = sm.all[e];
-        if (kv >= lb && kv != 0ull) {
-            const int i = atomicAdd(&sm.n_cand, 1);
-            sm.cand[i] = kv;
-            sm.who[i] = (int16_t)e;
-        }
-    }
-    __syncthreads();
-    const int nc = sm.n_cand;
-    const size_t out = (size_t)group * k;
-    for (int c = tid; c < nc; c += kThreads) {
-        const uint64_t kc = sm.cand[c];
-        const int e = sm.who[c];
-        int rank = 0;
-#pragma unroll 4
-        for (int o = 0; o < nc; ++o) rank += sm.cand[o] > kc || (sm.cand[o] == kc && sm.who[o] < e);
-        if (rank < k) {
-            a.parents[out + rank] = e / k;
-            a.tokens[out + rank] = sm.tok[e];
-            a.out_scores[out + rank] = (float)key_score(kc);
-        }
-    }
-    for (int r = nc + tid; r < k; r += kThreads) {
-        a.parents[out + r] = -1;
-        a.tokens[out + r] = -1;
-        a.out_scores[out + r] = -INFINITY;
     }
 }
 
@@ -403,17 +456,21 @@ va_status va_beam_select(const void* logits, int format, int64_t row_stride, int
     a.row_count = reinterpret_cast<unsigned*>(p);
     a.group_count = a.row_count + va::beam::kMaxRows;
     p += va::beam::kCounterBytes;
-    a.tile_keys = reinterpret_cast<uint64_t*>(p);
+    a.run_keys = reinterpret_cast<uint64_t*>(p);
     p += rows * tiles * n_out * 8;
-    a.tile_stats = reinterpret_cast<float2*>(p);
+    a.run_stats = reinterpret_cast<float2*>(p);
     p += rows * tiles * 8;
     a.row_keys = reinterpret_cast<uint64_t*>(p);
     p += rows * n_out * 8;
     a.row_tokens = reinterpret_cast<int32_t*>(p);
     a.vocab = vocab; a.n_beams = n_beams; a.k = n_out; a.end_token = end_token;
+    a.n_tiles = tiles; a.n_rows = (int)rows;
+    // a CTA a tile while there are no more than fit at once (three an SM), else even shares of them
+    const int sms = va::device_sm_count();
+    const long long units = (long long)rows * tiles, most = 3ll * (sms > 0 ? sms : 148);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    va::pdl_config(&cfg, attr, dim3(tiles, (unsigned)rows), dim3(va::smp::kThreads), 0, (cudaStream_t)stream);
+    va::pdl_config(&cfg, attr, dim3((unsigned)(units < most ? units : most)), dim3(va::smp::kThreads), 0, (cudaStream_t)stream);
     return va::paged::launched(format == VA_LOGITS_BF16
                                    ? cudaLaunchKernelEx(&cfg, va::beam::beam_select_kernel<true>, a)
                                    : cudaLaunchKernelEx(&cfg, va::beam::beam_select_kernel<false>, a));
