@@ -331,9 +331,20 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
+_torch = None
+
+
+def _import_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _at(t, count: int, size: int, what: str) -> int:
     """Address of a dense tensor of `count` elements of `size` bytes (the C ABI takes no strides)."""
-    if t.numel() != count or t.itemsize != size or not t.is_contiguous():
+    if t.nbytes != count * size or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous tensor of {count} elements of {size} bytes")
     return t.data_ptr()
 
@@ -350,7 +361,7 @@ def _opt(t, count: int, size: int, what: str):
 
 def _launch(fn: str, call, t, stream, *args) -> None:
     """Call an entry point on the stream given, or on the current one of t's device, with that device current."""
-    import torch
+    torch = _torch or _import_torch()
     index = t.get_device()
     if index >= 0 and index != torch.cuda.current_device():
         with torch.cuda.device(index):
@@ -365,16 +376,16 @@ def _launch(fn: str, call, t, stream, *args) -> None:
 
 def _pool(k_codes, v_codes, k_scale, v_scale):
     """(layers, pages, kv heads, format, four addresses) of pools [pages, heads, 64, 128] or [layers, pages, ...]."""
-    import torch
-    *outer, heads, page, d = k_codes.shape
-    if not (len(outer) in (1, 2) and page == TILE and d == HEAD_DIM and v_codes.shape == k_codes.shape
-            and v_codes.dtype is k_codes.dtype and k_scale.shape == v_scale.shape
-            and tuple(k_scale.shape) == (*outer, heads, TILE // B8_BLOCK)):
+    torch = _torch or _import_torch()
+    shape, kind = k_codes.shape, k_codes.dtype
+    n = k_codes.nbytes
+    if not (4 <= len(shape) <= 5 and shape[-1] == HEAD_DIM and shape[-2] == TILE and v_codes.dtype is kind
+            and v_codes.shape == shape and k_scale.shape[-1] == TILE // B8_BLOCK):
         raise ValueError("pools are codes [..., pages, heads, 64, 128] of one 8-bit type and scales [..., pages, heads, 4]")
-    n, ns = k_codes.numel(), k_scale.numel()
-    return (outer[0] if len(outer) == 2 else 1, outer[-1], heads, B8_INT8 if k_codes.dtype is torch.int8 else B8_E4M3,
-            _at(k_codes, n, 1, "codes"), _at(v_codes, n, 1, "codes"), _at(k_scale, ns, 4, "scales"),
-            _at(v_scale, ns, 4, "scales"))
+    scales = n // (HEAD_DIM * B8_BLOCK)
+    return (shape[0] if len(shape) == 5 else 1, shape[-4], shape[-3], B8_INT8 if kind is torch.int8 else B8_E4M3,
+            _at(k_codes, n, 1, "codes"), _at(v_codes, n, 1, "codes"), _at(k_scale, scales, 4, "scales"),
+            _at(v_scale, scales, 4, "scales"))
 
 
 def _table(table, n: int):
@@ -476,7 +487,7 @@ def va_beam_select(logits, scores, n_beams: int, parents, tokens, out_scores, wo
     """The best n_out continuations of each request's n_beams hypotheses: logits [n_groups * n_beams, vocab] (float32
     or bfloat16, rows at any stride that keeps them 16-byte aligned), scores [n_groups * n_beams]; writes parents,
     tokens and out_scores [n_groups, n_out].  ``workspace``: va_beam_workspace_bytes(...) bytes, zeroed once."""
-    import torch
+    torch = _torch or _import_torch()
     rows, vocab = logits.shape
     groups, n_out = parents.shape
     stride, inner = logits.stride()
