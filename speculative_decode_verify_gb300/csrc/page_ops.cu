@@ -71,46 +71,61 @@ struct ExtendArgs {
 };
 
 struct PlanSmem {
-    int x0[kMaxSeqs], n[kMaxSeqs], base[kMaxSeqs];   // first entry, entries and first new page of a sequence
+    int x0[kMaxSeqs], upto[kMaxSeqs];                // a sequence's first entry; entries of the sequences up to it
     int sums[kPlanWarps + 1];
     int counts[kScan * kPlanWarps];
     int status, pairs, found;
 };
 
+// The table entries of all pages that will be written, numbered in order of (slot, entry), a thread each: a decode
+// step's are one or two a slot, so that a pass over them is one round trip to memory.  Pages of one reference stay
+// with their entry and need nothing; only for shared ones the holders are counted and the first one found.
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendArgs a) {
     __shared__ PlanSmem sm;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) sm.status = sm.pairs = sm.found = 0;
-    __syncthreads();
-    int status = 0, len = 0, add = 0;
+    int status = 0, len = 0, add = 0, mine = 0;
     if (tid < a.n_seqs) {
         len = a.lens[tid];
         add = a.n_new[tid];
         const long long end = (long long)len + add;
         if (len < 0 || add < 0) status |= VA_DEV_BAD_COUNT;
         else if (end > (long long)a.max_pages * kPage) status |= VA_DEV_BEYOND_CACHE;
-        const bool some = !status && add > 0;
-        sm.x0[tid] = some ? len / kPage : 0;
-        sm.n[tid] = some ? (int)((end + kPage - 1) / kPage) - len / kPage : 0;
+        if (!status && add > 0) mine = (int)((end + kPage - 1) / kPage) - len / kPage;
+        sm.x0[tid] = len / kPage;
     }
+    const int upto = block_scan(mine, sm.sums);
+    if (tid < a.n_seqs) sm.upto[tid] = upto;
+    const int entries = sm.sums[kPlanWarps];
     __syncthreads();
-    // the pages to be written: counted from zero holders
-    for (int b = warp; b < a.n_seqs; b += kPlanWarps) {
-        const int32_t* row = a.table + (size_t)b * a.max_pages + sm.x0[b];
-        for (int e = lane; e < sm.n[b]; e += 32) {
-            const int p = row[e];
-            if (p < -1 || p >= a.n_pages || (p >= 0 && a.refs[p] < 1)) {
-                status |= VA_DEV_BAD_PAGE;
-            } else if (p >= 0) {
-                a.w.holders[p] = 0;
-                a.w.first[p] = 0x7FFFFFFF;
-            }
+    // entry i: its slot (the first whose entries reach past i), place in the table and page
+    auto slot_of = [&](int i) {
+        int lo = 0, hi = a.n_seqs - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (sm.upto[mid] > i) hi = mid;
+            else lo = mid + 1;
+        }
+        return lo;
+    };
+    auto in_slot = [&](int i, int b) { return i - (b > 0 ? sm.upto[b - 1] : 0); };
+    auto place = [&](int i, int b) { return b * a.max_pages + sm.x0[b] + in_slot(i, b); };
+    bool shared = false;
+    for (int i = tid; i < entries; i += kPlanThreads) {
+        const int p = a.table[place(i, slot_of(i))];
+        const int r = p >= 0 && p < a.n_pages ? a.refs[p] : 0;
+        if (p < -1 || p >= a.n_pages || (p >= 0 && r < 1)) {
+            status |= VA_DEV_BAD_PAGE;
+        } else if (r > 1) {
+            shared = true;
+            a.w.holders[p] = 0;
+            a.w.first[p] = 0x7FFFFFFF;
         }
     }
     if (status) atomicOr(&sm.status, status);
-    __syncthreads();
+    const bool some_shared = __syncthreads_or(shared);
     if (sm.status) {
         if (tid == 0) {
             *a.w.n_pairs = 0;
@@ -118,44 +133,30 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendA
         }
         return;
     }
-    for (int b = warp; b < a.n_seqs; b += kPlanWarps) {
-        const int at = b * a.max_pages + sm.x0[b];
-        for (int e = lane; e < sm.n[b]; e += 32) {
-            const int p = a.table[at + e];
-            if (p >= 0) {
+    if (some_shared) {
+        for (int i = tid; i < entries; i += kPlanThreads) {
+            const int p = a.table[place(i, slot_of(i))];
+            if (p >= 0 && a.refs[p] > 1) {
                 atomicAdd(a.w.holders + p, 1);
-                atomicMin(a.w.first + p, at + e);
+                atomicMin(a.w.first + p, i);
             }
         }
-    }
-    __syncthreads();
-    // first[p] stays the entry that keeps page p, or becomes -1: its first holder keeps it if no entry outside
-    // this call's pages names it
-    for (int b = warp; b < a.n_seqs; b += kPlanWarps) {
-        const int at = b * a.max_pages + sm.x0[b];
-        for (int e = lane; e < sm.n[b]; e += 32) {
-            const int p = a.table[at + e];
-            if (p >= 0 && __ldcg(a.w.first + p) == at + e && __ldcg(a.w.holders + p) != a.refs[p]) __stcg(a.w.first + p, -1);
+        __syncthreads();
+        // first[p] stays the entry that keeps page p, or becomes -1: its first holder keeps it if no entry outside
+        // this call's names it
+        for (int i = tid; i < entries; i += kPlanThreads) {
+            const int p = a.table[place(i, slot_of(i))];
+            if (p >= 0 && a.refs[p] > 1 && __ldcg(a.w.first + p) == i && __ldcg(a.w.holders + p) != a.refs[p])
+                __stcg(a.w.first + p, -1);
         }
+        __syncthreads();
     }
-    __syncthreads();
-    for (int b = warp; b < a.n_seqs; b += kPlanWarps) {
-        const int at = b * a.max_pages + sm.x0[b];
-        int need = 0;
-        for (int e0 = 0; e0 < sm.n[b]; e0 += 32) {
-            const int e = e0 + lane;
-            const int p = e < sm.n[b] ? a.table[at + e] : 0;
-            const bool fresh = e < sm.n[b] && (p < 0 || __ldcg(a.w.first + p) != at + e);
-            need += __popc(__ballot_sync(0xffffffffu, fresh));
-        }
-        if (lane == 0) sm.base[b] = need;
+    auto gets_new = [&](int i, int p) { return p < 0 || (a.refs[p] > 1 && __ldcg(a.w.first + p) != i); };
+    int total = 0;
+    for (int i0 = 0; i0 < entries; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        total += __syncthreads_count(i < entries && gets_new(i, a.table[place(i, slot_of(i))]));
     }
-    __syncthreads();
-    const int mine = tid < a.n_seqs ? sm.base[tid] : 0;
-    const int upto = block_scan(mine, sm.sums);
-    const int total = sm.sums[kPlanWarps];
-    if (tid < a.n_seqs) sm.base[tid] = upto - mine;
-    __syncthreads();
     // the `total` lowest-numbered free pages, in order
     for (int c0 = 0; c0 < a.n_pages && sm.found < total; c0 += kScan * kPlanThreads) {
         unsigned mask[kScan];
@@ -192,30 +193,37 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendA
         }
         return;
     }
-    for (int b = warp; b < a.n_seqs; b += kPlanWarps) {
-        const int at = b * a.max_pages + sm.x0[b];
-        int rank = sm.base[b];
-        for (int e0 = 0; e0 < sm.n[b]; e0 += 32) {
-            const int e = e0 + lane;
-            const int p = e < sm.n[b] ? a.table[at + e] : 0;
-            const bool fresh = e < sm.n[b] && (p < 0 || __ldcg(a.w.first + p) != at + e);
-            const unsigned who = __ballot_sync(0xffffffffu, fresh);
-            if (fresh) {
-                const int page = a.w.list[rank + __popc(who & ((1u << lane) - 1u))];
-                a.table[at + e] = page;
-                a.refs[page] = 1;
-                if (p >= 0) {
-                    atomicSub(a.refs + p, 1);
-                    // only the first entry can hold positions already
-                    if (e == 0 && a.lens[b] % kPage != 0) {
-                        const int i = atomicAdd(&sm.pairs, 1);
-                        a.w.src[i] = p;
-                        a.w.dst[i] = page;
-                    }
-                }
-            }
-            rank += __popc(who);
+    // Hand them out; the list keeps the shared page that each replaces, whose count changes once all have chosen.
+    int rank0 = 0;
+    for (int i0 = 0; i0 < entries; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        int at = 0, b = 0, p = 0;
+        bool fresh = false;
+        if (i < entries) {
+            b = slot_of(i);
+            at = place(i, b);
+            p = a.table[at];
+            fresh = gets_new(i, p);
         }
+        const int rank = rank0 + block_scan(fresh ? 1 : 0, sm.sums) - 1;
+        rank0 += sm.sums[kPlanWarps];
+        if (fresh) {
+            const int page = a.w.list[rank];
+            a.table[at] = page;
+            a.refs[page] = 1;
+            a.w.list[rank] = p;
+            // only a slot's first entry can hold positions already
+            if (p >= 0 && in_slot(i, b) == 0 && a.lens[b] % kPage != 0) {
+                const int j = atomicAdd(&sm.pairs, 1);
+                a.w.src[j] = p;
+                a.w.dst[j] = page;
+            }
+        }
+        __syncthreads();
+    }
+    for (int r = tid; r < total; r += kPlanThreads) {
+        const int p = a.w.list[r];
+        if (p >= 0) atomicSub(a.refs + p, 1);
     }
     __syncthreads();
     if (tid < a.n_seqs && add > 0) a.lens[tid] = len + add;
@@ -385,13 +393,12 @@ struct ReorderArgs {
 };
 
 constexpr int kReorderThreads = 256;
-constexpr int kReorderCells = 8192;   // entries that a CTA holds: all slots' of a few columns
 
-// A CTA takes all slots' entries of kCols columns: columns do not depend on one another, so the table is
-// rewritten in place.  The counts are sums of +1 and -1, whatever the order.
-template <int kCols>
+// A CTA takes all slots' entries of kCols columns (one 32-byte sector a row): columns do not depend on one another, so
+// the table is rewritten in place.  The counts are sums of +1 and -1, whatever the order.
+constexpr int kCols = 8;
 __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const ReorderArgs a) {
-    __shared__ int old[kReorderCells];
+    __shared__ int old[kMaxSeqs * kCols];
     __shared__ int from[kMaxSeqs];
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
@@ -403,6 +410,7 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const ReorderA
         if (!ok) status |= VA_DEV_BAD_COUNT;
         from[j] = !ok ? j : (s < 0 ? -1 : j / a.group * a.group + s);
     }
+#pragma unroll 8
     for (int c = tid; c < a.n_seqs * kCols; c += kReorderThreads) {
         const int j = c / kCols, x = x0 + c % kCols;
         old[c] = x < a.max_pages ? a.table[(size_t)j * a.max_pages + x] : -1;
@@ -496,12 +504,9 @@ va_status kv_page_reorder(int32_t* table, int32_t* lens, int n_seqs, int max_pag
     a.n_seqs = n_seqs; a.max_pages = max_pages; a.group = group > 0 ? group : n_seqs; a.n_pages = n_pages;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    // 32 columns (128-byte pieces of rows) while all slots' fit, else 8 (one 32-byte sector)
-    const int cols = n_seqs <= kReorderCells / 32 ? 32 : 8;
-    va::pdl_config(&cfg, attr, dim3((unsigned)((max_pages + cols - 1) / cols)), dim3(kReorderThreads), 0,
+    va::pdl_config(&cfg, attr, dim3((unsigned)((max_pages + kCols - 1) / kCols)), dim3(kReorderThreads), 0,
                    (cudaStream_t)stream);
-    return launched(cols == 32 ? cudaLaunchKernelEx(&cfg, reorder_kernel<32>, a)
-                               : cudaLaunchKernelEx(&cfg, reorder_kernel<8>, a));
+    return launched(cudaLaunchKernelEx(&cfg, reorder_kernel, a));
 }
 
 va_status kv_page_copy(const int32_t* src, const int32_t* dst, int n_pairs, int n_pages, int n_layers, int n_kv_heads,
