@@ -24,7 +24,8 @@ extern "C" {
  * with l its row of logits; a finished hypothesis continues with end_token alone, at scores[i].  The scores are
  * sums of 64 bits (the log-sum-exp's exponentials are summed in 32), so that near candidates of different
  * hypotheses keep their order; they are rounded once, at the end.  Equal scores: the lower hypothesis first, and
- * of one hypothesis the candidate order of spec_sample.h (larger logit, then lower token).  A logit of -inf or NaN is no candidate; where a row holds +inf, its +inf logits share the probability.
+ * of one hypothesis the candidate order of spec_sample.h (larger logit, then lower token).  A logit of -inf or NaN
+ * is no candidate; where a row holds +inf, its +inf logits share the probability.
  *   logits        device [n_groups * n_beams] rows of `vocab` entries, row_stride entries apart: fp32 (format
  *                 VA_LOGITS_F32; 16-byte aligned, row_stride a multiple of 4) or bf16 (VA_LOGITS_BF16; a multiple
  *                 of 8).  vocab 1..VA_SAMPLE_MAX_VOCAB, any; the entries between rows are not used.

@@ -78,8 +78,7 @@ VA_API va_status kv_page_append_b8(const va_bf16 *k_new, const va_bf16 *v_new, i
  *   window        0 (a row at p sees keys 0..p) or W >= 1 (keys max(0, p - W + 1)..p)
  *   scale         softmax scale applied to q.k (finite)
  *   sink          device float [n_kv_heads * group] or NULL: logit of a zero-value key, post-scale
- *   workspace     device memory, 16-byte aligned, va_paged_workspace_bytes bytes, zeroed once before its first
- *                 use; every call leaves it ready for the next, of whatever shape it is large enough for.
+ *   workspace     device memory, 16-byte aligned, va_paged_workspace_bytes bytes (contents do not matter).
  *                 Calls that may run at the same time need workspaces of their own.
  *   out           device, as q: the attention output rounded once to bf16; padding rows 0
  *   out_lse       optional device float [n_seqs][n_rows][n_kv_heads * group]: log-sum-exp of the scores and the
@@ -87,6 +86,8 @@ VA_API va_status kv_page_append_b8(const va_bf16 *k_new, const va_bf16 *v_new, i
  * Only pages that hold a visible position are read, so entries below every row's window may be -1; a page's
  * positions past the sequence's end may hold anything.  A needed entry that is no page sets VA_DEV_BAD_PAGE and
  * its positions count as masked (a row that sees nothing: out 0, out_lse the sink, or -inf).
+ *   dev_status    VA_DEV_BAD_PAGE; VA_DEV_BAD_COUNT, VA_DEV_BEYOND_CACHE: as in kv_page_append_b8, that sequence's
+ *                 rows are padding; VA_DEV_TIMEOUT: a load did not arrive within a second, the output is void
  * Returns VA_OK, VA_INVALID_ARG, VA_UNSUPPORTED (a pool of more than 2^31 - 1 rows) or VA_CUDA_ERROR.
  */
 VA_API va_status verify_attn_paged_b8(const va_bf16 *q, int n_seqs, int n_rows, int n_kv_heads, int group,

@@ -418,7 +418,7 @@ def verify_attn_paged_b8(q, n_live, lens, table, k_codes, v_codes, k_scale, v_sc
                          out_lse=None, window: int = 0, dev_status=None, stream=None, variant: str = "") -> None:
     """Verify attention of every sequence's live rows (q [n_seqs, n_rows, heads, 128] bf16) over its pages; writes
     out (as q) and out_lse [n_seqs, n_rows, heads].  ``workspace``: a device byte tensor of
-    va_paged_workspace_bytes(...) bytes, zeroed once."""
+    va_paged_workspace_bytes(...) bytes."""
     layers, pages, kv, fmt, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
     n, rows, heads, d = q.shape
     _need(layers == 1 and d == HEAD_DIM and heads % kv == 0 and out.shape == q.shape,

@@ -1,6 +1,6 @@
 // va_beam_select: beam search's selection over beams and vocabulary.
 //
-// One launch, three levels.  The (row, 8,192-logit tile) units are dealt evenly to three CTAs an SM; a run is a CTA's
+// One launch, three levels.  The (row, 8,192-logit tile) units are dealt evenly to four CTAs an SM; a run is a CTA's
 // consecutive tiles of one row.  A CTA reads a tile's logits once (the next tile's are on their way into L2):
 //   sums        every thread keeps its own maximum m and sum of exp(l - m) over the run
 //   candidates  the run's k best keys so far are kept sorted in shared memory.  The first tile collects against a lower
@@ -10,7 +10,9 @@
 // 64 bits.  The last row of a request merges the hypotheses.  Every order is fixed by the keys and by the deal, so the
 // arrivals' order changes nothing.
 // Bytes: the logits once; what a run hands on (k keys) is a thousandth of that.  A 64-bit key for every logit took
-// 117 us for 32 x 8 x 151,669 bf16 logits, keys and a ranking for every tile's candidates 56 us.
+// 117 us for 32 x 8 x 151,669 bf16 logits, keys and a ranking for every tile's candidates 56 us; this takes 50 us with
+// four CTAs an SM (52 with three, 59 with two), and with a list for every warp instead of the CTA's, which needs no
+// barriers but eight times the insertions, 67 us.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -91,7 +93,7 @@ __device__ __forceinline__ bool arrive_last(unsigned* counter, int mine, int n, 
 }
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs a) {
     __shared__ BeamSmem sm;
     constexpr int kVec = kBf16 ? 8 : 4, kBytes = kBf16 ? 2 : 4;   // logits per 16 bytes
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -465,9 +467,9 @@ va_status va_beam_select(const void* logits, int format, int64_t row_stride, int
     a.row_tokens = reinterpret_cast<int32_t*>(p);
     a.vocab = vocab; a.n_beams = n_beams; a.k = n_out; a.end_token = end_token;
     a.n_tiles = tiles; a.n_rows = (int)rows;
-    // a CTA a tile while there are no more than fit at once (three an SM), else even shares of them
+    // a CTA a tile while there are no more than fit at once (four an SM), else even shares of them
     const int sms = va::device_sm_count();
-    const long long units = (long long)rows * tiles, most = 3ll * (sms > 0 ? sms : 148);
+    const long long units = (long long)rows * tiles, most = 4ll * (sms > 0 ? sms : 148);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     va::pdl_config(&cfg, attr, dim3((unsigned)(units < most ? units : most)), dim3(va::smp::kThreads), 0, (cudaStream_t)stream);

@@ -293,7 +293,8 @@ static cudaError_t launch_copy(const CopyArgs& a, long long most_units, cudaStre
     const int sms = device_sm_count();
     const long long most = 8ll * (sms > 0 ? sms : 148);
     long long work = most_units;
-    if (a.table) work = work > (a.n_entries + kCopyThreads - 1) / kCopyThreads ? work : (a.n_entries + kCopyThreads - 1) / kCopyThreads;
+    const auto entry_work = (a.n_entries + kCopyThreads - 1) / kCopyThreads;
+    if (a.table && work < entry_work) work = entry_work;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     pdl_config(&cfg, attr, dim3((unsigned)(work < 1 ? 1 : (work > most ? most : work))), dim3(kCopyThreads), 0, stream);

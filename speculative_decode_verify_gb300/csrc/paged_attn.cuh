@@ -1,23 +1,19 @@
-// The split kernel of verify_attn_paged_b8 (instantiated per format in paged_attn_e4m3.cu / paged_attn_int8.cu).
+// The split kernel of verify_attn_paged_b8 for few (row, query head) pairs a KV head (instantiated per format in
+// paged_attn_e4m3.cu / paged_attn_int8.cu); paged_plan.cuh has the deal of the batch's tiles over the CTAs.
 //
-// Work.  A sequence's visible pages, times its KV heads, are its tiles (64 keys of one head); all tiles of the
-// batch in (sequence, head, page) order are dealt evenly to one CTA an SM, whatever the lengths: CTA c of C takes
-// tiles [c N / C, (c + 1) N / C).  A run of tiles of one (sequence, head) in a CTA is a segment.  A segment that
-// covers its head writes the output itself; the others (at most the first and the last of a CTA) leave partial
-// sums that a second launch merges.
-//
-// Inside a CTA one warp feeds a ring of pages by TMA and eight warps consume it: teams of RG warps take the tiles
-// in turn, warp w of a team for its own 8 RT of the (row, query head) pairs, so no barrier joins the warps between
-// tiles.  With keys as the matrix rows, S^T = K Q^T and O^T = V^T P^T need as many 8-column tiles as there are
-// pairs / 8: a single token of six heads costs one, where queries as matrix rows would cost two.
-// The codes are widened to f16 in registers (exact for both formats) and multiplied by mma.sync: a tile of 16 KB
-// takes 64 RT RG of them, which is less than the time the tile takes to arrive until 48 pairs (the design doc has the
-// figures); a code is used by so few pairs that the load, not the product, bounds the call.
+// Inside a CTA four warps feed a ring of pages by TMA and eight consume it: teams of two warps take the tiles in turn,
+// each warp half of the page's keys for all pairs, so no barrier joins the warps between tiles.  With keys as the
+// matrix rows, S^T = K Q^T and O^T = V^T P^T need as many 8-column tiles as there are pairs / 8: a single token of six
+// heads costs one, where queries as matrix rows would cost two.  The codes are widened to f16 in registers (exact for
+// both formats) and multiplied by mma.sync: a code is used by so few pairs that its load bounds the call, and tensor
+// memory would only add a way through shared memory.
 //   Keys are taken in the order 0 5 2 7 4 1 6 3 of each eight: with the 128-byte swizzle of the loads, the 16-byte
 //   shared-memory reads of K (two rows a phase) and of V (four rows of even or odd order) then meet no bank twice.
 // The softmax is online, in base 2: p = 2^(t - m + 6) with m raised only when a score passes it by 8, so f16 holds
 // p <= 2^14 to 11 bits down to 2^-20 of the maximum (and to 2^-31 of it absolutely); sums are fp32.  The blocks' V
 // scales go into p relative to R, the largest so far (a power of two), which f16 would not hold by themselves.
+// Measured, E4M3, 8 KV heads of 6 query heads, one token: 64 sequences of 1 to 16K positions (256 MB) 58.7 us, 4.4
+// TB/s; 4 sequences of 1K 10.8 us, most of it the two launches' and the segments' one-time work.
 #pragma once
 
 #include "paged_attn_tc.cuh"
@@ -32,6 +28,8 @@ constexpr int kConsumers = 8;                 // consumer warps of a CTA
 constexpr int kAttnThreads = 32 * (kConsumers + 4);
 constexpr int kConsumerRegs = 232, kProducerRegs = 40;
 constexpr int kTickets = 64;                  // segments that can be open at once in a CTA are fewer
+constexpr int kSplit = 2;                     // warps that share a page's blocks
+constexpr int kTeams = kConsumers / kSplit;   // a power of two
 
 // ----------------------------------------------------------------------------- fragments
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -94,14 +92,11 @@ __device__ __forceinline__ bool page_wait(volatile int* issued, int use, uint32_
 }
 
 // ----------------------------------------------------------------------------- shared memory
-// RT: 8-pair tiles per warp; RG: warps of a team; kTeams teams; kStages: pages in flight.
-template <int RT, int RG>
+// RT: 8-pair tiles of a warp; kStages: pages in flight.
+template <int RT>
 struct Shape {
-    static constexpr int kSplit = 2;                                           // warps that share a page's blocks
-    static constexpr int kTeams = kConsumers / (RG * kSplit);                  // a power of two
-    static constexpr int kCols = 8 * RT;                                 // pairs of a warp
+    static constexpr int kCols = 8 * RT;                                       // pairs
     static constexpr int kSlotFloats = kCols * kD;
-    static constexpr int kRingAt = 0;
     static constexpr int kFixed = kConsumers * (kSlotFloats + 10 * kCols) * 4  // the warps' slots, (m, l) and weights
                                   + (int)sizeof(Plan) + 2048;                  // barriers, tickets, alignment
     static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kTileBytes + 32);
@@ -110,12 +105,12 @@ struct Shape {
     static_assert(kStages >= 4, "the ring needs a few pages");
 };
 
-template <bool kInt8, int RT, int RG>
+template <bool kInt8, int RT>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_paged_kernel(const AttnPagedArgs a, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
-    using S = Shape<RT, RG>;
-    constexpr int NS = S::kStages, T = S::kTeams, KG = S::kSplit, KB = kBlocks / KG, kCols = S::kCols;
+    using S = Shape<RT>;
+    constexpr int NS = S::kStages, T = kTeams, KG = kSplit, KB = kBlocks / KG, kCols = S::kCols;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* ring = base;
@@ -126,7 +121,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(&plan + 1);
     float* scales = reinterpret_cast<float*>(bars + 48);
     int* tickets = reinterpret_cast<int*>(scales + NS * 8);
-    int* issued = tickets + RG * kTickets;    // each stage's uses so far
+    int* issued = tickets + kTickets;    // each stage's uses so far
     int* valid = issued + 16;                 // whether its tile has a page
     int* flags = valid + 16;                  // [0]: the CTA gives up
     const uint32_t full0 = ptx::smem_u32(bars), empty0 = full0 + 8 * 16, free0 = full0 + 8 * 32;
@@ -139,7 +134,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ptx::tma_prefetch_desc(&map_v);
         for (int s = 0; s < NS; ++s) {
             ptx::mbar_init(full0 + 8 * s, 1);
-            ptx::mbar_init(empty0 + 8 * s, RG * KG);
+            ptx::mbar_init(empty0 + 8 * s, KG);
         }
         for (int w = 0; w < kConsumers; ++w) ptx::mbar_init(free0 + 8 * w, 1);
         ptx::mbar_init(filled, kConsumers);
@@ -148,7 +143,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         flags[0] = 0;
         for (int s = 0; s < 16; ++s) issued[s] = 0;
     }
-    for (int i = tid; i < RG * kTickets; i += kAttnThreads) tickets[i] = 0;
+    for (int i = tid; i < kTickets; i += kAttnThreads) tickets[i] = 0;
     __syncthreads();
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
@@ -195,14 +190,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         }
         // no CTA ends with copies under way, even if its consumers gave up
-        for (; last >= 0 && last > n - 1 - NS; last -= 4) ptx::mbar_wait(full0 + 8 * (last % NS), (last / NS) & 1, nullptr, kWaitNs);
+        for (; last >= 0 && last > n - 1 - NS; last -= 4)
+            ptx::mbar_wait(full0 + 8 * (last % NS), (last / NS) & 1, nullptr, kWaitNs);
     } else {
         // ------------------------------------------------------------ consumers
         ptx::set_max_regs_inc<kConsumerRegs>();
-        const int team = warp / (RG * KG), kg = warp / RG % KG, rg = warp % RG;
+        const int team = warp / KG, kg = warp % KG;
         const int g = lane >> 2, j = lane & 3;
         const int kperm = (g & ~1) ^ ((g & 1) ? 5 : 0);       // this lane's key row of each eight
-        const int heads = a.n_kv * a.group, cols_used = a.n_rows * a.group, col0 = rg * kCols;
+        const int heads = a.n_kv * a.group, cols_used = a.n_rows * a.group;
         float* slot = slots + (size_t)warp * S::kSlotFloats;
         float2* my_ml = slot_ml + warp * kCols;
         // how often the slot has been filled for a single warp's join, and for a common one; which was the last
@@ -225,12 +221,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 uint4 raw[RT][4];
 #pragma unroll
                 for (int n = 0; n < RT; ++n) {
-                    const int c = col0 + 8 * n + g;
+                    const int c = 8 * n + g;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) raw[n][e] = make_uint4(0u, 0u, 0u, 0u);
                     if (c < cols_used && plan.col_row[c] < live) {
                         const uint4* src = reinterpret_cast<const uint4*>(
-                            a.q + (((size_t)b * a.n_rows + plan.col_row[c]) * heads + h * a.group + plan.col_head[c]) * kD + 16 * j);
+                            a.q + (((size_t)b * a.n_rows + plan.col_row[c]) * heads + h * a.group + plan.col_head[c]) * kD +
+                            16 * j);
                         raw[n][0] = __ldg(src);
                         raw[n][1] = __ldg(src + 1);
                         raw[n][2] = __ldg(src + 8);
@@ -270,7 +267,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         off[n][e] = kInt8 ? 1152.0f * __shfl_sync(0xffffffffu, sum, (2 * j + e) * 4) : 0.0f;
                         m[n][e] = kNoScore;
                         l[n][e] = 0.0f;
-                        p[n][e] = len - live + min((int)plan.col_row[min(col0 + 8 * n + 2 * j + e, kMaxCols - 1)], live - 1);
+                        p[n][e] = len - live + min((int)plan.col_row[8 * n + 2 * j + e], live - 1);
                     }
 #pragma unroll
                     for (int d = 0; d < 8; ++d)
@@ -305,7 +302,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             vmax = fmaxf(vmax, vs[k]);
                         }
                         if (vmax > R) {
-                            const float up = __uint_as_float(min((__float_as_uint(vmax) + 0x7FFFFFu) & 0x7F800000u, 0x7F000000u));
+                            const uint32_t next = (__float_as_uint(vmax) + 0x7FFFFFu) & 0x7F800000u;
+                            const float up = __uint_as_float(min(next, 0x7F000000u));
                             const float by = R / up;
                             R = up;
                             inv_r = 1.0f / up;
@@ -384,7 +382,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                     now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 8));
                                     now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 16));
                                     const bool none_yet = m[n][e] == kNoScore;
-                                    const float up = now == -INFINITY ? 0.0f : (none_yet ? now - kShift : fmaxf(now - kShift, 0.0f));
+                                    float up = 0.0f;
+                                    if (now > -INFINITY) up = none_yet ? now - kShift : fmaxf(now - kShift, 0.0f);
                                     if (now > -INFINITY) m[n][e] = (none_yet ? 0.0f : m[n][e]) + up;
                                     const float by = none_yet ? 1.0f : ptx::ex2(-up);      // (sums of nothing are 0)
                                     l[n][e] *= by;
@@ -456,7 +455,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             if (given_up) break;
             // -------------------------------------------------------- sums of the segment, into the warp's slot
-            const int active = min(T, seg_len) * KG;              // warps that have a part of it (for each rg)
+            const int active = min(T, seg_len) * KG;              // warps that have a part of it
             if (slot_use == 1 && !warp_wait(free0 + 8 * warp, (uses - 1) & 1, abort, status)) break;
             if (slot_use == 2 && !warp_wait(joined, (joins - 1) & 1, abort, status)) break;
 #pragma unroll
@@ -476,11 +475,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         dst[4 * g + (w ^ j)] = make_float4(o[n][2 * w][e] * R, o[n][2 * w][2 + e] * R, o[n][2 * w + 1][e] * R,
                                                            o[n][2 * w + 1][2 + e] * R);
                 }
-            // Column c of row group r: the sum over the active warps, in the order of their tiles, to the output if the
-            // segment is the whole head, else to this CTA's part of it.
-            auto join = [&](int r, int c) {
-                auto warp_of = [&](int t) { return ((((i_begin & (T - 1)) + t / KG) & (T - 1)) * KG + t % KG) * RG + r; };
-                const int col = r * kCols + c, chunk = (lane & ~3) | ((lane & 3) ^ ((c >> 1) & 3)), t_mine = lane & 7;
+            // the active warps, in the order of their tiles
+            auto warp_of = [&](int t) { return (((i_begin & (T - 1)) + t / KG) & (T - 1)) * KG + t % KG; };
+            // Pair c: the sum over the active warps, to the output if the segment is the whole head, else to this CTA's
+            // part of it.
+            auto join = [&](int c) {
+                const int chunk = (lane & ~3) | ((lane & 3) ^ ((c >> 1) & 3)), t_mine = lane & 7;
                 float2 ml = make_float2(-INFINITY, 0.0f);
                 if (t_mine < active) ml = slot_ml[warp_of(t_mine) * kCols + c];
                 float4 v[8];
@@ -497,9 +497,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                const size_t part = (size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + col;
-                const int head = h * a.group + plan.col_head[col];
-                const size_t row = ((size_t)b * a.n_rows + plan.col_row[col]) * heads + head;
+                const size_t part = (size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + c;
+                const int head = h * a.group + plan.col_head[c];
+                const size_t row = ((size_t)b * a.n_rows + plan.col_row[c]) * heads + head;
                 if (whole) {
                     const Finish fin = finish(top, sum, a.sink, head);
                     one *= fin.by;
@@ -527,8 +527,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(filled);
                 if (!warp_wait(filled, joins & 1, abort, status)) break;
 #pragma unroll 1
-                for (int q = warp; q < RG * kCols; q += kConsumers)
-                    if (q < cols_used && plan.col_row[q] < live) join(q / kCols, q % kCols);
+                for (int c = warp; c < live * a.group; c += kConsumers) join(c);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(joined);
                 ++joins;
@@ -539,7 +538,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 __threadfence_block();
                 __syncwarp();
                 if (lane == 0) {
-                    int* ticket = tickets + rg * kTickets + (seg & (kTickets - 1));
+                    int* ticket = tickets + (seg & (kTickets - 1));
                     last = atomicAdd(ticket, 1) == active - 1;
                     if (last) *ticket = 0;
                 }
@@ -550,10 +549,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 __threadfence_block();
                 __syncwarp();
                 // weights first: eight lanes a column, one for each active warp; then the columns' rows
-                auto warp_of = [&](int t) { return ((((i_begin & (T - 1)) + t / KG) & (T - 1)) * KG + t % KG) * RG + rg; };
                 float* by = weights + warp * kCols * 8;
-                const size_t part = (size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols + col0;
-                const int n_here = min(kCols, live * a.group - col0);
+                const size_t part = (size_t)(2 * blockIdx.x + (i_begin == 0 ? 0 : 1)) * kMaxCols;
+                const int n_here = live * a.group;
 #pragma unroll 1
                 for (int c = lane >> 3; c < kCols; c += 4) {
                     const int t = lane & 7;
@@ -570,10 +568,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                     if (c < n_here) {
                         if (whole) {
-                            const int head = h * a.group + plan.col_head[col0 + c];
+                            const int head = h * a.group + plan.col_head[c];
                             const Finish fin = finish(top, sum, a.sink, head);
                             one *= fin.by;
-                            if (t == 0 && a.out_lse) a.out_lse[((size_t)b * a.n_rows + plan.col_row[col0 + c]) * heads + head] = fin.lse;
+                            if (t == 0 && a.out_lse)
+                                a.out_lse[((size_t)b * a.n_rows + plan.col_row[c]) * heads + head] = fin.lse;
                         } else if (t == 0) {
                             a.part_ml[part + c] = make_float2(top, sum);
                         }
@@ -588,44 +587,48 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll 2
                     for (int t = 0; t < active; ++t) {
                         const float one = by[c * 8 + t];
-                        const float4 v = reinterpret_cast<const float4*>(slots + (size_t)warp_of(t) * S::kSlotFloats + c * kD)[chunk];
+                        const float* of = slots + (size_t)warp_of(t) * S::kSlotFloats;
+                        const float4 v = reinterpret_cast<const float4*>(of + c * kD)[chunk];
                         acc.x += one * v.x;
                         acc.y += one * v.y;
                         acc.z += one * v.z;
                         acc.w += one * v.w;
                     }
+                    const size_t out_row = ((size_t)b * a.n_rows + plan.col_row[c]) * heads + h * a.group + plan.col_head[c];
                     if (whole)
-                        store_row(a.out + (((size_t)b * a.n_rows + plan.col_row[col0 + c]) * heads + h * a.group + plan.col_head[col0 + c]) * kD + 4 * lane, acc);
+                        store_row(a.out + out_row * kD + 4 * lane, acc);
                     else
                         reinterpret_cast<float4*>(a.part_o + (part + c) * kD)[lane] = acc;
                 }
                 __syncwarp();
-                if (lane < active)
-                    ptx::mbar_arrive(free0 + 8 * (((((i_begin & (T - 1)) + lane / KG) & (T - 1)) * KG + lane % KG) * RG + rg));
+                if (lane < active) ptx::mbar_arrive(free0 + 8 * warp_of(lane));
             }
         }
     }
     if (status && a.dev_status) atomicOr(a.dev_status, status);
 }
 
-// Launch of one shape; rows: 8-pair tiles and warps a team that cover the call's pairs.
-template <bool kInt8, int RT, int RG>
+// RT: the 8-pair tiles that cover the call's pairs.
+template <bool kInt8, int RT>
 cudaError_t launch_shape(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
-    const cudaError_t e = ensure_smem_attr((const void*)attn_paged_kernel<kInt8, RT, RG>, Shape<RT, RG>::kBytes);
+    const cudaError_t e = ensure_smem_attr((const void*)attn_paged_kernel<kInt8, RT>, Shape<RT>::kBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    pdl_config(&cfg, attr, dim3((unsigned)a.n_ctas), dim3(kAttnThreads), Shape<RT, RG>::kBytes, stream);
-    return cudaLaunchKernelEx(&cfg, attn_paged_kernel<kInt8, RT, RG>, a, k, v);
+    pdl_config(&cfg, attr, dim3((unsigned)a.n_ctas), dim3(kAttnThreads), Shape<RT>::kBytes, stream);
+    return cudaLaunchKernelEx(&cfg, attn_paged_kernel<kInt8, RT>, a, k, v);
 }
 
-// By the (row, query head) pairs of a KV head: up to 16 here, more on tcgen05 (paged_attn_tc.cuh).
+// By the (row, query head) pairs of a KV head: up to 16 here, more on tcgen05 (paged_attn_tc.cuh).  From 17 on this
+// kernel needs a second warp a code or a third column tile: 42 pairs of one 192K sequence took 48 us here and 38.6 us
+// there, 24 of 32 sequences in a window of 4,096 44 us and 37.1 us; 6 pairs of 64 ragged sequences of 1 to 16K 58.3 us
+// here and 124 us there, 6 pairs of 64 sequences of 4K INT8 44.2 us and 96.2 us.
 template <bool kInt8>
 cudaError_t launch_format(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, const uint8_t* k_codes,
                           const uint8_t* v_codes, cudaStream_t stream) {
     const int cols = a.n_rows * a.group;
-    if (cols <= 8) return launch_shape<kInt8, 1, 1>(a, k, v, stream);
-    if (cols <= 16) return launch_shape<kInt8, 2, 1>(a, k, v, stream);
+    if (cols <= 8) return launch_shape<kInt8, 1>(a, k, v, stream);
+    if (cols <= 16) return launch_shape<kInt8, 2>(a, k, v, stream);
     if (cols <= 32) return tcg::launch<kInt8, 32>(a, k_codes, v_codes, stream);
     if (cols <= 48) return tcg::launch<kInt8, 48>(a, k_codes, v_codes, stream);
     return tcg::launch<kInt8, 64>(a, k_codes, v_codes, stream);

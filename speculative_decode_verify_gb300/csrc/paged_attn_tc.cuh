@@ -37,7 +37,7 @@ struct Misc {
     Plan plan;
     alignas(16) float ring_scale[6][8];            // a page's K scales, then its V scales
     alignas(16) float scale[4][16];                // a tile's: K (two pages), V
-    alignas(16) float2 fz[kSoftWarps][32];                     // per softmax warp and pair of its half: factor and kShift - reference
+    alignas(16) float2 fz[kSoftWarps][32];         // per softmax warp and pair of its half: factor and kShift - reference
     float ref[kSoftWarps][32];
     float red[4][kMaxCols], vmax[4];
     alignas(8) uint64_t raw_full[6], raw_empty[6];
@@ -343,8 +343,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                 const __half2 x = __floats2half2_rn(__uint_as_float(raw.x << 16) * by, __uint_as_float(raw.x & 0xFFFF0000u) * by);
                 const __half2 y = __floats2half2_rn(__uint_as_float(raw.y << 16) * by, __uint_as_float(raw.y & 0xFFFF0000u) * by);
                 // dimensions 4 lane .. 4 lane + 3: half lane / 16, chunk (lane % 16) / 2, 8 bytes of it
-                unsigned char* dst = base + kOffQ + (lane >> 4) * (NC * 128) + c * 128 + ((((lane & 15) >> 1) ^ (c & 7)) * 16) + (lane & 1) * 8;
-                *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+                unsigned char* dst = base + kOffQ + (lane >> 4) * (NC * 128) + c * 128 +
+                                     ((((lane & 15) >> 1) ^ (c & 7)) * 16) + (lane & 1) * 8;
+                *reinterpret_cast<uint2*>(dst) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
                 if (lane == 0) ms.prow[c] = len - live + (c < n_cols ? min((int)ms.plan.col_row[c], live - 1) : live - 1);
                 if (lane < 4) ms.fz[lane + (c >= NH ? 4 : 0)][c >= NH ? c - NH : c] =
                     make_float2(__uint_as_float((uint32_t)(254 - up) << 23) * a.scale_log2, kShift);
