@@ -12,8 +12,8 @@
 // The softmax is online, in base 2: p = 2^(t - m + 6) with m raised only when a score passes it by 8, so f16 holds
 // p <= 2^14 to 11 bits down to 2^-20 of the maximum (and to 2^-31 of it absolutely); sums are fp32.  The blocks' V
 // scales go into p relative to R, the largest so far (a power of two), which f16 would not hold by themselves.
-// Measured, E4M3, 8 KV heads of 6 query heads, one token: 64 sequences of 1 to 16K positions (256 MB) 58.7 us, 4.4
-// TB/s; 4 sequences of 1K 10.8 us, most of it the two launches' and the segments' one-time work.
+// Measured, E4M3, one token of 6 query heads a KV head: 64 sequences of 1 to 16K positions, 8 KV heads (262 MB) 58.3
+// us, 4.5 TB/s; 4 sequences of 1K, one KV head 10.9 us, most of it the two launches' and the segments' one-time work.
 #pragma once
 
 #include "paged_attn_tc.cuh"
@@ -50,19 +50,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 // A word's codes c0..c3 to the f16 pairs (c0, c1), (c2, c3), exactly.  E4M3: two conversions, which issue like any
 // integer instruction here (2.2 cycles a warp measured; placing the bits by shifts and masks took seven).  INT8:
-// 0x64xx is 1024 + xx, so the biased code (+128) becomes the low byte and 1152 comes off again.
-// kBiased leaves the 1152 on (the keys': their scores lose 1152 sum q, one subtraction a score).
-template <bool kInt8, bool kBiased>
+// 0x64xx is 1024 + xx, so the biased code (+128) becomes the low byte and 1152 comes off again (taking 1152 sum q off
+// a score instead would save the subtractions here, and lose five bits of the score).
+template <bool kInt8>
 __device__ __forceinline__ void widen(uint32_t w, uint32_t& x, uint32_t& y) {
     if (kInt8) {
         const uint32_t u = w ^ 0x80808080u;
         const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
         uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-        if (kBiased) {
-            x = a;
-            y = b;
-            return;
-        }
         const __half2 lo = __hsub2(*reinterpret_cast<__half2*>(&a), bias), hi = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
         x = *reinterpret_cast<const uint32_t*>(&lo);
         y = *reinterpret_cast<const uint32_t*>(&hi);
@@ -121,7 +116,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(&plan + 1);
     float* scales = reinterpret_cast<float*>(bars + 48);
     int* tickets = reinterpret_cast<int*>(scales + NS * 8);
-    int* issued = tickets + kTickets;    // each stage's uses so far
+    int* issued = tickets + kTickets;         // each stage's uses so far
     int* valid = issued + 16;                 // whether its tile has a page
     int* flags = valid + 16;                  // [0]: the CTA gives up
     const uint32_t full0 = ptx::smem_u32(bars), empty0 = full0 + 8 * 16, free0 = full0 + 8 * 32;
@@ -212,9 +207,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             int i = i_begin + ((team - i_begin) & (T - 1));
             if (i >= i_end) continue;
             // Q, each row brought to f16's upper range by a power of two (exact but for elements 2^-39 of the row's
-            // largest); f turns accumulated scores into base-2 exponents, and off takes INT8's bias out of them
+            // largest); f turns accumulated scores into base-2 exponents
             uint32_t qf[RT][8][2];
-            float f[RT][2], off[RT][2], m[RT][2], l[RT][2];
+            float f[RT][2], m[RT][2], l[RT][2];
             int p[RT][2];                                     // positions of the columns' rows
             float o[RT][8][4];
             {
@@ -245,26 +240,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int up = min(max(268 - (int)(top >> 7), 1), 253);
                     const float by = __uint_as_float((uint32_t)up << 23);
                     const float back = __uint_as_float((uint32_t)(254 - up) << 23) * a.scale_log2;
-                    float sum = 0.0f;
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const uint32_t v = w[2 * s + e];
                             qf[n][s][e] = pack_f16(__uint_as_float(v << 16) * by, __uint_as_float(v & 0xFFFF0000u) * by);
-                            if (kInt8) {
-                                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&qf[n][s][e]));
-                                sum += x.x + x.y;
-                            }
                         }
-                    if (kInt8) {
-                        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         f[n][e] = __shfl_sync(0xffffffffu, back, (2 * j + e) * 4);
-                        off[n][e] = kInt8 ? 1152.0f * __shfl_sync(0xffffffffu, sum, (2 * j + e) * 4) : 0.0f;
                         m[n][e] = kNoScore;
                         l[n][e] = 0.0f;
                         p[n][e] = len - live + min((int)plan.col_row[8 * n + 2 * j + e], live - 1);
@@ -339,8 +324,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                     const uint32_t wa[4] = {ra[k].x, ra[k].y, ra[k].z, ra[k].w};
                                     const uint32_t wb[4] = {rb[k].x, rb[k].y, rb[k].z, rb[k].w};
                                     uint32_t a0, a1, a2, a3;
-                                    widen<kInt8, true>(wa[w], a0, a2);
-                                    widen<kInt8, true>(wb[w], a1, a3);
+                                    widen<kInt8>(wa[w], a0, a2);
+                                    widen<kInt8>(wb[w], a1, a3);
 #pragma unroll
                                     for (int n = 0; n < RT; ++n)
                                         mma_f16(s[k][n], a0, a1, a2, a3, qf[n][4 * u + w][0], qf[n][4 * u + w][1]);
@@ -358,8 +343,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 top[n][e] = -INFINITY;
 #pragma unroll
                                 for (int k = 0; k < KB; ++k) {
-                                    const float fk = f[n][e] * sc[k0 + k], zk = kInt8 ? fmaf(-off[n][e], fk, z) : z;
-                                    float x0 = fmaf(s[k][n][e], fk, zk), x1 = fmaf(s[k][n][2 + e], fk, zk);
+                                    const float fk = f[n][e] * sc[k0 + k];
+                                    float x0 = fmaf(s[k][n][e], fk, z), x1 = fmaf(s[k][n][2 + e], fk, z);
                                     if (edge) {
                                         const int key = key0 + (k0 + k) * kBlock + kperm;
                                         const int lo = a.window > 0 ? p[n][e] - a.window : -1;
@@ -436,13 +421,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             for (int w = 0; w < 4; ++w) {
                                 // dimensions 4 w, 4 w + 1 of the even and odd keys side by side, then 4 w + 2, 4 w + 3
                                 uint32_t a0, a1, a2, a3;
-                                widen<kInt8, false>(__byte_perm(u0[w], u1[w], 0x5140), a0, a1);
-                                widen<kInt8, false>(__byte_perm(u2[w], u3[w], 0x5140), a2, a3);
+                                widen<kInt8>(__byte_perm(u0[w], u1[w], 0x5140), a0, a1);
+                                widen<kInt8>(__byte_perm(u2[w], u3[w], 0x5140), a2, a3);
 #pragma unroll
                                 for (int n = 0; n < RT; ++n)
                                     mma_f16(o[n][2 * w], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
-                                widen<kInt8, false>(__byte_perm(u0[w], u1[w], 0x7362), a0, a1);
-                                widen<kInt8, false>(__byte_perm(u2[w], u3[w], 0x7362), a2, a3);
+                                widen<kInt8>(__byte_perm(u0[w], u1[w], 0x7362), a0, a1);
+                                widen<kInt8>(__byte_perm(u2[w], u3[w], 0x7362), a2, a3);
 #pragma unroll
                                 for (int n = 0; n < RT; ++n)
                                     mma_f16(o[n][2 * w + 1], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
@@ -620,9 +605,9 @@ cudaError_t launch_shape(const AttnPagedArgs& a, const CUtensorMap& k, const CUt
 }
 
 // By the (row, query head) pairs of a KV head: up to 16 here, more on tcgen05 (paged_attn_tc.cuh).  From 17 on this
-// kernel needs a second warp a code or a third column tile: 42 pairs of one 192K sequence took 48 us here and 38.6 us
-// there, 24 of 32 sequences in a window of 4,096 44 us and 37.1 us; 6 pairs of 64 ragged sequences of 1 to 16K 58.3 us
-// here and 124 us there, 6 pairs of 64 sequences of 4K INT8 44.2 us and 96.2 us.
+// kernel needs a second warp a code or a third column tile: 48 pairs of one 192K sequence took 48 us here and 36.5 us
+// there, 30 of 32 sequences in a window of 4,096 44 us and 35.6 us; 6 pairs of 64 ragged sequences of 1 to 16K 58.3 us
+// here and 124 us there, 4 pairs of 64 sequences of 4K INT8 45.2 us and 96.2 us.
 template <bool kInt8>
 cudaError_t launch_format(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, const uint8_t* k_codes,
                           const uint8_t* v_codes, cudaStream_t stream) {
