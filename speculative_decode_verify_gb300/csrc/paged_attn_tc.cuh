@@ -5,14 +5,19 @@
 // with keys as the matrix rows: S^T[128 keys x NC pairs] = K Q^T and O^T[128 dimensions x NC pairs] += V^T P^T, f16
 // operands in shared memory (exact for both code formats), f32 accumulators in TMEM, S double-buffered.
 //   producer   pages' codes and scales into a ring by bulk copies
-//   wideners   eight warps: a tile's K, then its V, from codes to swizzled f16 (K's buffer is free when the scores
-//              are done, V's two when the products of the tile before the last are)
+//   wideners   four warps for K, four for V, from codes to swizzled f16: a page's codes are in registers before their
+//              place is free (K's when the scores of the tile before are done, V's two when the products of the tile
+//              before the last are)
 //   issuer     one thread: the scores of tile i + 1 before the products of tile i
-//   softmax    eight warps, a key a thread, half the pairs each: as in paged_attn.cuh (base 2, a reference that is
+//   scales     one warp: a tile's scales, and the largest V scale
+//   softmax    four warps for every 16 pairs, a key a thread: as in paged_attn.cuh (base 2, a reference that is
 //              raised when a score passes it by 2^8, V's scales relative to the largest so far), with one reference a
 //              pair for the whole CTA, so that a segment leaves one sum and nothing is joined inside the CTA.  The
-//              eight warps agree on each tile whether to raise; raising rescales the accumulator in TMEM.
-// Bound by the softmax and the widening warps (a tile of 128 keys in about the time of its loads at 48 pairs).
+//              warps agree on each tile whether to raise; raising rescales the accumulator in TMEM.
+// Bound by the softmax warps: 1.6 us for a tile of 128 keys at 48 pairs, 2.9 us where a reference is raised; and by
+// what a segment costs once (7.5 us until the first scores, 3 us for its sums).  Measured:
+// 48 pairs of one sequence of 192K, E4M3, one KV head 36.5 us (eight softmax warps, and wideners that took K and V in turn: 38.7 us),
+// 30 pairs of 32 sequences in a window of 4,096, INT8, two KV heads 35.6 us (37.2 us).
 #pragma once
 
 #include "paged_plan.cuh"
@@ -21,11 +26,7 @@ namespace va {
 namespace paged {
 namespace tcg {
 
-constexpr int kSoftWarps = 8, kWideWarps = 8;
-// Five warpgroups of 96 registers a thread at launch (61,440 in all); then the softmax warps hold 136, the wideners
-// 72, the last group (producer, issuer and two that wait) 56: 34,816 + 18,432 + 7,168.
-constexpr int kThreads = 32 * (kSoftWarps + kWideWarps + 4);
-constexpr int kSoftRegs = 136, kWideRegs = 72, kLastRegs = 56;
+constexpr int kMaxSoftWarps = 16, kWideWarps = 8;
 constexpr int kKeys = 128;                         // keys of a tile
 constexpr uint32_t kHalf = kKeys * 128;            // one half of the dimensions of a tile in f16
 constexpr uint32_t kOffK = 0, kOffV = 2 * kHalf, kOffP = 6 * kHalf;   // one K buffer, two of V
@@ -37,21 +38,32 @@ struct Misc {
     Plan plan;
     alignas(16) float ring_scale[6][8];            // a page's K scales, then its V scales
     alignas(16) float scale[4][16];                // a tile's: K (two pages), V
-    alignas(16) float2 fz[kSoftWarps][32];         // per softmax warp and pair of its half: factor and kShift - reference
-    float ref[kSoftWarps][32];
+    alignas(16) float2 fz[kMaxSoftWarps][16];      // per softmax warp and pair of its own: factor and kShift - reference
+    float ref[kMaxSoftWarps][16];
     float red[4][kMaxCols], vmax[4];
     alignas(8) uint64_t raw_full[6], raw_empty[6];
     uint64_t k_ready, v_ready[2], s_full[2], s_free[2], p_ready[2], pv_done[2], q_ready, o_done, o_free, vote[2], join, drain;
     int prow[kMaxCols];                            // positions of the pairs' rows
     int ring_ok[6], ok[4];
-    alignas(8) unsigned char flag[2][kSoftWarps];
+    alignas(16) unsigned char flag[2][kMaxSoftWarps];
     uint32_t tmem;
     int abort;
-    alignas(16) float2 ub[kSoftWarps][32];         // raising: what comes off a pair's exponents, its sums' factor
+    alignas(16) float2 ub[kMaxSoftWarps][16];      // raising: what comes off a pair's exponents, its sums' factor
 };
 
+// Softmax warps: four for every 16 pairs.  Registers a thread at launch (kThreads of them, one CTA an SM), then of the
+// softmax warps, the wideners and the last group (producer, issuer, scales and one that waits):
+//   NC 32  640 threads x 96 = 256 x 120 + 256 x 72 + 128 x 96
+//   NC 48  768 threads x 80 = 384 x  88 + 256 x 72 + 128 x 72
+//   NC 64  896 threads x 72 = 512 x  72 + 256 x 64 + 128 x 88
 template <int NC>
 struct Shape {
+    static constexpr int NH = 16;
+    static constexpr int kSoftWarps = 4 * NC / NH;
+    static constexpr int kThreads = 32 * (kSoftWarps + kWideWarps + 4);
+    static constexpr int kSoftRegs = NC == 32 ? 120 : (NC == 48 ? 88 : 72), kWideRegs = NC == 64 ? 64 : 72;
+    static constexpr int kLaunchRegs = NC == 32 ? 96 : (NC == 48 ? 80 : 72);
+    static constexpr int kLastRegs = NC == 32 ? 96 : (NC == 48 ? 72 : 88);
     static constexpr uint32_t kOffRing = kOffQ + NC * 256u;
     static constexpr int kFit = (int)((227u * 1024u - 1024u - kOffRing - sizeof(Misc)) / kTileBytes);
     static constexpr int kStages = kFit < 6 ? kFit : 6;
@@ -88,27 +100,23 @@ __device__ __forceinline__ void widen16(const uint4& c, uint4& lo, uint4& hi) {
 
 template <int n>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[n]) {
-    static_assert(n == 16 || n == 24 || n == 32, "half the pairs");
-    if constexpr (n == 16) ptx::tmem_ld16_wait(taddr, v);
-    if constexpr (n == 24) ptx::tmem_ld24_wait(taddr, v);
-    if constexpr (n == 32) {
-        ptx::tmem_ld16_wait(taddr, v);
-        ptx::tmem_ld16_wait(taddr + 16, v + 16);
-    }
+    static_assert(n == 8 || n == 16, "a softmax warp's pairs");
+    if constexpr (n == 8) ptx::tmem_ld8_wait(taddr, v);
+    else ptx::tmem_ld16_wait(taddr, v);
 }
 template <int n>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[n]) {
-    ptx::tmem_st16(taddr, v);
-    if constexpr (n == 24) ptx::tmem_st8(taddr + 16, v + 16);
-    if constexpr (n == 32) ptx::tmem_st16(taddr + 16, v + 16);
+    if constexpr (n == 8) ptx::tmem_st8(taddr, v);
+    else ptx::tmem_st16(taddr, v);
     ptx::tmem_wait_st();
 }
 
 template <bool kInt8, int NC>
-__global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPagedArgs a, const uint8_t* __restrict__ k_codes,
-                                                                    const uint8_t* __restrict__ v_codes) {
+__global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
+    attn_paged_tc_kernel(const AttnPagedArgs a, const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ v_codes) {
     using S = Shape<NC>;
-    constexpr int NR = S::kStages, NH = NC / 2;
+    constexpr int NR = S::kStages, NH = S::NH, kSoftWarps = S::kSoftWarps, kThreads = S::kThreads;
+    constexpr int kIssuer = kSoftWarps + kWideWarps;       // then the producer's and the scales' warp
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* ring = base + S::kOffRing;
@@ -120,11 +128,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
     if (tid == 0) {
         for (int s = 0; s < NR; ++s) {
             ptx::mbar_init(bar(ms.raw_full[s]), 1);
-            ptx::mbar_init(bar(ms.raw_empty[s]), kWideWarps);
+            ptx::mbar_init(bar(ms.raw_empty[s]), kWideWarps + 1);
         }
-        ptx::mbar_init(bar(ms.k_ready), kWideWarps);
+        ptx::mbar_init(bar(ms.k_ready), kWideWarps / 2 + 1);
         for (int s = 0; s < 2; ++s) {
-            ptx::mbar_init(bar(ms.v_ready[s]), kWideWarps);
+            ptx::mbar_init(bar(ms.v_ready[s]), kWideWarps / 2);
             ptx::mbar_init(bar(ms.s_full[s]), 1);
             ptx::mbar_init(bar(ms.s_free[s]), kSoftWarps);
             ptx::mbar_init(bar(ms.p_ready[s]), kSoftWarps);
@@ -138,6 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
         ptx::mbar_init(bar(ms.drain), 1);
         ptx::mbar_init_fence();
         ms.abort = 0;
+        for (int s = 0; s < 2; ++s) *reinterpret_cast<uint4*>(ms.flag[s]) = make_uint4(0u, 0u, 0u, 0u);
     }
     __syncthreads();
     ptx::griddep_launch_dependents();
@@ -152,9 +161,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
     const uint32_t tmem = ms.tmem;
     const int heads = a.n_kv * a.group, n_cols = a.n_rows * a.group;
 
-    if (warp >= kSoftWarps + kWideWarps) {
-    ptx::set_max_regs_dec<kLastRegs>();
-    if (warp == kSoftWarps + kWideWarps) {
+    if (warp >= kIssuer) {
+    if constexpr (S::kLastRegs < S::kLaunchRegs) ptx::set_max_regs_dec<S::kLastRegs>();
+    if constexpr (S::kLastRegs > S::kLaunchRegs) ptx::set_max_regs_inc<S::kLastRegs>();
+    if (warp == kIssuer + 1) {
         // ------------------------------------------------------------ producer: 32 pages looked up at once
         int last = -1;
         bool given_up = false;
@@ -188,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
         // no CTA ends with copies under way, even if the others gave up
         for (int i = max(0, last + 1 - NR); i <= last; ++i)
             ptx::mbar_wait(bar(ms.raw_full[i % NR]), (i / NR) & 1, nullptr, kWaitNs);
-    } else if (warp == kSoftWarps + kWideWarps + 1) {
+    } else if (warp == kIssuer) {
         // ------------------------------------------------------------ issuer (one lane)
         if (lane == 0) {
             bool ok = true;
@@ -241,70 +251,104 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
             ptx::mbar_wait(bar(ms.drain), 0, nullptr, kWaitNs);
         }
         __syncwarp();
+    } else if (warp == kIssuer + 2) {
+        // ------------------------------------------------------------ the tiles' scales, and their largest V scales
+        Walk walk(share);
+        int t = 0;
+        bool ok = true;
+        while (ok && walk.next(ms.plan, a, share.n)) {
+            for (int p0 = walk.begin; p0 < walk.end; p0 += 2, ++t) {
+                const int n_pages = min(2, walk.end - p0), key0 = (walk.page0 + p0 - walk.begin) * kPage;
+                float sc[2] = {0.0f, 0.0f}, vmax = 0.0f;
+                int good = 0;
+                for (int hp = 0; hp < n_pages && ok; ++hp) {
+                    const int s = (p0 + hp) % NR;
+                    if (!(ok = warp_wait(bar(ms.raw_full[s]), ((p0 + hp) / NR) & 1, abort, status))) break;
+                    const bool page_ok = ms.ring_ok[s] != 0;
+                    if (lane < 8) sc[hp] = ms.ring_scale[s][lane];
+                    const bool in = page_ok && lane >= 4 && lane < 8 && key0 + hp * kPage + 16 * (lane & 3) < walk.len;
+                    // (positive floats order like their bits)
+                    vmax = fmaxf(vmax, __uint_as_float(__reduce_max_sync(0xffffffffu, in ? __float_as_uint(sc[hp]) : 0u)));
+                    good |= page_ok ? 1 << hp : 0;
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(ms.raw_empty[s]));
+                }
+                // with the keys of this tile, not before (the barrier counts both)
+                if (!ok || (t > 0 && !(ok = warp_wait(bar(ms.s_full[(t - 1) & 1]), ((t - 1) >> 1) & 1, abort, status)))) break;
+                if (lane < 8) {
+                    ms.scale[t & 3][(lane & 4) * 2 + (lane & 3)] = sc[0];
+                    ms.scale[t & 3][(lane & 4) * 2 + 4 + (lane & 3)] = sc[1];
+                }
+                if (lane == 0) {
+                    ms.vmax[t & 3] = vmax;
+                    ms.ok[t & 3] = good;
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(ms.k_ready));
+            }
+        }
     }
     } else if (warp >= kSoftWarps) {
-        ptx::set_max_regs_dec<kWideRegs>();
-        // ------------------------------------------------------------ wideners: thread (row r, chunk c) of each page
-        const int wt = tid - 32 * kSoftWarps;          // 0..255: rows wt / 8 and wt / 8 + 32, 16-byte chunk wt % 8
+        ptx::set_max_regs_dec<S::kWideRegs>();
+        // ------------------------------------------------------------ wideners: four warps for K, four for V
+        // Thread (row r0, r0 + 16, .. of each page; 16-byte chunk c).  A page's codes are in registers before the place
+        // they go to is free, so the page is given back early.
+        const int wt = (tid - 32 * kSoftWarps) & 127;
+        const bool is_v = warp >= kSoftWarps + kWideWarps / 2;
         const int c = wt & 7, r0 = wt >> 3;
         const int first = 2 * (c & 3) + (c >> 2), second = first ^ 1;   // order of the two f16 chunks: no bank twice
         Walk walk(share);
         int t = 0;
         bool ok = true;
         while (ok && walk.next(ms.plan, a, share.n)) {
-            for (int p0 = walk.begin; p0 < walk.end && ok; p0 += 2, ++t) {
+            for (int p0 = walk.begin; p0 < walk.end; p0 += 2, ++t) {
                 const int n_pages = min(2, walk.end - p0);
                 const int key0 = (walk.page0 + p0 - walk.begin) * kPage;
+                uint4 x[2][4];
 #pragma unroll
-                for (int is_v = 0; is_v < 2; ++is_v) {
-                    // K's buffer is free once the scores of the tile before are done, V's once the products of the
-                    // one before that are
-                    if (t > is_v && !warp_wait(is_v ? bar(ms.pv_done[t & 1]) : bar(ms.s_full[(t - 1) & 1]),
-                                               (is_v ? (t >> 1) - 1 : (t - 1) >> 1) & 1, abort, status)) {
-                        ok = false;
-                        break;
-                    }
-                    for (int hp = 0; hp < n_pages; ++hp) {
+                for (int hp = 0; hp < 2; ++hp)
+                    if (hp < n_pages && ok) {
                         const int s = (p0 + hp) % NR;
-                        if (!is_v && !warp_wait(bar(ms.raw_full[s]), ((p0 + hp) / NR) & 1, abort, status)) {
-                            ok = false;
-                            break;
-                        }
-                        const bool page_ok = ms.ring_ok[s] != 0;
-                        const unsigned char* src = ring + s * kTileBytes + is_v * kHeadBytes;
+                        ok = warp_wait(bar(ms.raw_full[s]), ((p0 + hp) / NR) & 1, abort, status);
+                        const unsigned char* src = ring + s * kTileBytes + (is_v ? kHeadBytes : 0) + r0 * kD + c * 16;
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int r = r0 + 32 * u, key = hp * kPage + r;
-                            uint4 x = *reinterpret_cast<const uint4*>(src + r * kD + c * 16), y[2];
-                            // (what lies past the sequence or in no page may be NaN, and would stay it with weight 0)
-                            if (is_v && (!page_ok || key0 + key >= walk.len)) x = make_uint4(0u, 0u, 0u, 0u);
-                            widen16<kInt8>(x, y[0], y[1]);
-                            unsigned char* dst = base + (is_v ? kOffV + (t & 1) * 2 * kHalf : kOffK) + (c >> 2) * kHalf + key * 128;
-                            *reinterpret_cast<uint4*>(dst + ((first ^ (key & 7)) * 16)) = c & 4 ? y[1] : y[0];
-                            *reinterpret_cast<uint4*>(dst + ((second ^ (key & 7)) * 16)) = c & 4 ? y[0] : y[1];
+                        for (int u = 0; u < 4; ++u) x[hp][u] = *reinterpret_cast<const uint4*>(src + 16 * u * kD);
+                        // (what lies past the sequence or in no page may be NaN, and would stay it with weight 0)
+                        const int in = ms.ring_ok[s] != 0 ? walk.len - key0 - hp * kPage - r0 : 0;
+                        if (is_v && in < kPage) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                if (16 * u >= in) x[hp][u] = make_uint4(0u, 0u, 0u, 0u);
                         }
-                        if (!is_v && warp == kSoftWarps) {
-                            // the tile's scales, and its largest V scale (positive floats order like their bits)
-                            const float sc = lane < 8 ? ms.ring_scale[s][lane] : 0.0f;
-                            if (lane < 8) ms.scale[t & 3][(lane & 4) * 2 + hp * 4 + (lane & 3)] = sc;
-                            const bool in = page_ok && lane >= 4 && lane < 8 && key0 + hp * kPage + 16 * (lane & 3) < walk.len;
-                            const uint32_t top = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(sc) : 0u);
-                            if (lane == 0) {
-                                ms.vmax[t & 3] = hp == 0 ? __uint_as_float(top) : fmaxf(ms.vmax[t & 3], __uint_as_float(top));
-                                ms.ok[t & 3] = (hp == 0 ? 0 : ms.ok[t & 3]) | (page_ok ? 1 << hp : 0);
-                            }
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bar(ms.raw_empty[s]));
+                    }
+                // K's buffer is free once the scores of the tile before are done, V's once the products of the one
+                // before that are
+                if (ok && t > (is_v ? 1 : 0))
+                    ok = warp_wait(is_v ? bar(ms.pv_done[t & 1]) : bar(ms.s_full[(t - 1) & 1]),
+                                   (is_v ? (t >> 1) - 1 : (t - 1) >> 1) & 1, abort, status);
+                if (!ok) break;
+                unsigned char* to = base + (is_v ? kOffV + (t & 1) * 2 * kHalf : kOffK) + (c >> 2) * kHalf + r0 * 128;
+#pragma unroll
+                for (int hp = 0; hp < 2; ++hp)
+                    if (hp < n_pages) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            uint4 y[2];
+                            widen16<kInt8>(x[hp][u], y[0], y[1]);
+                            unsigned char* dst = to + (hp * kPage + 16 * u) * 128;
+                            *reinterpret_cast<uint4*>(dst + ((first ^ (r0 & 7)) * 16)) = c & 4 ? y[1] : y[0];
+                            *reinterpret_cast<uint4*>(dst + ((second ^ (r0 & 7)) * 16)) = c & 4 ? y[0] : y[1];
                         }
                     }
-                    if (!ok) break;
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(is_v ? bar(ms.v_ready[t & 1]) : bar(ms.k_ready));
-                    if (is_v && lane < n_pages) ptx::mbar_arrive(bar(ms.raw_empty[(p0 + lane) % NR]));
-                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(is_v ? bar(ms.v_ready[t & 1]) : bar(ms.k_ready));
             }
         }
     } else {
-        ptx::set_max_regs_inc<kSoftRegs>();
+        if constexpr (S::kSoftRegs > S::kLaunchRegs) ptx::set_max_regs_inc<S::kSoftRegs>();
         // ------------------------------------------------------------ softmax: key (or dimension) 32 q + lane, pairs n0..
         const int q = warp & 3, n0 = (warp >> 2) * NH, me = 32 * q + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
@@ -313,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
         Walk walk(share);
         int t = 0, joins = 0;
         bool ok = true;
-        // All eight warps have come here (with a limit).
+        // All of these warps have come here (with a limit).
         auto meet = [&]() {
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(ms.join));
@@ -322,6 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
         };
         while (ok && walk.next(ms.plan, a, share.n)) {
             const int b = walk.b, h = walk.h, len = walk.len, live = walk.live, pages = walk.end - walk.begin;
+            auto row_of = [&](int c) {      // of pair c, in q, out and out_lse
+                return ((size_t)b * a.n_rows + ms.plan.col_row[c]) * heads + h * a.group + ms.plan.col_head[c];
+            };
             // Q, each row brought to f16's upper range by a power of two, a row a warp at a time
             uint2 raws[NC / kSoftWarps];
 #pragma unroll
@@ -329,8 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                 const int c = warp + k * kSoftWarps;
                 raws[k] = make_uint2(0u, 0u);
                 if (c < n_cols && ms.plan.col_row[c] < live)
-                    raws[k] = __ldg(reinterpret_cast<const uint2*>(
-                                        a.q + (((size_t)b * a.n_rows + ms.plan.col_row[c]) * heads + h * a.group + ms.plan.col_head[c]) * kD) + lane);
+                    raws[k] = __ldg(reinterpret_cast<const uint2*>(a.q + row_of(c) * kD) + lane);
             }
 #pragma unroll
             for (int k = 0; k < NC / kSoftWarps; ++k) {
@@ -348,10 +394,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                 *reinterpret_cast<uint2*>(dst) =
                     make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
                 if (lane == 0) ms.prow[c] = len - live + (c < n_cols ? min((int)ms.plan.col_row[c], live - 1) : live - 1);
-                if (lane < 4) ms.fz[lane + (c >= NH ? 4 : 0)][c >= NH ? c - NH : c] =
-                    make_float2(__uint_as_float((uint32_t)(254 - up) << 23) * a.scale_log2, kShift);
+                if (lane < 4)
+                    ms.fz[4 * (c / NH) + lane][c % NH] = make_float2(__uint_as_float((uint32_t)(254 - up) << 23) * a.scale_log2, kShift);
             }
-            ref[lane] = kNoScore;
+            if (lane < NH) ref[lane] = kNoScore;
             ptx::fence_proxy_async_smem();
             if (!meet()) break;                        // (the factors are written by other warps)
             if (lane == 0) ptx::mbar_arrive(bar(ms.q_ready));
@@ -410,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                     ptx::mbar_arrive(bar(ms.vote[t & 1]));
                 }
                 if (!(ok = warp_wait(bar(ms.vote[t & 1]), (t >> 1) & 1, abort, status))) break;
-                if (*reinterpret_cast<const volatile unsigned long long*>(ms.flag[t & 1]) != 0) {
+                const volatile unsigned long long* flags = reinterpret_cast<const volatile unsigned long long*>(ms.flag[t & 1]);
+                if ((flags[0] | flags[1]) != 0) {
                     // columns' maxima over the tile's keys, by warp, then over the four warps that share them
 #pragma unroll
                     for (int c = 0; c < NH; ++c) {
@@ -420,7 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                     if (!meet()) break;
                     float r_by = 1.0f;
                     if (vmax > R) {
-                        const float up = __uint_as_float(min((__float_as_uint(vmax) + 0x7FFFFFu) & 0x7F800000u, 0x7F000000u));
+                        const uint32_t next = (__float_as_uint(vmax) + 0x7FFFFFu) & 0x7F800000u;
+                        const float up = __uint_as_float(min(next, 0x7F000000u));
                         r_by = R / up;
                         R = up;
                         inv_r = 1.0f / up;
@@ -505,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                 float sum = (v.x + v.y) + (v.z + v.w);
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const float at = c < NH ? ms.ref[0][c] : ms.ref[kSoftWarps / 2][c - NH];
+                const float at = ms.ref[4 * (c / NH)][c % NH];
                 const float m = at == kNoScore ? -INFINITY : at - kShift;
                 float by = 0.0f;
                 if (c < n_cols && ms.plan.col_row[c] < live) {
@@ -514,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                         const int head = h * a.group + ms.plan.col_head[c];
                         const Finish fin = finish(m, sum, a.sink, head);
                         by *= fin.by;
-                        if (lane == 0 && a.out_lse) a.out_lse[((size_t)b * a.n_rows + ms.plan.col_row[c]) * heads + head] = fin.lse;
+                        if (lane == 0 && a.out_lse) a.out_lse[row_of(c)] = fin.lse;
                     } else if (lane == 0) {
                         a.part_ml[part + c] = make_float2(m, sum);
                     }
@@ -535,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const AttnPa
                 v.z *= by;
                 v.w *= by;
                 if (walk.whole)
-                    store_row(a.out + (((size_t)b * a.n_rows + ms.plan.col_row[c]) * heads + h * a.group + ms.plan.col_head[c]) * kD + 4 * lane, v);
+                    store_row(a.out + row_of(c) * kD + 4 * lane, v);
                 else
                     reinterpret_cast<float4*>(a.part_o + (part + c) * kD)[lane] = v;
             }
@@ -558,7 +606,7 @@ cudaError_t launch(const AttnPagedArgs& a, const uint8_t* k, const uint8_t* v, c
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    pdl_config(&cfg, attr, dim3((unsigned)a.n_ctas), dim3(kThreads), Shape<NC>::kBytes, stream);
+    pdl_config(&cfg, attr, dim3((unsigned)a.n_ctas), dim3(Shape<NC>::kThreads), Shape<NC>::kBytes, stream);
     return cudaLaunchKernelEx(&cfg, attn_paged_tc_kernel<kInt8, NC>, a, k, v);
 }
 
