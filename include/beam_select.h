@@ -34,7 +34,7 @@ extern "C" {
  *   n_beams       1..VA_BEAM_MAX_BEAMS; n_out 1..VA_SAMPLE_MAX_K; n_groups 1..VA_BEAM_MAX_GROUPS
  *   parents, tokens  device int32 [n_groups][n_out]: hypothesis (0..n_beams-1) and token, best first; -1 and
  *                 -1 past the candidates there are
- *   out_scores    device float [n_groups][n_out]; -inf past the candidates there are
+ *   out_scores    device float [n_groups][n_out]; -inf past the candidates there are (not the memory of `scores`)
  *   workspace     device memory of va_beam_workspace_bytes bytes, 16-byte aligned, zeroed once before its first
  *                 use; every call leaves its counters at zero, so that it serves calls of any smaller shape.
  *                 Calls that may run at the same time need their own.

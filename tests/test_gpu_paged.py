@@ -68,6 +68,30 @@ def test_append_is_the_oracles_bit_for_bit(fmt, lens, live, rows, kv, spread):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("exponent", [0, 100, -70, -79, -81, -100, -120])      # of the blocks' largest value
+def test_append_rounds_every_quotient_of_bfloat16_values_correctly(fmt, exponent):
+    """A block for each of the 128 significands of the largest value; in it, each significand of an element under 15
+    exponents (and their negatives).  Then a larger row: the 15 before it are coded again from their codes."""
+    top = (1 + np.arange(128) / 128) * 2.0 ** exponent
+    x = np.zeros((128, 16, 1, D), np.float32)
+    for r in range(15):
+        x[:, r, 0] = (-1) ** r * (1 + np.arange(128) / 128) * 2.0 ** (exponent - 1 - r)
+    x[:, 14, 0, 0] = top
+    x[:, 15, 0] = x[:, 3, 0] * 1.5
+    x[:, 15, 0, 5] = 2 * top[::-1]
+    c = Cache(29, [0] * 128, 1, fmt, spare=128)
+    c.table = [[b] for b in range(128)]
+    dev = c.dev(0)
+    for start, end in ((0, 15), (15, 16)):
+        t, rows = bf16(x[:, start:end])
+        va.kv_page_append_b8(t.cuda(), t.cuda(), ints([end - start] * 128), ints([end] * 128), ints(c.table), *dev)
+        for w in "kv":
+            for b in range(128):
+                P.append(rows[b].astype(np.float32), start, end, c.table[b], c.codes[w][0], c.scale[w][0], fmt)
+        _check_pool(c, dev)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_append_codes_infinities_and_nan_and_says_so(fmt):
     c = Cache(22, [37, 64], 2, fmt)
     dev = c.dev(0)
