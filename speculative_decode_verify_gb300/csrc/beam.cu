@@ -13,6 +13,7 @@
 // 117 us for 32 x 8 x 151,669 bf16 logits, keys and a ranking for every tile's candidates 56 us; this takes 50 us with
 // four CTAs an SM (52 with three, 59 with two), and with a list for every warp instead of the CTA's, which needs no
 // barriers but eight times the insertions, 67 us.
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -36,10 +37,14 @@ constexpr int kMaxTiles = VA_SAMPLE_MAX_VOCAB / kTileLogits;          // 32
 constexpr int kMaxMerge = kMaxK * kMaxTiles;                          // a row's tile keys
 constexpr int kMaxFinal = kMaxK * VA_BEAM_MAX_BEAMS;                  // a request's candidates
 constexpr int kWarps = kThreads / 32;
+constexpr int kHold = 64;                                             // keys that wait for a ranking
+constexpr int kDirect = 256;                                          // keys that are ranked without a bound first
+constexpr int kMaskWords = (kMaxRows + 31) / 32;
 
 struct BeamSmem {
-    uint64_t cand[kMaxMerge];   // run: its best so far, then a tile's candidates; row and request: what is ranked
-    uint64_t best[kMaxK];       // run: the new best
+    uint64_t cand[kMaxMerge];   // run: its best at the last ranking, then the candidates since; row and request: what is ranked
+    uint64_t best[2][kMaxK];    // run: the best of a ranking, in turn
+    int count[3];               // run: candidates of a tile, in turn
     uint64_t red[kWarps];
     uint32_t wmin[kWarps];
     float fred[kWarps], fsum[kWarps];
@@ -50,6 +55,8 @@ struct BeamSmem {
     uint64_t tau;
     double max, log_sum;
     int n_cand, last;
+    uint32_t live[kMaskWords];  // rows that are not finished
+    int live_before[kWarps], row0, n_live;
 };
 
 struct BeamArgs {
@@ -96,94 +103,175 @@ template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs a) {
     __shared__ BeamSmem sm;
     constexpr int kVec = kBf16 ? 8 : 4, kBytes = kBf16 ? 2 : 4;   // logits per 16 bytes
+    constexpr int kWords = kPerThread * kBytes / 4;               // a thread's part of a tile, in 32-bit words
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n_tiles = a.n_tiles, k = a.k;
-    // this CTA's share of the (row, tile) units, in order
-    const unsigned units = (unsigned)a.n_rows * n_tiles;      // at most 2^20, by fewer than 2^11 CTAs
-    const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
     auto row_at = [&](int row) { return static_cast<const unsigned char*>(a.logits) + (size_t)row * a.stride * kBytes; };
-    auto prefetch = [&](int u) {
-        if (tid == 0 && u < u1) {
-            const int first = u % n_tiles * kTileLogits, n = min(kTileLogits, a.vocab - first) * kBytes & ~15;
-            if (n > 0) ptx::bulk_prefetch_l2(row_at(u / n_tiles) + (size_t)first * kBytes, (uint32_t)n);
+    auto prefetch = [&](int row, int tile) {      // into L2
+        if (tid == 0) {
+            const int first = tile * kTileLogits, n = min(kTileLogits, a.vocab - first) * kBytes & ~15;
+            if (n > 0) ptx::bulk_prefetch_l2(row_at(row) + (size_t)first * kBytes, (uint32_t)n);
         }
     };
+    // a share of u units, of which a CTA begins at the same place if no row is finished
+    auto begin_of = [&](unsigned units, unsigned cta) { return (int)(units * cta / gridDim.x); };
     ptx::griddep_launch_dependents();
-    prefetch(u0);          // pulled into L2 before the dependency resolves, as in the sampler
+    {   // pulled into L2 before the dependency resolves, as in the sampler
+        const int u = begin_of((unsigned)a.n_rows * n_tiles, blockIdx.x);
+        prefetch(u / n_tiles, u % n_tiles);
+    }
     ptx::griddep_wait();
-    const float l2e = 1.4426950408889634f;
+    // The rows that are not finished, and this CTA's share of their (row, tile) units (at most 2^20, by fewer than 2^11
+    // CTAs), in order: u0 .. u1 - 1, beginning in row row0, which is number u0 / n_tiles of them.
+    int n_live = a.n_rows, row = 0, next = 0;
+    if (a.finished) {
+        for (int r0 = warp * 32; r0 < a.n_rows; r0 += kThreads) {
+            const uint32_t bits = __ballot_sync(0xffffffffu, r0 + lane < a.n_rows && __ldcg(a.finished + min(r0 + lane, a.n_rows - 1)) == 0);
+            if (lane == 0) sm.live[r0 / 32] = bits;
+        }
+        __syncthreads();
+        // words w0 .. w0 + per - 1 of a thread, and the live rows before them
+        const int words = (a.n_rows + 31) / 32, per = (words + kThreads - 1) / kThreads, w0 = tid * per;
+        int mine = 0;
+        for (int w = w0; w < min(w0 + per, words); ++w) mine += __popc(sm.live[w]);
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += t;
+        }
+        if (lane == 31) sm.live_before[warp] = upto;
+        __syncthreads();
+        n_live = 0;
+        int before = upto - mine;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            before += w < warp ? sm.live_before[w] : 0;
+            n_live += sm.live_before[w];
+        }
+        int target = begin_of((unsigned)n_live * n_tiles, blockIdx.x) / n_tiles - before;
+        if (target >= 0 && target < mine)
+            for (int w = w0;; ++w) {
+                const int here = __popc(sm.live[w]);
+                if (target < here) {
+                    sm.row0 = w * 32 + (int)__fns(sm.live[w], 0u, target + 1);
+                    break;
+                }
+                target -= here;
+            }
+        __syncthreads();
+        row = sm.row0;
+    }
+    const unsigned units = (unsigned)n_live * n_tiles;
+    const int u0 = begin_of(units, blockIdx.x), u1 = begin_of(units, blockIdx.x + 1);
+    if (!a.finished) row = u0 / n_tiles;
+    // the live row after one
+    auto row_after = [&](int row) {
+        if (!a.finished) return row + 1;
+        int w = (row + 1) / 32;
+        const int words = (a.n_rows + 31) / 32;
+        if (w >= words) return a.n_rows;
+        uint32_t bits = sm.live[w] & (0xFFFFFFFFu << ((row + 1) & 31));
+        while (bits == 0u && ++w < words) bits = sm.live[w];
+        return bits == 0u ? a.n_rows : w * 32 + __ffs(bits) - 1;
+    };
+    const float l2e = 1.4426950408889634f, lowest = __uint_as_float(kBf16 ? 0xFF7F0000u : 0xFF7FFFFFu);
     int run = 0;                            // tiles of the run so far
+    int held = 0, turn = 0;                 // keys in cand; which of the two best is next
+    float tau = 0.0f;                       // candidates are at least this
+    if (tid < 2 * kMaxK) sm.best[tid / kMaxK][tid % kMaxK] = 0ull;
     float m = -INFINITY, sum = 0.0f;        // this thread's maximum of them, and its sum of exp(l - m)
-    for (int u = u0; u < u1; ++u) {
-        const int row = u / n_tiles, tile = u % n_tiles, first = tile * kTileLogits;
+    if (u0 < u1) {
+        next = row_after(row);
+        if (u0 + 1 < u1) prefetch((u0 + 1) % n_tiles ? row : next, (u0 + 1) % n_tiles);
+    }
+    // then, for the finished rows of this CTA (u >= u1), their only candidate
+    int ended = blockIdx.x;
+    for (int u = u0;; ++u) {
+        bool done = u >= u1;
+        if (done) {
+            if (!a.finished) break;
+            while (ended < a.n_rows && (sm.live[ended / 32] >> (ended & 31) & 1u)) ended += gridDim.x;
+            if (ended >= a.n_rows) break;
+            row = ended;
+            ended += gridDim.x;
+        }
+        const int number = u / n_tiles, tile = u % n_tiles, first = tile * kTileLogits;    // of a live row
+        if (!done && tile == 0 && u != u0) {
+            row = next;
+            next = row_after(row);
+        }
         const unsigned char* src = row_at(row);
-        prefetch(u + 1);
-        const bool done = a.finished && __ldcg(a.finished + row) != 0;
         const float base = __ldcg(a.scores + row);
         if (!done) {
+            if (u + 2 < u1 && (u + 2) / n_tiles - number < 2)
+                prefetch((u + 2) / n_tiles == number ? row : next, (u + 2) % n_tiles);
             // -------------------------------------------------------- tile
-            float f[kPerThread];
+            uint32_t w[kWords];          // as they are in memory
             const int n_in = min(kTileLogits, a.vocab - first);
 #pragma unroll
-            for (int i = 0; i < kPerThread / kVec; ++i) {
+            for (int i = 0; i < kWords / 4; ++i) {
                 const int at = (i * kThreads + tid) * kVec;
-                uint32_t w[4];
                 if (at + kVec <= n_in) {
                     const uint4 raw = __ldcs(reinterpret_cast<const uint4*>(src + (size_t)(first + at) * kBytes));
-                    w[0] = raw.x;
-                    w[1] = raw.y;
-                    w[2] = raw.z;
-                    w[3] = raw.w;
+                    w[4 * i] = raw.x;
+                    w[4 * i + 1] = raw.y;
+                    w[4 * i + 2] = raw.z;
+                    w[4 * i + 3] = raw.w;
                 } else {   // the row's end: entry by entry, -inf behind it
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         if (kBf16) {
-                            uint32_t v = 0;
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int x = at + 2 * c + e;
-                                v |= (x < n_in ? (uint32_t)*reinterpret_cast<const uint16_t*>(src + (size_t)(first + x) * 2) : 0xFF80u)
-                                     << (16 * e);
-                            }
-                            w[c] = v;
+                            const uint16_t* e = reinterpret_cast<const uint16_t*>(src) + first;
+                            const int x = at + 2 * c;
+                            w[4 * i + c] = (x < n_in ? (uint32_t)e[x] : 0xFF80u) | (x + 1 < n_in ? (uint32_t)e[x + 1] : 0xFF80u) << 16;
                         } else {
                             const int x = at + c;
-                            w[c] = x < n_in ? *reinterpret_cast<const uint32_t*>(src + (size_t)(first + x) * 4) : 0xFF800000u;
+                            w[4 * i + c] = x < n_in ? reinterpret_cast<const uint32_t*>(src)[first + x] : 0xFF800000u;
                         }
                     }
                 }
+            }
+            // a NaN is no candidate: -inf; the thread's largest
+            float mine = -INFINITY;
+            if (kBf16) {
+                const __nv_bfloat162 low = __floats2bfloat162_rn(-INFINITY, -INFINITY);
+                __nv_bfloat162 top = low;
 #pragma unroll
-                for (int c = 0; c < kVec; ++c) {
-                    const float x = kBf16 ? __uint_as_float((c & 1) ? (w[c / 2] & 0xFFFF0000u) : (w[c / 2] << 16))
-                                          : __uint_as_float(w[c & 3]);
-                    f[i * kVec + c] = fmaxf(x, -INFINITY);      // a NaN is no candidate: -inf
+                for (int c = 0; c < kWords; ++c) {
+                    const __nv_bfloat162 x = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&w[c]), low);
+                    w[c] = *reinterpret_cast<const uint32_t*>(&x);
+                    top = __hmax2(top, x);
+                }
+                mine = fmaxf(__low2float(top), __high2float(top));
+            } else {
+#pragma unroll
+                for (int c = 0; c < kWords; ++c) {
+                    const float x = fmaxf(__uint_as_float(w[c]), -INFINITY);
+                    w[c] = __float_as_uint(x);
+                    mine = fmaxf(mine, x);
                 }
             }
-            float mine = -INFINITY;      // the thread's largest
-#pragma unroll
-            for (int e = 0; e < kPerThread; ++e) mine = fmaxf(mine, f[e]);
+            auto f = [&](int e) {        // the thread's logit e
+                return __uint_as_float(kBf16 ? ((e & 1) ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16) : w[e]);
+            };
+            auto place_of = [&](int e) { return first + ((e / kVec) * kThreads + tid) * kVec + e % kVec; };
             // sums, as 2^(l log2 e + off); a maximum for which off has no digits takes the careful way
             if (mine > -INFINITY) {
                 const float up = fmaxf(m, mine), off = -up * l2e;
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < kPerThread; ++e) part[e & 3] += ptx::ex2(fmaf(f[e], l2e, off));
+                for (int e = 0; e < kPerThread; ++e) part[e & 3] += ptx::ex2(fmaf(f(e), l2e, off));
                 float add = (part[0] + part[1]) + (part[2] + part[3]);
                 if (!(fabsf(up) < 1024.0f)) {
                     add = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < kPerThread; ++e) add += f[e] == up ? 1.0f : ptx::ex2((f[e] - up) * l2e);
+                    for (int e = 0; e < kPerThread; ++e) add += f(e) == up ? 1.0f : ptx::ex2((f(e) - up) * l2e);
                 }
                 sum = (m == up ? sum : (m == -INFINITY ? 0.0f : sum * ptx::ex2((m - up) * l2e))) + add;
                 m = up;
             }
-            // the bound that candidates have to pass
-            const int held = run > 0 ? k : 0;
-            float tau;
-            if (run > 0) {
-                const uint64_t kth = sm.cand[k - 1];
-                tau = kth != 0ull ? ord_to_float((uint32_t)(kth >> 32) + 1u) : -FLT_MAX;   // the next larger float
-            } else {
+            if (run == 0) {
                 // A lower bound of the tile's k-th largest logit: with f warps whose 32 threads all hold logits and
                 // j = ceil(k / f), the smallest over those warps of the warp's j-th largest distinct thread maximum
                 // (one warp-wide maximum a round).  Fewer than 32 threads of logits: every logit is a candidate.
@@ -195,22 +283,30 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                     v = v == low ? 0u : v;
                 }
                 if (lane == 0) sm.wmin[warp] = warp < full_warps ? low : 0xFFFFFFFFu;
+                if (tid == 0) sm.count[0] = 0;
                 __syncthreads();
                 uint32_t least = sm.wmin[0];
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) least = min(least, sm.wmin[w]);
                 if (full_warps == 0) least = 0u;
-                tau = least > ord_bits(-INFINITY) ? ord_to_float(least) : -FLT_MAX;
+                tau = least > ord_bits(-INFINITY) ? ord_to_float(least) : lowest;
+                held = 0;
             }
-            unsigned bits = 0;
-            if (mine >= tau) {
+            // candidates behind those that wait: a warp's take consecutive places.  The tile's counter is cleared two
+            // barriers before its use, and read before the next barrier.
+            if (tid == 0) sm.count[(run + 1) % 3] = 0;
+            if (__any_sync(0xffffffffu, mine >= tau)) {
+                // bit b: in bf16 half b / 16 of word b % 16, else word b
+                unsigned bits = 0;
+                if (kBf16) {
+                    const __nv_bfloat162 bound = __float2bfloat162_rn(tau);      // (tau is one of them)
 #pragma unroll
-                for (int e = 0; e < kPerThread; ++e) bits |= f[e] >= tau ? 1u << e : 0u;
-            }
-            if (tid == 0) sm.n_cand = held;
-            if (__syncthreads_or(bits != 0)) {
-                // compaction behind the best so far: a warp's candidates take consecutive places; the values are read
-                // again (few are)
+                    for (int c = 0; c < kWords; ++c)
+                        bits |= __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[c]), bound) & (0x10001u << c);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kWords; ++c) bits |= __uint_as_float(w[c]) >= tau ? 1u << c : 0u;
+                }
                 const int cnt = __popc(bits);
                 int incl = cnt;
 #pragma unroll
@@ -219,55 +315,61 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                     if (lane >= o) incl += t;
                 }
                 int slot = 0;
-                if (lane == 31 && incl > 0) slot = atomicAdd(&sm.n_cand, incl);
-                slot = __shfl_sync(0xffffffffu, slot, 31) + incl - cnt;
-                for (unsigned rest = bits; rest != 0; rest &= rest - 1) {
-                    const int e = __ffs(rest) - 1;
-                    const int at = first + ((e / kVec) * kThreads + tid) * kVec + e % kVec;
+                if (lane == 31) slot = atomicAdd(&sm.count[run % 3], incl);
+                slot = held + __shfl_sync(0xffffffffu, slot, 31) + incl - cnt;
+                for (unsigned rest = bits; rest != 0; rest &= rest - 1) {   // the values are read again (few are)
+                    const int b = __ffs(rest) - 1, at = place_of(kBf16 ? 2 * (b & 15) + (b >> 4) : b);
                     const float x = kBf16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src)[at] << 16)
                                           : reinterpret_cast<const float*>(src)[at];
-                    if (slot < held + kMaxCand) sm.cand[slot] = make_key(x, at);
+                    if (slot < kMaxMerge) sm.cand[slot] = make_key(x, at);
                     ++slot;
                 }
-                if (tid < k) sm.best[tid] = 0ull;
-                __syncthreads();
-                int n = sm.n_cand;
-                if (n > held + kMaxCand) {
-                    // many equal logits at the bound: the tile's k best by k rounds of block-wide maximum
-                    uint64_t taken = ~0ull;
-                    for (int r = 0; r < k; ++r) {
-                        uint64_t best = 0;
+            }
+            __syncthreads();
+            int n = held + sm.count[run % 3];
+            if (n > kMaxMerge) {
+                // many equal logits at the bound: the tile's k best by k rounds of block-wide maximum
+                uint64_t taken = ~0ull;
+                for (int r = 0; r < k; ++r) {
+                    uint64_t best = 0;
 #pragma unroll
-                        for (int e = 0; e < kPerThread; ++e) {
-                            const uint64_t kv = f[e] >= tau ? make_key(f[e], first + ((e / kVec) * kThreads + tid) * kVec + e % kVec) : 0ull;
-                            best = kv < taken && kv > best ? kv : best;
-                        }
-                        best = block_max_u64(best, sm.red);
-                        if (tid == 0) sm.cand[held + r] = best;
-                        taken = best;
+                    for (int e = 0; e < kPerThread; ++e) {
+                        const uint64_t kv = f(e) >= tau ? make_key(f(e), place_of(e)) : 0ull;
+                        best = kv < taken && kv > best ? kv : best;
                     }
-                    n = held + k;
-                    __syncthreads();
+                    best = block_max_u64(best, sm.red);
+                    if (tid == 0) sm.cand[held + r] = best;
+                    taken = best;
                 }
+                n = held + k;
+                __syncthreads();
+            }
+            const bool ends = tile == n_tiles - 1 || u + 1 == u1;
+            if (run == 0 || n > kHold || ends) {
                 // rank by counting: a key goes to the place of the number of larger ones, if that is below k
+                if (tid < k) sm.best[turn ^ 1][tid] = 0ull;
                 for (int c = tid; c < n; c += kThreads) {
                     const uint64_t kc = sm.cand[c];
                     int rank = 0;
 #pragma unroll 8
                     for (int o = 0; o < n; ++o) rank += sm.cand[o] > kc;
-                    if (rank < k && kc != 0ull) sm.best[rank] = kc;
+                    if (rank < k && kc != 0ull) sm.best[turn][rank] = kc;
                 }
                 __syncthreads();
-                if (tid < k) sm.cand[tid] = sm.best[tid];
-            } else if (run == 0 && tid < k) {
-                sm.cand[tid] = 0ull;
+                if (tid < k) sm.cand[tid] = sm.best[turn][tid];
+                const uint64_t kth = sm.best[turn][k - 1];
+                // the next larger value of the logits' type
+                tau = kth != 0ull ? ord_to_float((uint32_t)(kth >> 32) + (kBf16 ? 0x10000u : 1u)) : lowest;
+                held = k;
+                turn ^= 1;
+            } else {
+                held = n;
             }
-            __syncthreads();
             ++run;
-            if (tile != n_tiles - 1 && u + 1 != u1) continue;
+            if (!ends) continue;
             // -------------------------------------------------------- the run's end
-            const int c_first = (int)(((unsigned)(row * n_tiles + 1) * gridDim.x - 1u) / units);
-            const int c_last = (int)(((unsigned)((row + 1) * n_tiles) * gridDim.x - 1u) / units);
+            const int c_first = (int)(((unsigned)(number * n_tiles + 1) * gridDim.x - 1u) / units);
+            const int c_last = (int)(((unsigned)((number + 1) * n_tiles) * gridDim.x - 1u) / units);
             const int n_runs = c_last - c_first + 1;
             float top = m;
 #pragma unroll
@@ -289,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                 for (int w = 0; w < kWarps; ++w) all += sm.fsum[w];
                 a.run_stats[place] = make_float2(top, all);
             }
-            if (tid < k) a.run_keys[place * k + tid] = sm.cand[tid];
+            if (tid < k) a.run_keys[place * k + tid] = sm.best[turn ^ 1][tid];
             run = 0;
             m = -INFINITY;
             sum = 0.0f;
@@ -297,9 +399,25 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
             // -------------------------------------------------------- row
             const uint64_t* rw = a.run_keys + (size_t)row * n_tiles * k;
             const int total = n_runs * k;
-            for (int e = tid; e < total; e += kThreads) sm.all[e] = __ldcg(rw + e);
+            const bool direct = total <= kDirect;
+            uint64_t* keys = direct ? sm.cand : sm.all;
+            for (int e = tid; e < total; e += kThreads) keys[e] = __ldcg(rw + e);
+            if (tid < kMaxK) sm.top[tid] = 0ull;
             __syncthreads();
-            if (warp == 0) {
+            if (warp == kWarps - 1) {
+                // log-sum-exp over the runs, one a lane
+                const float2 st = lane < n_runs ? __ldcg(a.run_stats + (size_t)row * n_tiles + lane) : make_float2(-INFINITY, 0.0f);
+                float top = st.x;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                double s = st.x == -INFINITY ? 0.0 : (st.x == top ? (double)st.y : (double)(st.y * expf(st.x - top)));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane == 0) {
+                    sm.max = (double)top;
+                    sm.log_sum = log(s);
+                }
+            } else if (warp == 0 && !direct) {
                 // a lower bound of the row's k-th key: the smallest of every run's ceil(k / runs)-th
                 const int m = min(k, (k + n_runs - 1) / n_runs);
                 uint64_t b = ~0ull;
@@ -313,35 +431,24 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                     sm.tau = b;
                     sm.n_cand = 0;
                 }
-                // log-sum-exp over the runs, one a lane
-                const float2 st = lane < n_runs ? __ldcg(a.run_stats + (size_t)row * n_tiles + lane) : make_float2(-INFINITY, 0.0f);
-                float top = st.x;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                double s = st.x == -INFINITY ? 0.0 : (st.x == top ? (double)st.y : (double)(st.y * expf(st.x - top)));
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane == 0) {
-                    sm.max = (double)top;
-                    sm.log_sum = log(s);
+            }
+            int nc = total;
+            if (!direct) {
+                __syncthreads();
+                const uint64_t lb = sm.tau;
+                for (int e = tid; e < total; e += kThreads) {
+                    const uint64_t kv = sm.all[e];
+                    if (kv >= lb && kv != 0ull) sm.cand[atomicAdd(&sm.n_cand, 1)] = kv;
                 }
-            } else if (warp == 1) {
-                sm.top[lane] = 0ull;
+                __syncthreads();
+                nc = sm.n_cand;
             }
-            __syncthreads();
-            const uint64_t lb = sm.tau;
-            for (int e = tid; e < total; e += kThreads) {
-                const uint64_t kv = sm.all[e];
-                if (kv >= lb && kv != 0ull) sm.cand[atomicAdd(&sm.n_cand, 1)] = kv;
-            }
-            __syncthreads();
-            const int nc = sm.n_cand;
             for (int c = tid; c < nc; c += kThreads) {
                 const uint64_t kc = sm.cand[c];
                 int rank = 0;
 #pragma unroll 8
                 for (int o = 0; o < nc; ++o) rank += sm.cand[o] > kc;
-                if (rank < k) sm.top[rank] = kc;
+                if (rank < k && kc != 0ull) sm.top[rank] = kc;
             }
             __syncthreads();
             if (tid < k) {
@@ -356,8 +463,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                 a.row_tokens[(size_t)row * k + tid] = key_index(kv);
             }
         } else {
-            // a finished hypothesis: the CTA that has its last tile speaks for it
-            if (tile != n_tiles - 1) continue;
+            // a finished hypothesis
             if (tid < k) {
                 a.row_keys[(size_t)row * k + tid] = tid == 0 ? score_key((double)base) : 0ull;
                 a.row_tokens[(size_t)row * k + tid] = a.end_token;
@@ -368,43 +474,54 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         if (!arrive_last(a.group_count + group, 1, a.n_beams, &sm.last)) continue;
         const int total = a.n_beams * k;
         const size_t at = (size_t)group * total;
+        const bool direct = total <= kDirect;
+        uint64_t* keys = direct ? sm.cand : sm.all;
+        if (tid == 0) sm.n_cand = 0;
+        __syncthreads();
+        int mine = 0;
         for (int e = tid; e < total; e += kThreads) {
-            sm.all[e] = __ldcg(a.row_keys + at + e);
+            keys[e] = __ldcg(a.row_keys + at + e);
             sm.tok[e] = __ldcg(a.row_tokens + at + e);
+            if (direct) {
+                sm.who[e] = (int16_t)e;
+                mine += keys[e] != 0ull;
+            }
         }
+        if (direct && mine) atomicAdd(&sm.n_cand, mine);
         __syncthreads();
-        if (warp == 0) {   // a lower bound of the k-th score: the smallest of every hypothesis' ceil(k / beams)-th
-            const int m = (k + a.n_beams - 1) / a.n_beams;
-            uint64_t b = lane < a.n_beams ? sm.all[lane * k + m - 1] : ~0ull;
+        if (!direct) {
+            if (warp == 0) {   // a lower bound of the k-th score: the smallest of every hypothesis' ceil(k / beams)-th
+                const int m = (k + a.n_beams - 1) / a.n_beams;
+                uint64_t b = lane < a.n_beams ? sm.all[lane * k + m - 1] : ~0ull;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const uint64_t w = __shfl_xor_sync(0xffffffffu, b, o);
-                b = w < b ? w : b;
+                for (int o = 16; o > 0; o >>= 1) {
+                    const uint64_t w = __shfl_xor_sync(0xffffffffu, b, o);
+                    b = w < b ? w : b;
+                }
+                if (lane == 0) sm.tau = b;
             }
-            if (lane == 0) {
-                sm.tau = b;
-                sm.n_cand = 0;
+            __syncthreads();
+            const uint64_t lb = sm.tau;
+            for (int e = tid; e < total; e += kThreads) {
+                const uint64_t kv = sm.all[e];
+                if (kv >= lb && kv != 0ull) {
+                    const int i = atomicAdd(&sm.n_cand, 1);
+                    sm.cand[i] = kv;
+                    sm.who[i] = (int16_t)e;
+                }
             }
+            __syncthreads();
         }
-        __syncthreads();
-        const uint64_t lb = sm.tau;
-        for (int e = tid; e < total; e += kThreads) {
-            const uint64_t kv = sm.all[e];
-            if (kv >= lb && kv != 0ull) {
-                const int i = atomicAdd(&sm.n_cand, 1);
-                sm.cand[i] = kv;
-                sm.who[i] = (int16_t)e;
-            }
-        }
-        __syncthreads();
-        const int nc = sm.n_cand;
+        // nc candidates among the `in` keys: larger ones first, of equal ones the earlier (its hypothesis, then its order)
+        const int nc = sm.n_cand, in = direct ? total : nc;
         const size_t out = (size_t)group * k;
-        for (int c = tid; c < nc; c += kThreads) {
+        for (int c = tid; c < in; c += kThreads) {
             const uint64_t kc = sm.cand[c];
             const int e = sm.who[c];
+            if (kc == 0ull) continue;
             int rank = 0;
-#pragma unroll 4
-            for (int o = 0; o < nc; ++o) rank += sm.cand[o] > kc || (sm.cand[o] == kc && sm.who[o] < e);
+#pragma unroll 8
+            for (int o = 0; o < in; ++o) rank += (int)(sm.cand[o] > kc) | ((int)(sm.cand[o] == kc) & (int)(sm.who[o] < e));
             if (rank < k) {
                 a.parents[out + rank] = e / k;
                 a.tokens[out + rank] = sm.tok[e];
