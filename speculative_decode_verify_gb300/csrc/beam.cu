@@ -1,18 +1,23 @@
 // va_beam_select: beam search's selection over beams and vocabulary.
 //
-// One launch, three levels.  The (row, 8,192-logit tile) units are dealt evenly to four CTAs an SM; a run is a CTA's
-// consecutive tiles of one row.  A CTA reads a tile's logits once (the next tile's are on their way into L2):
+// One launch, three levels.  The (row, 8,192-logit tile) units of the rows that are not finished are dealt evenly to
+// four CTAs an SM; a run is a CTA's consecutive tiles of one row.  A CTA reads a tile's logits once (the next two
+// tiles' are on their way into L2), and keeps them as they are in memory:
 //   sums        every thread keeps its own maximum m and sum of exp(l - m) over the run
-//   candidates  the run's k best keys so far are kept sorted in shared memory.  The first tile collects against a lower
-//               bound of its k-th logit, as the sampler does; a later one only the logits above the k-th so far (its
-//               indices are higher, so equal ones lose), few of which are left to rank.
+//   candidates  the run's k best keys at the last ranking, sorted in shared memory, and the candidates since.  The first
+//               tile collects against a lower bound of its k-th logit, as the sampler does; later ones only the logits
+//               above the k-th at the last ranking (their indices are higher, so equal ones lose).  A ranking comes
+//               with the first tile, the last, and when more than 64 keys wait; a tile without one costs one barrier.
 // The last run of a row to arrive merges the runs: log-sum-exp in 64 bits, the row's k best keys and their scores in
 // 64 bits.  The last row of a request merges the hypotheses.  Every order is fixed by the keys and by the deal, so the
 // arrivals' order changes nothing.
-// Bytes: the logits once; what a run hands on (k keys) is a thousandth of that.  A 64-bit key for every logit took
-// 117 us for 32 x 8 x 151,669 bf16 logits, keys and a ranking for every tile's candidates 56 us; this takes 50 us with
-// four CTAs an SM (52 with three, 59 with two), and with a list for every warp instead of the CTA's, which needs no
-// barriers but eight times the insertions, 67 us.
+// Bytes: the logits once; what a run hands on (k keys) is a thousandth of that.  32 x 8 x 151,669 bf16 logits, 38 of the
+// 256 rows finished (66 MB), take 36.9 us: the tiles' instructions bound it (0.6 us a tile and SM), then the start and
+// the merges, which are chains of round trips (5 us and 7 us).  On the way: a 64-bit key for every logit 117 us, a
+// ranking for every tile 50 us, finished rows in the deal 50 us, a division for every tile and 32 keys kept in registers
+// for the equal logits' sake 39 us; a list for every warp, which needs no barriers but eight times the insertions,
+// 67 us; three CTAs an SM 37.2 us, the next tile's loads before the barrier 38.3 us (36.5 us with three CTAs).
+// 1 x 4 x 160,000 logits: 9.7 us, all of it such chains.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -126,7 +131,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
     int n_live = a.n_rows, row = 0, next = 0;
     if (a.finished) {
         for (int r0 = warp * 32; r0 < a.n_rows; r0 += kThreads) {
-            const uint32_t bits = __ballot_sync(0xffffffffu, r0 + lane < a.n_rows && __ldcg(a.finished + min(r0 + lane, a.n_rows - 1)) == 0);
+            const bool here = r0 + lane < a.n_rows && __ldcg(a.finished + r0 + lane) == 0;
+            const uint32_t bits = __ballot_sync(0xffffffffu, here);
             if (lane == 0) sm.live[r0 / 32] = bits;
         }
         __syncthreads();
@@ -177,35 +183,39 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
     };
     const float l2e = 1.4426950408889634f, lowest = __uint_as_float(kBf16 ? 0xFF7F0000u : 0xFF7FFFFFu);
     int run = 0;                            // tiles of the run so far
-    int held = 0, turn = 0;                 // keys in cand; which of the two best is next
+    int held = 0, turn = 0, counter = 0;    // keys in cand; which of the two best, of the three counters is next
     float tau = 0.0f;                       // candidates are at least this
     if (tid < 2 * kMaxK) sm.best[tid / kMaxK][tid % kMaxK] = 0ull;
     float m = -INFINITY, sum = 0.0f;        // this thread's maximum of them, and its sum of exp(l - m)
+    int number = u0 / n_tiles, tile = u0 - number * n_tiles;       // the tile at hand: of which live row, which of it
     if (u0 < u1) {
         next = row_after(row);
-        if (u0 + 1 < u1) prefetch((u0 + 1) % n_tiles ? row : next, (u0 + 1) % n_tiles);
+        if (u0 + 1 < u1) prefetch(tile + 1 < n_tiles ? row : next, tile + 1 < n_tiles ? tile + 1 : 0);
     }
     // then, for the finished rows of this CTA (u >= u1), their only candidate
     int ended = blockIdx.x;
-    for (int u = u0;; ++u) {
-        bool done = u >= u1;
+    for (int u = u0;; ++u, ++tile) {
+        const bool done = u >= u1;
         if (done) {
             if (!a.finished) break;
             while (ended < a.n_rows && (sm.live[ended / 32] >> (ended & 31) & 1u)) ended += gridDim.x;
             if (ended >= a.n_rows) break;
             row = ended;
             ended += gridDim.x;
-        }
-        const int number = u / n_tiles, tile = u % n_tiles, first = tile * kTileLogits;    // of a live row
-        if (!done && tile == 0 && u != u0) {
+        } else if (tile == n_tiles) {
+            tile = 0;
+            ++number;
             row = next;
             next = row_after(row);
         }
         const unsigned char* src = row_at(row);
-        const float base = __ldcg(a.scores + row);
         if (!done) {
-            if (u + 2 < u1 && (u + 2) / n_tiles - number < 2)
-                prefetch((u + 2) / n_tiles == number ? row : next, (u + 2) % n_tiles);
+            const int first = tile * kTileLogits;
+            if (u + 2 < u1) {       // the tile after the next
+                const bool over = tile + 2 >= n_tiles;
+                const int then = over ? tile + 2 - n_tiles : tile + 2;
+                if (then < n_tiles) prefetch(over ? next : row, then);
+            }
             // -------------------------------------------------------- tile
             uint32_t w[kWords];          // as they are in memory
             const int n_in = min(kTileLogits, a.vocab - first);
@@ -224,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                         if (kBf16) {
                             const uint16_t* e = reinterpret_cast<const uint16_t*>(src) + first;
                             const int x = at + 2 * c;
-                            w[4 * i + c] = (x < n_in ? (uint32_t)e[x] : 0xFF80u) | (x + 1 < n_in ? (uint32_t)e[x + 1] : 0xFF80u) << 16;
+                            const uint32_t lo = x < n_in ? e[x] : 0xFF80u, hi = x + 1 < n_in ? e[x + 1] : 0xFF80u;
+                            w[4 * i + c] = lo | hi << 16;
                         } else {
                             const int x = at + c;
                             w[4 * i + c] = x < n_in ? reinterpret_cast<const uint32_t*>(src)[first + x] : 0xFF800000u;
@@ -283,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                     v = v == low ? 0u : v;
                 }
                 if (lane == 0) sm.wmin[warp] = warp < full_warps ? low : 0xFFFFFFFFu;
-                if (tid == 0) sm.count[0] = 0;
+                if (tid == 0) sm.count[counter] = 0;
                 __syncthreads();
                 uint32_t least = sm.wmin[0];
 #pragma unroll
@@ -294,7 +305,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
             }
             // candidates behind those that wait: a warp's take consecutive places.  The tile's counter is cleared two
             // barriers before its use, and read before the next barrier.
-            if (tid == 0) sm.count[(run + 1) % 3] = 0;
+            const int mine_is = counter;
+            counter = counter == 2 ? 0 : counter + 1;
+            if (tid == 0) sm.count[counter] = 0;
             if (__any_sync(0xffffffffu, mine >= tau)) {
                 // bit b: in bf16 half b / 16 of word b % 16, else word b
                 unsigned bits = 0;
@@ -315,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                     if (lane >= o) incl += t;
                 }
                 int slot = 0;
-                if (lane == 31) slot = atomicAdd(&sm.count[run % 3], incl);
+                if (lane == 31) slot = atomicAdd(&sm.count[mine_is], incl);
                 slot = held + __shfl_sync(0xffffffffu, slot, 31) + incl - cnt;
                 for (unsigned rest = bits; rest != 0; rest &= rest - 1) {   // the values are read again (few are)
                     const int b = __ffs(rest) - 1, at = place_of(kBf16 ? 2 * (b & 15) + (b >> 4) : b);
@@ -326,12 +339,14 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                 }
             }
             __syncthreads();
-            int n = held + sm.count[run % 3];
+            int n = held + sm.count[mine_is];
             if (n > kMaxMerge) {
                 // many equal logits at the bound: the tile's k best by k rounds of block-wide maximum
                 uint64_t taken = ~0ull;
                 for (int r = 0; r < k; ++r) {
                     uint64_t best = 0;
+#pragma unroll
+                    for (int c = 0; c < kWords; ++c) asm volatile("" : "+r"(w[c]));     // no 32 keys kept over the rounds
 #pragma unroll
                     for (int e = 0; e < kPerThread; ++e) {
                         const uint64_t kv = f(e) >= tau ? make_key(f(e), place_of(e)) : 0ull;
@@ -344,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                 n = held + k;
                 __syncthreads();
             }
-            const bool ends = tile == n_tiles - 1 || u + 1 == u1;
+            const bool ends = tile + 1 == n_tiles || u + 1 == u1;
             if (run == 0 || n > kHold || ends) {
                 // rank by counting: a key goes to the place of the number of larger ones, if that is below k
                 if (tid < k) sm.best[turn ^ 1][tid] = 0ull;
@@ -457,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                 if (kv != 0ull) {
                     const double l = (double)ord_to_float((uint32_t)(kv >> 32));
                     const double above = l == sm.max ? 0.0 : l - sm.max;
-                    sk = score_key((double)base + (above - sm.log_sum));
+                    sk = score_key((double)__ldcg(a.scores + row) + (above - sm.log_sum));
                 }
                 a.row_keys[(size_t)row * k + tid] = sk;
                 a.row_tokens[(size_t)row * k + tid] = key_index(kv);
@@ -465,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         } else {
             // a finished hypothesis
             if (tid < k) {
-                a.row_keys[(size_t)row * k + tid] = tid == 0 ? score_key((double)base) : 0ull;
+                a.row_keys[(size_t)row * k + tid] = tid == 0 ? score_key((double)__ldcg(a.scores + row)) : 0ull;
                 a.row_tokens[(size_t)row * k + tid] = a.end_token;
             }
         }

@@ -85,6 +85,31 @@ def test_equal_logits_go_to_the_lowest_token_and_hypothesis():
     assert pa.tolist() == [[0, 1, 0, 0]] and tk.tolist() == [[17777, 17777, 0, 1]]
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("finished", [None, "some", "all"])
+def test_runs_of_many_tiles(dtype, finished):
+    """2,080 tiles: several a CTA, over the ends of rows.  Rows whose every tile beats the one before (more candidates
+    than are kept), fall, are constant, have few values or only their last ones; finished rows among them."""
+    rows, vocab, beams, k = 160, 100001, 5, 12
+    rng = np.random.default_rng(8)
+    x = _rows(9, rows, vocab, dtype)
+    for i, row in enumerate(rng.permutation(rows)[:40].tolist()):
+        line = torch.linspace(-6, 6, vocab, device="cuda")
+        x[row] = (line, -line, 0 * line + 1.5, (line * 0.5).round(), torch.where(line > 5.9999, line, -np.inf))[i % 5].to(dtype)
+    fin = None
+    if finished:
+        fin = (rng.random(rows) < 0.4).astype(np.int32) if finished == "some" else np.ones(rows, np.int32)
+        fin[35:40], fin[40:45] = 1, fin[40:45] if finished == "all" else 0
+        fin = fin.tolist()
+    _check(x, -5 + rng.standard_normal(rows), beams, k, finished=fin, end=4)
+
+
+def test_more_rows_than_ctas():
+    rng = np.random.default_rng(2)
+    fin = (rng.random(3000) < 0.5).astype(np.int32).tolist()
+    _check(_rows(11, 3000, 50, torch.float32), -5 + 0.5 * rng.permutation(3000), 3, 4, finished=fin, end=49)
+
+
 def test_one_workspace_for_every_shape_and_a_captured_call():
     ws = torch.zeros(va.va_beam_workspace_bytes(6, 8, 60000, 32), dtype=torch.uint8, device="cuda")
     rng = np.random.default_rng(1)
