@@ -12,12 +12,12 @@
 // 64 bits.  The last row of a request merges the hypotheses.  Every order is fixed by the keys and by the deal, so the
 // arrivals' order changes nothing.
 // Bytes: the logits once; what a run hands on (k keys) is a thousandth of that.  32 x 8 x 151,669 bf16 logits, 38 of the
-// 256 rows finished (66 MB), take 36.9 us: the tiles' instructions bound it (0.6 us a tile and SM), then the start and
+// 256 rows finished (66 MB), take 37.4 us: the tiles' instructions bound it (0.6 us a tile and SM), then the start and
 // the merges, which are chains of round trips (5 us and 7 us).  On the way: a 64-bit key for every logit 117 us, a
 // ranking for every tile 50 us, finished rows in the deal 50 us, a division for every tile and 32 keys kept in registers
 // for the equal logits' sake 39 us; a list for every warp, which needs no barriers but eight times the insertions,
 // 67 us; three CTAs an SM 37.2 us, the next tile's loads before the barrier 38.3 us (36.5 us with three CTAs).
-// 1 x 4 x 160,000 logits: 9.7 us, all of it such chains.
+// 1 x 4 x 160,000 logits, one row finished: 10.8 us, all of it such chains.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -118,11 +118,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
             if (n > 0) ptx::bulk_prefetch_l2(row_at(row) + (size_t)first * kBytes, (uint32_t)n);
         }
     };
-    // a share of u units, of which a CTA begins at the same place if no row is finished
-    auto begin_of = [&](unsigned units, unsigned cta) { return (int)(units * cta / gridDim.x); };
+    // where CTA `cta` of `ctas` begins in `units` >= ctas units; those behind the last have none
+    auto begin_of = [](unsigned units, unsigned ctas, unsigned cta) { return cta < ctas ? (int)(units * cta / ctas) : (int)units; };
     ptx::griddep_launch_dependents();
     {   // pulled into L2 before the dependency resolves, as in the sampler
-        const int u = begin_of((unsigned)a.n_rows * n_tiles, blockIdx.x);
+        const int u = begin_of((unsigned)a.n_rows * n_tiles, gridDim.x, blockIdx.x);
         prefetch(u / n_tiles, u % n_tiles);
     }
     ptx::griddep_wait();
@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
             before += w < warp ? sm.live_before[w] : 0;
             n_live += sm.live_before[w];
         }
-        int target = begin_of((unsigned)n_live * n_tiles, blockIdx.x) / n_tiles - before;
+        const unsigned units = (unsigned)n_live * n_tiles;
+        int target = begin_of(units, min(gridDim.x, units), blockIdx.x) / n_tiles - before;
         if (target >= 0 && target < mine)
             for (int w = w0;; ++w) {
                 const int here = __popc(sm.live[w]);
@@ -168,8 +169,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         __syncthreads();
         row = sm.row0;
     }
-    const unsigned units = (unsigned)n_live * n_tiles;
-    const int u0 = begin_of(units, blockIdx.x), u1 = begin_of(units, blockIdx.x + 1);
+    const unsigned units = (unsigned)n_live * n_tiles, ctas = min(gridDim.x, units);      // a unit each at least
+    const int u0 = begin_of(units, ctas, blockIdx.x), u1 = begin_of(units, ctas, blockIdx.x + 1);
     if (!a.finished) row = u0 / n_tiles;
     // the live row after one
     auto row_after = [&](int row) {
@@ -383,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
             ++run;
             if (!ends) continue;
             // -------------------------------------------------------- the run's end
-            const int c_first = (int)(((unsigned)(number * n_tiles + 1) * gridDim.x - 1u) / units);
-            const int c_last = (int)(((unsigned)((number + 1) * n_tiles) * gridDim.x - 1u) / units);
+            const int c_first = (int)(((unsigned)(number * n_tiles + 1) * ctas - 1u) / units);
+            const int c_last = (int)(((unsigned)((number + 1) * n_tiles) * ctas - 1u) / units);
             const int n_runs = c_last - c_first + 1;
             float top = m;
 #pragma unroll

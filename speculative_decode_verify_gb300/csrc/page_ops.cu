@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const CopyArgs 
 }
 
 static cudaError_t launch_copy(const CopyArgs& a, long long most_units, cudaStream_t stream) {
-    // eight CTAs an SM keep 16 KB of loads in flight on each
+    // eight CTAs an SM keep 64 KB of loads in flight on each
     const int sms = device_sm_count();
     const long long most = 8ll * (sms > 0 ? sms : 148);
     long long work = most_units;

@@ -104,6 +104,15 @@ def test_runs_of_many_tiles(dtype, finished):
     _check(x, -5 + rng.standard_normal(rows), beams, k, finished=fin, end=4)
 
 
+@pytest.mark.parametrize("finished", [[0, 0, 1, 0], [1, 0, 0, 0], [1, 1, 0, 1], [0, 1, 0, 1]])
+def test_fewer_tiles_than_ctas_once_rows_are_finished(finished):
+    rng = np.random.default_rng(5)
+    ws = torch.zeros(va.va_beam_workspace_bytes(2, 4, 160000, 8), dtype=torch.uint8, device="cuda")
+    for groups, vocab in ((1, 160000), (2, 40000), (1, 160000)):
+        _check(_rows(vocab + groups, 4 * groups, vocab, torch.bfloat16), -5 + rng.standard_normal(4 * groups), 4, 8,
+               finished=finished * groups, end=2, ws=ws)
+
+
 def test_more_rows_than_ctas():
     rng = np.random.default_rng(2)
     fin = (rng.random(3000) < 0.5).astype(np.int32).tolist()
