@@ -285,6 +285,47 @@ def test_another_stream():
     _check(c, got, [4, 3])
 
 
+@pytest.mark.parametrize("rows,group", [(2, 3), (4, 8)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_query_without_a_number_keeps_to_its_own_rows(rows, group, bad):
+    c = Cache(40, [900, 130], 2, "e4m3")
+    dev, live = c.dev(0), [rows, rows]
+    clean, _ = bf16(np.random.default_rng(2).standard_normal((2, rows, 2 * group, D)))
+    q = clean.clone()
+    q[0, 1, 2, 7] = bad
+    got = [_attend(c, dev, live, rows, group, qs=(t, None)) for t in (clean, q)]
+    hit = np.zeros(got[0][2].shape, bool)
+    hit[0, 1, 2] = True
+    assert np.all(np.isnan(got[1][1][hit])) and np.all(np.isnan(got[1][2][hit]))
+    for i in (1, 2):
+        np.testing.assert_array_equal(got[0][i][~hit], got[1][i][~hit])
+
+
+def test_two_calls_at_once():
+    """On two streams, with workspaces of their own and one pool, again and again."""
+    c = Cache(41, [2500, 64, 700], 2, "int8")
+    dev = c.dev(0)
+    calls = []
+    for rows, group in ((1, 6), (8, 6)):
+        q, _ = bf16(np.random.default_rng(rows).standard_normal((3, rows, 2 * group, D)))
+        calls.append([q.cuda(), ints([rows] * 3), torch.zeros(3, rows, 2 * group, D, dtype=torch.bfloat16, device="cuda"),
+                      torch.zeros(va.va_paged_workspace_bytes(3, rows, 2, group), dtype=torch.uint8, device="cuda"),
+                      torch.cuda.Stream()])
+    lens, table = ints(c.lens), ints(c.table)
+    want = []
+    for q, live, out, ws, _ in calls:
+        va.verify_attn_paged_b8(q, live, lens, table, *dev, SCALE, None, ws, out)
+        want.append(out.clone())
+        out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, live, out, ws, stream in calls:
+            va.verify_attn_paged_b8(q, live, lens, table, *dev, SCALE, None, ws, out, stream=stream)
+    torch.cuda.synchronize()
+    for (_, _, out, _, _), w in zip(calls, want):
+        assert torch.equal(out, w)
+
+
 def test_positions_and_pool_offsets_past_32_bits_of_bytes():
     """A pool of over 4 GB (page numbers whose byte offsets pass 2^32) and a history of 131,080 positions."""
     kv, fmt, n = 8, "int8", 131080
