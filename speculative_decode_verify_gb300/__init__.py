@@ -363,7 +363,7 @@ def _launch(fn: str, call, t, stream, *args) -> None:
     """Call an entry point on the stream given, or on the current one of t's device, with that device current."""
     torch = _torch or _import_torch()
     index = t.get_device()
-    if index >= 0 and index != torch.cuda.current_device():
+    if index >= 0 and index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             status = call(*args, _stream(stream))
     elif stream is None and index >= 0:

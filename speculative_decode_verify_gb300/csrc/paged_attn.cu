@@ -143,12 +143,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnPaged
 }
 
 // A pool as rows of 128 codes; boxes of one head's 64 positions, swizzled.
-static bool encode_pool(CUtensorMap* map, const void* base, int rows, int box_rows) {
+static bool encode_pool(CUtensorMap* map, const void* base, int rows) {
     tc::EncodeTiledFn fn = tc::encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)kD};
-    const cuuint32_t box[2] = {(cuuint32_t)kD, (cuuint32_t)box_rows};
+    const cuuint32_t box[2] = {(cuuint32_t)kD, (cuuint32_t)kPage};
     const cuuint32_t elem[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -192,10 +192,9 @@ va_status verify_attn_paged_b8(const va_bf16* q, int n_seqs, int n_rows, int n_k
     a.n_seqs = n_seqs; a.n_rows = n_rows; a.n_kv = n_kv_heads; a.group = group;
     a.max_pages = max_pages; a.n_pages = n_pages; a.window = window;
     a.n_ctas = sms > 0 && sms < kMaxCtas ? sms : kMaxCtas;
-    CUtensorMap mk, mv;
+    CUtensorMap mk, mv;      // (paged_attn_tc.cuh takes none)
     const int pool_rows = n_pages * n_kv_heads * kPage;      // below 2^31 (check_pool)
-    if (!va::tc::cached_map(&mk, encode_pool, k_codes, pool_rows, kPage) ||
-        !va::tc::cached_map(&mv, encode_pool, v_codes, pool_rows, kPage))
+    if (n_rows * group <= kFewPairs && !(encode_pool(&mk, k_codes, pool_rows) && encode_pool(&mv, v_codes, pool_rows)))
         return VA_CUDA_ERROR;
     st = launched((format == VA_B8_INT8 ? launch_attn_int8 : launch_attn_e4m3)(
         a, mk, mv, static_cast<const uint8_t*>(k_codes), static_cast<const uint8_t*>(v_codes), (cudaStream_t)stream));

@@ -613,7 +613,7 @@ cudaError_t launch_format(const AttnPagedArgs& a, const CUtensorMap& k, const CU
                           const uint8_t* v_codes, cudaStream_t stream) {
     const int cols = a.n_rows * a.group;
     if (cols <= 8) return launch_shape<kInt8, 1>(a, k, v, stream);
-    if (cols <= 16) return launch_shape<kInt8, 2>(a, k, v, stream);
+    if (cols <= kFewPairs) return launch_shape<kInt8, 2>(a, k, v, stream);
     if (cols <= 32) return tcg::launch<kInt8, 32>(a, k_codes, v_codes, stream);
     if (cols <= 48) return tcg::launch<kInt8, 48>(a, k_codes, v_codes, stream);
     return tcg::launch<kInt8, 64>(a, k_codes, v_codes, stream);

@@ -22,6 +22,7 @@ constexpr int kTileBytes = 2 * kHeadBytes;    // K and V codes of a tile
 constexpr uint64_t kWaitNs = 1000000000ull;   // a wait gives up after a second (VA_DEV_TIMEOUT)
 constexpr float kShift = 6.0f;                // p = 2^(t - m + kShift)
 constexpr float kLazy = 8.0f;                 // m is raised when a score passes it by this much
+constexpr int kFewPairs = 16;                 // pairs that paged_attn.cuh takes; paged_attn_tc.cuh more
 constexpr float kNoScore = -3.0e38f;          // m before the first score (any score passes it)
 
 // Workspace: partial sums of 2 segments a CTA, [2 kMaxCtas][kMaxCols][128] floats, then their (m, l).
