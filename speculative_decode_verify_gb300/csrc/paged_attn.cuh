@@ -98,6 +98,7 @@ struct Shape {
     static constexpr int kStages = kFit < 12 ? kFit : 12;
     static constexpr int kBytes = 1024 + kFixed + kStages * (kTileBytes + 32);
     static_assert(kStages >= 4, "the ring needs a few pages");
+    static_assert(sizeof(Plan) % 16 == 0, "the scales behind it are written by bulk copies");
 };
 
 template <bool kInt8, int RT>
