@@ -6,7 +6,7 @@
 // on the order in which threads run.  The plans (who gets which page) are integers: one CTA makes each, the
 // copies that it asks for run in a launch of their own over all SMs, behind a programmatic dependency.
 // Measured: kv_page_compact of 1,500 live pages of 4,096 (2 heads, 4 layers: 250 MB) 50 us, of which the copy 38 us, 6.5
-// TB/s; kv_page_reorder and kv_page_extend of 32 x 8 hypotheses (4 layers, 2 heads) 17 us, of 1 x 4 8 us.
+// TB/s; kv_page_reorder and kv_page_extend of 32 x 8 hypotheses (4 layers, 2 heads) 17 us, of 1 x 4 7 us.
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 
@@ -77,17 +77,57 @@ struct PlanSmem {
     int sums[kPlanWarps + 1];
     int counts[kScan * kPlanWarps];
     int status, pairs, found;
+    alignas(16) int page[kPlanThreads];              // of at most as many entries as threads: the shared pages, -2 = none,
+    int list[kPlanThreads];                          // and the free pages to be handed out
 };
 
-// The table entries of all pages that will be written, numbered in order of (slot, entry), a thread each: a decode
-// step's are one or two a slot, so that a pass over them is one round trip to memory.  Pages of one reference stay
+// The free pages among kScan * kPlanThreads from c0 on (r: their counts, page c0 + i * kPlanThreads + tid in r[i]), in order
+// behind the sm.found before, to the first `total` places of `list`.
+__device__ __forceinline__ void list_free(const int (&r)[kScan], int c0, int total, PlanSmem& sm, int32_t* list) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned mask[kScan];
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) mask[i] = __ballot_sync(0xffffffffu, r[i] == 0);
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kScan; ++i) sm.counts[i * kPlanWarps + warp] = __popc(mask[i]);
+    }
+    __syncthreads();
+    const int c = tid < kScan * kPlanWarps ? sm.counts[tid] : 0;
+    const int s = block_scan(c, sm.sums);
+    const int found = sm.found;
+    if (tid < kScan * kPlanWarps) sm.counts[tid] = found + s - c;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) {
+        if ((mask[i] >> lane) & 1u) {
+            const int rank = sm.counts[i * kPlanWarps + warp] + __popc(mask[i] & ((1u << lane) - 1u));
+            if (rank < total) list[rank] = c0 + i * kPlanThreads + tid;
+        }
+    }
+    if (tid == 0) sm.found = found + sm.sums[kPlanWarps];
+    __syncthreads();
+}
+
+// The table entries of all pages that will be written, numbered in order of (slot, entry).  Pages of one reference stay
 // with their entry and need nothing; only for shared ones the holders are counted and the first one found.
+//   Up to 1,024 entries (a decode step's are one or two a slot): a thread each, everything between the loads and the
+//   stores in registers and shared memory, the first 16,384 counts loaded with the lengths: three round trips to memory.
+//   More (prompts): in passes over the entries, with the holders and the free list in the workspace.
+// kv_page_reorder and kv_page_extend of 1 x 4 and 32 x 8 hypotheses took 13.4 and 22.0 us with the passes alone (three
+// copies of the state among them), 11.9 and 21.7 us so.
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendArgs a) {
     __shared__ PlanSmem sm;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     if (tid == 0) sm.status = sm.pairs = sm.found = 0;
+    int counts[kScan];
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) {
+        const int p = i * kPlanThreads + tid;
+        counts[i] = p < a.n_pages ? a.refs[p] : 1;
+    }
     int status = 0, len = 0, add = 0, mine = 0;
     if (tid < a.n_seqs) {
         len = a.lens[tid];
@@ -114,6 +154,68 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendA
     };
     auto in_slot = [&](int i, int b) { return i - (b > 0 ? sm.upto[b - 1] : 0); };
     auto place = [&](int i, int b) { return b * a.max_pages + sm.x0[b] + in_slot(i, b); };
+    auto refuse = [&](int why) {
+        if (tid == 0) {
+            *a.w.n_pairs = 0;
+            if (a.dev_status) atomicOr(a.dev_status, why);
+        }
+    };
+    if (entries <= kPlanThreads) {
+        int b = 0, at = 0, p = -1, n_refs = 0;
+        if (tid < entries) {
+            b = slot_of(tid);
+            at = place(tid, b);
+            p = a.table[at];
+            n_refs = p >= 0 && p < a.n_pages ? a.refs[p] : 0;
+            if (p < -1 || p >= a.n_pages || (p >= 0 && n_refs < 1)) status |= VA_DEV_BAD_PAGE;
+        }
+        sm.page[tid] = n_refs > 1 ? p : -2;
+        if (status) atomicOr(&sm.status, status);
+        const bool some = __syncthreads_or(n_refs > 1);
+        if (sm.status) return refuse(sm.status);
+        // a shared page stays with its first holder here if no entry outside this call's names it
+        bool fresh = tid < entries && p < 0;
+        if (some && n_refs > 1) {
+            int holders = 0, first = tid;
+#pragma unroll 4
+            for (int j = 0; j < entries; j += 4) {       // (-2 behind the entries)
+                const int4 q = *reinterpret_cast<const int4*>(sm.page + j);
+                const int here = (q.x == p) + (q.y == p) + (q.z == p) + (q.w == p);
+                if (here && j < first) first = min(first, q.x == p ? j : q.y == p ? j + 1 : q.z == p ? j + 2 : j + 3);
+                holders += here;
+            }
+            fresh = holders != n_refs || first != tid;
+        }
+        const int rank = block_scan(fresh ? 1 : 0, sm.sums) - 1, total = sm.sums[kPlanWarps];
+        __syncthreads();
+        if (total > 0) list_free(counts, 0, total, sm, sm.list);
+        for (int c0 = kScan * kPlanThreads; c0 < a.n_pages && sm.found < total; c0 += kScan * kPlanThreads) {
+#pragma unroll
+            for (int i = 0; i < kScan; ++i) {
+                const int q = c0 + i * kPlanThreads + tid;
+                counts[i] = q < a.n_pages ? a.refs[q] : 1;
+            }
+            list_free(counts, c0, total, sm, sm.list);
+        }
+        if (sm.found < total) return refuse(VA_DEV_NO_PAGES);
+        if (fresh) {
+            const int page = sm.list[rank];
+            a.table[at] = page;
+            a.refs[page] = 1;
+            if (p >= 0) {
+                atomicSub(a.refs + p, 1);
+                if (in_slot(tid, b) == 0 && a.lens[b] % kPage != 0) {      // only a slot's first entry can hold positions
+                    const int j = atomicAdd(&sm.pairs, 1);
+                    a.w.src[j] = p;
+                    a.w.dst[j] = page;
+                }
+            }
+        }
+        __syncthreads();
+        if (tid < a.n_seqs && add > 0) a.lens[tid] = len + add;
+        if (tid == 0) *a.w.n_pairs = sm.pairs;
+        return;
+    }
     bool shared = false;
     for (int i = tid; i < entries; i += kPlanThreads) {
         const int p = a.table[place(i, slot_of(i))];
@@ -128,13 +230,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendA
     }
     if (status) atomicOr(&sm.status, status);
     const bool some_shared = __syncthreads_or(shared);
-    if (sm.status) {
-        if (tid == 0) {
-            *a.w.n_pairs = 0;
-            if (a.dev_status) atomicOr(a.dev_status, sm.status);
-        }
-        return;
-    }
+    if (sm.status) return refuse(sm.status);
     if (some_shared) {
         for (int i = tid; i < entries; i += kPlanThreads) {
             const int p = a.table[place(i, slot_of(i))];
@@ -160,41 +256,16 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendA
         total += __syncthreads_count(i < entries && gets_new(i, a.table[place(i, slot_of(i))]));
     }
     // the `total` lowest-numbered free pages, in order
-    for (int c0 = 0; c0 < a.n_pages && sm.found < total; c0 += kScan * kPlanThreads) {
-        unsigned mask[kScan];
+    if (total > 0) list_free(counts, 0, total, sm, a.w.list);
+    for (int c0 = kScan * kPlanThreads; c0 < a.n_pages && sm.found < total; c0 += kScan * kPlanThreads) {
 #pragma unroll
         for (int i = 0; i < kScan; ++i) {
             const int p = c0 + i * kPlanThreads + tid;
-            const int r = p < a.n_pages ? a.refs[p] : 1;
-            mask[i] = __ballot_sync(0xffffffffu, r == 0);
+            counts[i] = p < a.n_pages ? a.refs[p] : 1;
         }
-        if (lane == 0) {
-#pragma unroll
-            for (int i = 0; i < kScan; ++i) sm.counts[i * kPlanWarps + warp] = __popc(mask[i]);
-        }
-        __syncthreads();
-        const int c = tid < kScan * kPlanWarps ? sm.counts[tid] : 0;
-        const int s = block_scan(c, sm.sums);
-        const int found = sm.found;
-        if (tid < kScan * kPlanWarps) sm.counts[tid] = found + s - c;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kScan; ++i) {
-            if ((mask[i] >> lane) & 1u) {
-                const int rank = sm.counts[i * kPlanWarps + warp] + __popc(mask[i] & ((1u << lane) - 1u));
-                if (rank < total) a.w.list[rank] = c0 + i * kPlanThreads + tid;
-            }
-        }
-        if (tid == 0) sm.found = found + sm.sums[kPlanWarps];
-        __syncthreads();
+        list_free(counts, c0, total, sm, a.w.list);
     }
-    if (sm.found < total) {
-        if (tid == 0) {
-            *a.w.n_pairs = 0;
-            if (a.dev_status) atomicOr(a.dev_status, VA_DEV_NO_PAGES);
-        }
-        return;
-    }
+    if (sm.found < total) return refuse(VA_DEV_NO_PAGES);
     // Hand them out; the list keeps the shared page that each replaces, whose count changes once all have chosen.
     int rank0 = 0;
     for (int i0 = 0; i0 < entries; i0 += kPlanThreads) {

@@ -102,6 +102,33 @@ def test_too_few_pages_changes_nothing():
     s.check()
 
 
+@pytest.mark.parametrize("slots,new,free", [(4, 150, [5, 16383, 16384, 16385, 20000, 32767, 32768, 39990, 39991, 39998, 39999, 12]),
+                                            (3, 25000, list(range(100, 36000, 30))),
+                                            (1024, 64, [0] + list(range(20000, 22000)))])
+def test_free_pages_far_into_a_large_pool(slots, new, free):
+    pages, width = 40000, 400
+    refs = np.ones(pages, np.int32)
+    refs[free] = 0
+    table = np.full((slots, width), -1, np.int32)
+    codes = torch.zeros(pages, 1, 64, D, dtype=torch.uint8, device="cuda")
+    scale = torch.zeros(pages, 1, 4, device="cuda")
+    t, r, n, status = ints(table.tolist()), ints(refs.tolist()), ints([0] * slots), ints([0])
+    ws = torch.empty(va.va_page_ops_workspace_bytes(slots, width, pages), dtype=torch.uint8, device="cuda")
+    va.kv_page_extend(t, n, ints([new] * slots), r, codes, codes, scale, scale, ws, dev_status=status)
+    table, refs, lens = table.tolist(), refs.tolist(), [0] * slots
+    assert P.extend(table, lens, refs, [new] * slots) == [] and int(status.item()) == 0
+    assert t.tolist() == table and r.tolist() == refs and n.tolist() == lens
+
+
+def test_every_slot_shares_one_page():
+    s = Pool(12, [[7, -1]] * 900, [3] * 900, 1000)
+    s.extend([1] * 900)
+    s.check()
+    s = Pool(13, [[7, -1]] * 900, [3] * 900, 1000)
+    s.extend([0, 0] + [1] * 898)
+    s.check()
+
+
 @pytest.mark.parametrize("change,bit", [("negative", 1024), ("long", 4), ("page", 128), ("free", 128), ("length", 1024)])
 def test_extend_refuses_and_changes_nothing(change, bit):
     s = Pool(9, [[0, 1], [2, -1]], [70, 20], 6)
