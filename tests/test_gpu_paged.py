@@ -209,6 +209,18 @@ def test_scales_that_differ_by_orders_of_magnitude(fmt):
     _check(c, _attend(c, c.dev(0), [2, 2], 2, 6), [2, 2])
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,group", [(4, 7), (8, 6), (8, 8)])
+def test_scales_that_differ_by_orders_of_magnitude_with_many_pairs(fmt, rows, group):
+    c = Cache(43, [1300, 400], 1, fmt)
+    rng = np.random.default_rng(3)
+    for w, low, high in (("k", -3, 0), ("v", -12, 12)):
+        f = np.sort(10.0 ** rng.uniform(low, high, c.scale[w].shape), axis=1 if w == "k" else 3)
+        c.scale[w] = (c.scale[w] * f).astype(np.float32)
+    c.scale["v"][:, c.table[0][2]] = 0.0
+    _check(c, _attend(c, c.dev(0), [rows, rows], rows, group), [rows, rows])
+
+
 def test_pages_that_are_none_are_masked_and_told():
     c = Cache(35, [300, 200, 64], 1, "e4m3")
     for bad in (-1, c.pages, 2 ** 31 - 1, -7):
@@ -218,6 +230,19 @@ def test_pages_that_are_none_are_masked_and_told():
         for sink in (None, [0.5, 1.5]):
             _check(c, _attend(c, c.dev(0), [2, 1, 2], 2, 2, table=table, sink=sink), [2, 1, 2], table=table, sink=sink,
                    status=128)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,group,window", [(8, 3, 0), (8, 6, 0), (8, 8, 0), (5, 5, 200), (7, 8, 65)])
+def test_many_pairs_with_pages_that_are_none_windows_and_empty_sequences(fmt, rows, group, window):
+    c = Cache(42, [700, 0, 129, 64, 1500, 3], 2, fmt)
+    live = [rows, 0, 1, rows, 2, 3]
+    table = [list(r) for r in c.table]
+    table[0][9] = table[4][22] = -1
+    table[2][2] = c.pages
+    table[4][20] = table[4][21]
+    _check(c, _attend(c, c.dev(0), live, rows, group, window=window, table=table, spread=2.0), live, window=window, table=table,
+           status=128)
 
 
 def test_wrong_counts_make_an_empty_sequence():
