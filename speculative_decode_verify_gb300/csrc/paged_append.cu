@@ -87,9 +87,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 8) append_kernel(const Appe
     const Seq sq = load_seq(a.lens, a.n_live, (int)b, a.n_rows, a.max_pages);
     const int start = sq.len - sq.live;
     const int block = start / kBlock + i;
-    const int p0 = block * kBlock;
     int status = sq.status;
-    if (sq.live > 0 && p0 < sq.len) {
+    // (blocks are compared, not positions: a block behind the last may begin past 2^31)
+    if (sq.live > 0 && block <= (sq.len - 1) / kBlock) {
+        const int p0 = block * kBlock;
         // the rows on their way before the page is known
         const uint16_t* src = (is_v ? a.v_new : a.k_new) + ((size_t)b * a.n_rows * a.n_kv + h) * kD + 8 * li;
         uint4 raw[8];

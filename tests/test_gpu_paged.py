@@ -125,6 +125,29 @@ def test_append_leaves_a_wrong_sequence_alone(bad, bit):
             assert any(not np.array_equal(a[p].view(np.uint8), b[p].view(np.uint8)) for p in c.table[0] if p >= 0)
 
 
+@pytest.mark.parametrize("live", [1, 5, 40])
+def test_append_to_the_last_positions_that_a_table_can_hold(live):
+    """A table of 2^25 - 1 pages, full: blocks behind the last would begin past 2^31, and their table entries lie in the
+    next sequence's row, which has no page there."""
+    width, rows, fmt = 2 ** 25 - 1, 100, "int8"
+    lens = [64 * width, 5]
+    table = torch.full((2, width), -1, dtype=torch.int32, device="cuda")
+    table[0, width - 1], table[1, 0] = 3, 1
+    rng = np.random.default_rng(28)
+    codes = [rng.integers(-127, 128, (4, 2, 64, D)).astype(np.int8).view(np.uint8) for _ in "kv"]
+    scale = [rng.random((4, 2, 4)).astype(np.float32) for _ in "kv"]
+    dev = [torch.as_tensor(c.copy()).view(torch.int8).cuda() for c in codes] + [torch.as_tensor(s.copy()).cuda() for s in scale]
+    new = [bf16(rng.standard_normal((2, rows, 2, D))) for _ in "kv"]
+    status = ints([0])
+    va.kv_page_append_b8(new[0][0].cuda(), new[1][0].cuda(), ints([live, 2]), ints(lens), table, *dev, dev_status=status)
+    assert int(status.item()) == 0
+    for i in range(2):
+        for b, (n, page) in enumerate(((live, {width - 1: 3}), (2, {0: 1}))):
+            P.append(new[i][1][b].astype(np.float32), lens[b] - n, lens[b], page, codes[i], scale[i], fmt)
+        _same_codes(dev[i].view(torch.uint8).cpu().numpy(), codes[i], fmt)
+        np.testing.assert_array_equal(dev[2 + i].cpu().numpy(), scale[i])
+
+
 # ------------------------------------------------------------------------------------------------ attention
 def _attend(c, dev, live, rows, group, window=0, sink=None, scale=SCALE, seed=9, spread=1.0, table=None, lens=None,
             ws=None, qs=None):
