@@ -332,41 +332,47 @@ def _need(ok: bool, what: str) -> None:
 
 
 _torch = None
+_KINDS = {}      # what the tensors of a call may hold
 
 
 def _import_torch():
     global _torch
     if _torch is None:
         import torch
+        _KINDS.update({"int32": (torch.int32,), "float32": (torch.float32,),
+                       "bfloat16": (torch.bfloat16, torch.int16, torch.uint16),      # or their bit patterns
+                       "8-bit codes": (torch.int8, torch.uint8, torch.float8_e4m3fn)})
         _torch = torch
     return _torch
 
 
-def _at(t, count: int, size: int, what: str) -> int:
-    """Address of a dense tensor of `count` elements of `size` bytes (the C ABI takes no strides)."""
-    if t.nbytes != count * size or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous tensor of {count} elements of {size} bytes")
+def _at(t, count: int, kind: str, index: int, what: str) -> int:
+    """Address of a dense tensor of `count` elements on GPU `index` (the C ABI takes no strides)."""
+    if t.dtype not in _KINDS[kind] or t.numel() != count or not t.is_contiguous() or t.get_device() != index:
+        where = f"on cuda:{index}" if index >= 0 else "on a GPU"
+        raise ValueError(f"{what}: a contiguous tensor of {count} elements, {kind}, {where}")
     return t.data_ptr()
 
 
-def _bytes(t):
-    if not t.is_contiguous():
-        raise ValueError("the workspace: a contiguous tensor")
+def _bytes(t, index: int):
+    if not t.is_contiguous() or t.get_device() != index:
+        raise ValueError("the workspace: a contiguous tensor on the other tensors' GPU")
     return t.data_ptr(), t.numel() * t.itemsize
 
 
-def _opt(t, count: int, size: int, what: str):
-    return None if t is None else _at(t, count, size, what)
+def _opt(t, count: int, kind: str, index: int, what: str):
+    return None if t is None else _at(t, count, kind, index, what)
 
 
-def _launch(fn: str, call, t, stream, *args) -> None:
-    """Call an entry point on the stream given, or on the current one of t's device, with that device current."""
-    torch = _torch or _import_torch()
-    index = t.get_device()
-    if index >= 0 and index != torch._C._cuda_getDevice():
+def _launch(fn: str, call, index: int, stream, *args) -> None:
+    """Call an entry point on the stream given, or on the current one of GPU `index`, with that device current."""
+    if index < 0:
+        raise ValueError(f"{fn}: the tensors have to be on a GPU")
+    torch = _torch
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             status = call(*args, _stream(stream))
-    elif stream is None and index >= 0:
+    elif stream is None:
         status = call(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         status = call(*args, _stream(stream))
@@ -375,39 +381,41 @@ def _launch(fn: str, call, t, stream, *args) -> None:
 
 
 def _pool(k_codes, v_codes, k_scale, v_scale):
-    """(layers, pages, kv heads, format, four addresses) of pools [pages, heads, 64, 128] or [layers, pages, ...]."""
+    """(layers, pages, kv heads, format, GPU, four addresses) of pools [pages, heads, 64, 128] or [layers, pages, ...]."""
     torch = _torch or _import_torch()
-    shape, kind = k_codes.shape, k_codes.dtype
-    n = k_codes.nbytes
+    shape, kind, index = k_codes.shape, k_codes.dtype, k_codes.get_device()
+    n = k_codes.numel()
     if not (4 <= len(shape) <= 5 and shape[-1] == HEAD_DIM and shape[-2] == TILE and v_codes.dtype is kind
             and v_codes.shape == shape and k_scale.shape[-1] == TILE // B8_BLOCK):
         raise ValueError("pools are codes [..., pages, heads, 64, 128] of one 8-bit type and scales [..., pages, heads, 4]")
     scales = n // (HEAD_DIM * B8_BLOCK)
-    return (shape[0] if len(shape) == 5 else 1, shape[-4], shape[-3], B8_INT8 if kind is torch.int8 else B8_E4M3,
-            _at(k_codes, n, 1, "codes"), _at(v_codes, n, 1, "codes"), _at(k_scale, scales, 4, "scales"),
-            _at(v_scale, scales, 4, "scales"))
+    return (shape[0] if len(shape) == 5 else 1, shape[-4], shape[-3], B8_INT8 if kind is torch.int8 else B8_E4M3, index,
+            _at(k_codes, n, "8-bit codes", index, "k_codes (int8, float8_e4m3fn or its bits in uint8)"),
+            _at(v_codes, n, "8-bit codes", index, "v_codes"), _at(k_scale, scales, "float32", index, "k_scale"),
+            _at(v_scale, scales, "float32", index, "v_scale"))
 
 
-def _table(table, n: int):
+def _table(table, n: int, index: int):
     if table.dim() != 2 or table.shape[0] != n:
         raise ValueError("the table is int32 [n_seqs, max_pages]")
     width = table.shape[1]
-    return width, _at(table, n * width, 4, "the table")
+    return width, _at(table, n * width, "int32", index, "the table")
 
 
 def kv_page_append_b8(k_new, v_new, n_live, lens, table, k_codes, v_codes, k_scale, v_scale, dev_status=None,
                       stream=None, variant: str = "") -> None:
     """Code the live rows' K/V ([n_seqs, n_rows, n_kv_heads, 128] bf16) into the sequences' pages.  The pool's
     format goes by its dtype: int8, or E4M3 (float8_e4m3fn or uint8)."""
-    layers, pages, heads, fmt, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
+    layers, pages, heads, fmt, dev, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
     n, rows, h, d = k_new.shape
     _need(layers == 1 and h == heads and d == HEAD_DIM and v_new.shape == k_new.shape,
           "new rows are [n_seqs, n_rows, n_kv_heads, 128], the pool one layer's")
-    width, tb = _table(table, n)
+    width, tb = _table(table, n, dev)
     count = n * rows * heads * HEAD_DIM
-    _launch("kv_page_append_b8", lib(variant).kv_page_append_b8, k_codes, stream, _at(k_new, count, 2, "k_new"),
-            _at(v_new, count, 2, "v_new"), n, rows, heads, _at(n_live, n, 4, "n_live"), _at(lens, n, 4, "lens"), tb, width,
-            kc, vc, ks, vs, pages, fmt, _opt(dev_status, 1, 4, "dev_status"))
+    _launch("kv_page_append_b8", lib(variant).kv_page_append_b8, dev, stream, _at(k_new, count, "bfloat16", dev, "k_new"),
+            _at(v_new, count, "bfloat16", dev, "v_new"), n, rows, heads, _at(n_live, n, "int32", dev, "n_live"),
+            _at(lens, n, "int32", dev, "lens"), tb, width, kc, vc, ks, vs, pages, fmt,
+            _opt(dev_status, 1, "int32", dev, "dev_status"))
 
 
 def va_paged_workspace_bytes(n_seqs: int, n_rows: int, n_kv_heads: int, group: int) -> int:
@@ -419,17 +427,18 @@ def verify_attn_paged_b8(q, n_live, lens, table, k_codes, v_codes, k_scale, v_sc
     """Verify attention of every sequence's live rows (q [n_seqs, n_rows, heads, 128] bf16) over its pages; writes
     out (as q) and out_lse [n_seqs, n_rows, heads].  ``workspace``: a device byte tensor of
     va_paged_workspace_bytes(...) bytes."""
-    layers, pages, kv, fmt, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
+    layers, pages, kv, fmt, dev, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
     n, rows, heads, d = q.shape
     _need(layers == 1 and d == HEAD_DIM and heads % kv == 0 and out.shape == q.shape,
           "q and out are [n_seqs, n_rows, n_kv_heads * group, 128], the pool one layer's")
-    width, tb = _table(table, n)
+    width, tb = _table(table, n, dev)
     pairs = n * rows * heads
-    ws, size = _bytes(workspace)
-    _launch("verify_attn_paged_b8", lib(variant).verify_attn_paged_b8, k_codes, stream, _at(q, pairs * HEAD_DIM, 2, "q"), n,
-            rows, kv, heads // kv, _at(n_live, n, 4, "n_live"), _at(lens, n, 4, "lens"), tb, width, kc, vc, ks, vs, pages,
-            fmt, int(window), float(scale), _opt(sink, heads, 4, "sink"), ws, size, _at(out, pairs * HEAD_DIM, 2, "out"),
-            _opt(out_lse, pairs, 4, "out_lse"), _opt(dev_status, 1, 4, "dev_status"))
+    ws, size = _bytes(workspace, dev)
+    _launch("verify_attn_paged_b8", lib(variant).verify_attn_paged_b8, dev, stream,
+            _at(q, pairs * HEAD_DIM, "bfloat16", dev, "q"), n, rows, kv, heads // kv, _at(n_live, n, "int32", dev, "n_live"),
+            _at(lens, n, "int32", dev, "lens"), tb, width, kc, vc, ks, vs, pages, fmt, int(window), float(scale),
+            _opt(sink, heads, "float32", dev, "sink"), ws, size, _at(out, pairs * HEAD_DIM, "bfloat16", dev, "out"),
+            _opt(out_lse, pairs, "float32", dev, "out_lse"), _opt(dev_status, 1, "int32", dev, "dev_status"))
 
 
 def va_page_ops_workspace_bytes(n_seqs: int, max_pages: int, n_pages: int) -> int:
@@ -440,41 +449,44 @@ def kv_page_extend(table, lens, n_new, refs, k_codes, v_codes, k_scale, v_scale,
                    variant: str = "") -> None:
     """Pages for n_new[b] more tokens of every sequence (copy on write); lens grows by n_new.  Pools of all layers:
     [layers, pages, heads, 64, 128]."""
-    layers, pages, heads, _, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
+    layers, pages, heads, _, dev, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
     n = table.shape[0]
-    width, tb = _table(table, n)
-    ws, size = _bytes(workspace)
-    _launch("kv_page_extend", lib(variant).kv_page_extend, k_codes, stream, tb, _at(lens, n, 4, "lens"),
-            _at(n_new, n, 4, "n_new"), n, width, _at(refs, pages, 4, "refs"), pages, layers, heads, kc, vc, ks, vs, ws, size,
-            _opt(dev_status, 1, 4, "dev_status"))
+    width, tb = _table(table, n, dev)
+    ws, size = _bytes(workspace, dev)
+    _launch("kv_page_extend", lib(variant).kv_page_extend, dev, stream, tb, _at(lens, n, "int32", dev, "lens"),
+            _at(n_new, n, "int32", dev, "n_new"), n, width, _at(refs, pages, "int32", dev, "refs"), pages, layers, heads,
+            kc, vc, ks, vs, ws, size, _opt(dev_status, 1, "int32", dev, "dev_status"))
 
 
 def kv_page_reorder(table, lens, src, refs, group: int = 0, dev_status=None, stream=None, variant: str = "") -> None:
     """Slot j takes the sequence of slot src[j] of its group (j: kept, another: forked, -1: freed)."""
-    n, pages = table.shape[0], refs.numel()
-    width, tb = _table(table, n)
-    _launch("kv_page_reorder", lib(variant).kv_page_reorder, table, stream, tb, _at(lens, n, 4, "lens"), n, width,
-            _at(src, n, 4, "src"), int(group), _at(refs, pages, 4, "refs"), pages, _opt(dev_status, 1, 4, "dev_status"))
+    _torch or _import_torch()
+    n, pages, dev = table.shape[0], refs.numel(), table.get_device()
+    width, tb = _table(table, n, dev)
+    _launch("kv_page_reorder", lib(variant).kv_page_reorder, dev, stream, tb, _at(lens, n, "int32", dev, "lens"), n, width,
+            _at(src, n, "int32", dev, "src"), int(group), _at(refs, pages, "int32", dev, "refs"), pages,
+            _opt(dev_status, 1, "int32", dev, "dev_status"))
 
 
 def kv_page_copy(src, dst, k_codes, v_codes, k_scale, v_scale, dev_status=None, stream=None, variant: str = "") -> None:
     """Page dst[i] becomes a copy of page src[i], in all layers."""
-    layers, pages, heads, _, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
+    layers, pages, heads, _, dev, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
     n = src.numel()
-    _launch("kv_page_copy", lib(variant).kv_page_copy, k_codes, stream, _at(src, n, 4, "src"), _at(dst, n, 4, "dst"), n,
-            pages, layers, heads, kc, vc, ks, vs, _opt(dev_status, 1, 4, "dev_status"))
+    _launch("kv_page_copy", lib(variant).kv_page_copy, dev, stream, _at(src, n, "int32", dev, "src"),
+            _at(dst, n, "int32", dev, "dst"), n, pages, layers, heads, kc, vc, ks, vs,
+            _opt(dev_status, 1, "int32", dev, "dev_status"))
 
 
 def kv_page_compact(table, refs, k_codes, v_codes, k_scale, v_scale, moved_to, n_live_pages, workspace, dev_status=None,
                     stream=None, variant: str = "") -> None:
     """Move the live pages to the lowest numbers; moved_to [pages] tells where, n_live_pages [1] how many there are."""
-    layers, pages, heads, _, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
+    layers, pages, heads, _, dev, kc, vc, ks, vs = _pool(k_codes, v_codes, k_scale, v_scale)
     n = table.shape[0]
-    width, tb = _table(table, n)
-    ws, size = _bytes(workspace)
-    _launch("kv_page_compact", lib(variant).kv_page_compact, k_codes, stream, tb, n, width, _at(refs, pages, 4, "refs"),
-            pages, layers, heads, kc, vc, ks, vs, _at(moved_to, pages, 4, "moved_to"), _at(n_live_pages, 1, 4, "n_live_pages"),
-            ws, size, _opt(dev_status, 1, 4, "dev_status"))
+    width, tb = _table(table, n, dev)
+    ws, size = _bytes(workspace, dev)
+    _launch("kv_page_compact", lib(variant).kv_page_compact, dev, stream, tb, n, width, _at(refs, pages, "int32", dev, "refs"),
+            pages, layers, heads, kc, vc, ks, vs, _at(moved_to, pages, "int32", dev, "moved_to"),
+            _at(n_live_pages, 1, "int32", dev, "n_live_pages"), ws, size, _opt(dev_status, 1, "int32", dev, "dev_status"))
 
 
 # ----------------------------------------------------------------------------- beam search
@@ -491,14 +503,15 @@ def va_beam_select(logits, scores, n_beams: int, parents, tokens, out_scores, wo
     rows, vocab = logits.shape
     groups, n_out = parents.shape
     stride, inner = logits.stride()
-    bf16 = logits.dtype is torch.bfloat16
+    bf16, dev = logits.dtype is torch.bfloat16, logits.get_device()
     _need(groups * n_beams == rows and (vocab == 1 or inner == 1) and (bf16 or logits.dtype is torch.float32),
           "logits are float32 or bfloat16 [n_groups * n_beams, vocab]")
     count = groups * n_out
-    ws, size = _bytes(workspace)
-    _launch("va_beam_select", lib(variant).va_beam_select, logits, stream, logits.data_ptr(), 1 if bf16 else 0, stride, groups,
-            int(n_beams), vocab, _at(scores, rows, 4, "scores"), _opt(finished, rows, 4, "finished"), int(end_token), n_out,
-            _at(parents, count, 4, "parents"), _at(tokens, count, 4, "tokens"), _at(out_scores, count, 4, "out_scores"), ws, size)
+    ws, size = _bytes(workspace, dev)
+    _launch("va_beam_select", lib(variant).va_beam_select, dev, stream, logits.data_ptr(), 1 if bf16 else 0, stride, groups,
+            int(n_beams), vocab, _at(scores, rows, "float32", dev, "scores"), _opt(finished, rows, "int32", dev, "finished"),
+            int(end_token), n_out, _at(parents, count, "int32", dev, "parents"), _at(tokens, count, "int32", dev, "tokens"),
+            _at(out_scores, count, "float32", dev, "out_scores"), ws, size)
 
 
 # ----------------------------------------------------------------------------- self-test

@@ -6,6 +6,7 @@ import torch
 import oracle.paged as P
 import speculative_decode_verify_gb300 as va
 from paged_cases import Cache, attention_bounds, bf16, ints
+from test_paged_host import _calls
 
 pytestmark = pytest.mark.gpu
 D = 128
@@ -146,6 +147,16 @@ def test_append_to_the_last_positions_that_a_table_can_hold(live):
             P.append(new[i][1][b].astype(np.float32), lens[b] - n, lens[b], page, codes[i], scale[i], fmt)
         _same_codes(dev[i].view(torch.uint8).cpu().numpy(), codes[i], fmt)
         np.testing.assert_array_equal(dev[2 + i].cpu().numpy(), scale[i])
+
+
+@pytest.mark.parametrize("name", sorted(_calls()))
+def test_the_binding_refuses_a_host_tensor_among_the_others(name):
+    call, args = _calls()[name]
+    for key, t in args.items():
+        if torch.is_tensor(t):
+            mixed = {k: x.cuda() if torch.is_tensor(x) and k != key else x for k, x in args.items()}
+            with pytest.raises(ValueError):
+                call(**mixed)
 
 
 # ------------------------------------------------------------------------------------------------ attention

@@ -170,6 +170,69 @@ def test_the_binding_refuses_shapes_that_do_not_fit():
             call()
 
 
+def _calls():
+    """Every call with CPU tensors of the right shapes and types, by name: (function, arguments)."""
+    f32, i32, b16 = torch.float32, torch.int32, torch.bfloat16
+    codes, scale = torch.zeros(5, 2, 64, 128, dtype=torch.uint8), torch.zeros(5, 2, 4)
+    pool = dict(k_codes=codes, v_codes=codes.clone(), k_scale=scale, v_scale=scale.clone())
+    table, n, refs, one = (torch.zeros(s, dtype=i32) for s in ((3, 4), (3,), (5,), (1,)))
+    new, q = torch.zeros(3, 2, 2, 128, dtype=b16), torch.zeros(3, 2, 4, 128, dtype=b16)
+    ws, pick = torch.zeros(1 << 24, dtype=torch.uint8), torch.zeros(2, 3, dtype=i32)
+    return {
+        "append": (va.kv_page_append_b8, dict(k_new=new, v_new=new, n_live=n, lens=n, table=table, dev_status=one, **pool)),
+        "attention": (va.verify_attn_paged_b8, dict(q=q, n_live=n, lens=n, table=table, scale=0.1, sink=torch.zeros(4),
+                                                    workspace=ws, out=q, out_lse=torch.zeros(3, 2, 4), dev_status=one, **pool)),
+        "extend": (va.kv_page_extend, dict(table=table, lens=n, n_new=n, refs=refs, workspace=ws, dev_status=one, **pool)),
+        "reorder": (va.kv_page_reorder, dict(table=table, lens=n, src=n, refs=refs, dev_status=one)),
+        "copy": (va.kv_page_copy, dict(src=n, dst=n, dev_status=one, **pool)),
+        "compact": (va.kv_page_compact, dict(table=table, refs=refs, moved_to=refs, n_live_pages=one, workspace=ws,
+                                             dev_status=one, **pool)),
+        "beam": (va.va_beam_select, dict(logits=torch.zeros(8, 16), scores=torch.zeros(8), n_beams=4, parents=pick,
+                                         tokens=pick, out_scores=torch.zeros(2, 3), workspace=ws,
+                                         finished=torch.zeros(8, dtype=i32))),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(_calls()))
+def test_the_binding_refuses_tensors_that_are_on_no_gpu(name):
+    call, args = _calls()[name]
+    with pytest.raises(ValueError, match="have to be on a GPU"):
+        call(**args)
+
+
+@pytest.mark.parametrize("name", sorted(_calls()))
+def test_the_binding_refuses_every_tensor_of_another_type(name):
+    """Types of the same size among them: they would be read as what they are not."""
+    call, args = _calls()[name]
+    others = {torch.int32: [torch.float32, torch.uint32, torch.int64], torch.float32: [torch.int32, torch.float64, torch.bfloat16],
+              torch.bfloat16: [torch.float16, torch.float32], torch.uint8: [torch.float8_e5m2, torch.bool, torch.float16]}
+    tried = 0
+    for key, t in args.items():
+        if not torch.is_tensor(t) or key == "workspace":
+            continue
+        for kind in others[t.dtype]:
+            if key == "logits" and kind is torch.bfloat16:
+                continue
+            wrong = dict(args, **{key: torch.zeros(t.shape).to(kind)})
+            if key == "k_codes":
+                wrong["v_codes"] = wrong[key]
+            with pytest.raises(ValueError) as e:
+                call(**wrong)
+            assert "have to be on a GPU" not in str(e.value), (key, kind)
+            tried += 1
+    assert tried > 6
+
+
+def test_the_binding_takes_bfloat16_bits_and_each_8_bit_code_type():
+    """(as far as the check that comes last: these tensors are on no GPU)"""
+    call, args = _calls()["append"]
+    bits = args["k_new"].view(torch.int16)
+    for kind in (torch.int8, torch.uint8, torch.float8_e4m3fn):
+        codes = args["k_codes"].view(kind)
+        with pytest.raises(ValueError, match="have to be on a GPU"):
+            call(**dict(args, k_new=bits, v_new=bits, k_codes=codes, v_codes=codes))
+
+
 def test_binding_constants_match_the_headers():
     import test_abi_host
     d = test_abi_host._defines()
