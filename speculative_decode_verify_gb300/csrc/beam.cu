@@ -268,18 +268,19 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                 return __uint_as_float(kBf16 ? ((e & 1) ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16) : w[e]);
             };
             auto place_of = [&](int e) { return first + ((e / kVec) * kThreads + tid) * kVec + e % kVec; };
-            // sums, as 2^(l log2 e + off); a maximum for which off has no digits takes the careful way
+            // sums of 2^((l - m) log2 e): subtracted first, because one rounding of m log2 e would stay in the whole sum
+            // (4e-5 for a largest logit of 720), and in the row's scores with it.  +inf: its logits share the probability.
             if (mine > -INFINITY) {
-                const float up = fmaxf(m, mine), off = -up * l2e;
+                const float up = fmaxf(m, mine);
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
+                if (up < INFINITY) {
 #pragma unroll
-                for (int e = 0; e < kPerThread; ++e) part[e & 3] += ptx::ex2(fmaf(f(e), l2e, off));
-                float add = (part[0] + part[1]) + (part[2] + part[3]);
-                if (!(fabsf(up) < 1024.0f)) {
-                    add = 0.0f;
+                    for (int e = 0; e < kPerThread; ++e) part[e & 3] += ptx::ex2((f(e) - up) * l2e);
+                } else {
 #pragma unroll
-                    for (int e = 0; e < kPerThread; ++e) add += f(e) == up ? 1.0f : ptx::ex2((f(e) - up) * l2e);
+                    for (int e = 0; e < kPerThread; ++e) part[e & 3] += f(e) == up ? 1.0f : 0.0f;
                 }
+                const float add = (part[0] + part[1]) + (part[2] + part[3]);
                 sum = (m == up ? sum : (m == -INFINITY ? 0.0f : sum * ptx::ex2((m - up) * l2e))) + add;
                 m = up;
             }

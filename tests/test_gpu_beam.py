@@ -75,6 +75,27 @@ def test_masked_infinite_and_nan_logits():
     _check(x, [-1.0, -2.0, -1.5, -40.0, -0.25, -30.0], 6, 20)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", ["one", "constant", "peaked"])
+@pytest.mark.parametrize("top", [-720, 24, 96, 360, 720, 1016, 2032])
+def test_a_rows_offset_does_not_move_its_scores(dtype, shape, top):
+    """Two hypotheses of the same distribution, one with logits near 0 and one far from it; their scores are 1e-5 apart.
+    The largest terms of a sum are 2^0 (exact) and the others e^-8 and less, so a sum is right to 2^-22 (the
+    exponential's accuracy) times 2^-11, and the constant row's is a whole number; the log's 64 bits and the one rounding
+    of the score (2^-24) add to that.  2^-21 holds them all."""
+    vocab = 20000
+    x = torch.full((4, vocab + 96), float("nan"), device="cuda", dtype=dtype)[:, :vocab]
+    for row, far in ((0, top), (1, 8), (2, 8), (3, top)):
+        x[row] = far if shape == "constant" else far - 40
+        x[row, 9000 + row] = far
+        if shape == "peaked":
+            x[row, 50], x[row, 19999] = far, far - 8
+    scores = [-1.0, -1.00001, -2.0, -1.99999]
+    got = _check(x, scores, 2, 2)
+    want = P.beam_select(x.double().cpu().numpy(), np.asarray(scores, np.float32).astype(np.float64), 2, 2)[2]
+    assert np.all(np.abs(got[2].double().cpu().numpy() - want) <= 2.0 ** -21 + 2.0 ** -24 * np.abs(want))
+
+
 def test_equal_logits_go_to_the_lowest_token_and_hypothesis():
     x = torch.zeros(4, 20000, device="cuda")
     pa, tk, _ = _select(x, [-1.0, -1.0, -1.0, -2.0], 4, 32)
