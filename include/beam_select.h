@@ -28,7 +28,8 @@ extern "C" {
  * is no candidate; where a row holds +inf, its +inf logits share the probability.
  *   logits        device [n_groups * n_beams] rows of `vocab` entries, row_stride entries apart: fp32 (format
  *                 VA_LOGITS_F32; 16-byte aligned, row_stride a multiple of 4) or bf16 (VA_LOGITS_BF16; a multiple
- *                 of 8).  vocab 1..VA_SAMPLE_MAX_VOCAB, any; the entries between rows are not used.
+ *                 of 8; a single row's is not looked at).  vocab 1..VA_SAMPLE_MAX_VOCAB, any; the entries between rows
+ *                 are not used.  Rows of an odd vocabulary so need padding between them.
  *   scores        device float [n_groups * n_beams]; -inf: no hypothesis
  *   finished      optional device int32 [n_groups * n_beams], not 0 = finished; end_token then in 0..vocab-1
  *   n_beams       1..VA_BEAM_MAX_BEAMS; n_out 1..VA_SAMPLE_MAX_K; n_groups 1..VA_BEAM_MAX_GROUPS

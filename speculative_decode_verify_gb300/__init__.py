@@ -497,8 +497,10 @@ def va_beam_workspace_bytes(n_groups: int, n_beams: int, vocab: int, n_out: int)
 def va_beam_select(logits, scores, n_beams: int, parents, tokens, out_scores, workspace, finished=None, end_token: int = 0,
                    stream=None, variant: str = "") -> None:
     """The best n_out continuations of each request's n_beams hypotheses: logits [n_groups * n_beams, vocab] (float32
-    or bfloat16, rows at any stride that keeps them 16-byte aligned), scores [n_groups * n_beams]; writes parents,
-    tokens and out_scores [n_groups, n_out].  ``workspace``: va_beam_workspace_bytes(...) bytes, zeroed once."""
+    or bfloat16, rows at any stride that keeps them 16-byte aligned: a multiple of 4 or 8 entries, so that several rows
+    of a vocabulary that is none need padding, as in torch.empty(rows, padded)[:, :vocab]), scores [n_groups *
+    n_beams]; writes parents, tokens and out_scores [n_groups, n_out].  ``workspace``: va_beam_workspace_bytes(...)
+    bytes, zeroed once."""
     torch = _torch or _import_torch()
     rows, vocab = logits.shape
     groups, n_out = parents.shape

@@ -581,9 +581,9 @@ va_status va_beam_select(const void* logits, int format, int64_t row_stride, int
     if (need == 0 || !logits || !scores || !parents || !tokens || !out_scores || !workspace) return VA_INVALID_ARG;
     if (format != VA_LOGITS_F32 && format != VA_LOGITS_BF16) return VA_INVALID_ARG;
     if (!va::paged::aligned16(logits) || !va::paged::aligned16(workspace) || workspace_bytes < need) return VA_INVALID_ARG;
-    if (row_stride < vocab || row_stride % (format == VA_LOGITS_BF16 ? 8 : 4) != 0) return VA_INVALID_ARG;
-    if (finished && (end_token < 0 || end_token >= vocab)) return VA_INVALID_ARG;
     const size_t rows = (size_t)n_groups * n_beams;
+    if (rows > 1 && (row_stride < vocab || row_stride % (format == VA_LOGITS_BF16 ? 8 : 4) != 0)) return VA_INVALID_ARG;
+    if (finished && (end_token < 0 || end_token >= vocab)) return VA_INVALID_ARG;
     const int tiles = beam_tiles(vocab);
     va::beam::BeamArgs a;
     a.logits = logits; a.stride = row_stride; a.scores = scores; a.finished = finished;

@@ -76,6 +76,15 @@ def test_masked_infinite_and_nan_logits():
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab,stride", [(5, 5), (50257, 50257), (9001, 1), (8193, 0)])
+def test_a_single_rows_stride_does_not_matter(dtype, vocab, stride):
+    x = _rows(vocab, 1, vocab, dtype).clone()
+    _check(x.as_strided((1, vocab), (stride, 1)), [-1.0], 1, 4)
+    with pytest.raises(va.VerifyAttnError):
+        _select(_rows(vocab, 2, vocab, dtype).contiguous().as_strided((2, vocab - 1), (vocab, 1)), [-1.0, -2.0], 2, 2)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("shape", ["one", "constant", "peaked"])
 @pytest.mark.parametrize("top", [-720, 24, 96, 360, 720, 1016, 2032])
 def test_a_rows_offset_does_not_move_its_scores(dtype, shape, top):
