@@ -275,16 +275,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int key0 = (walk.page0 + (i - i_begin)) * kPage;
                     // some row does not see all of the page's keys
                     const bool edge = key0 + kPage - 1 > len - live || (a.window > 0 && key0 < len - a.window);
-                    // this warp's KB blocks; past: blocks that begin past the sequence, where scales may be anything
+                    // this warp's KB blocks; no row sees those past the sequence, where scales may be anything, and those
+                    // before its first window
                     const int k0 = kg * KB;
                     const bool none = edge && (key0 + k0 * kBlock >= len ||
-                                               (a.window > 0 && key0 + (k0 + KB) * kBlock <= len - live - a.window + 1));
+                                               key0 + (k0 + KB) * kBlock <= seen_from(len, live, a.window));
                     if (!none) {
                         float vs[KB];
                         float vmax = 0.0f;
 #pragma unroll
                         for (int k = 0; k < KB; ++k) {
-                            vs[k] = edge && key0 + (k0 + k) * kBlock >= len ? 0.0f : sc[kBlocks + k0 + k];
+                            vs[k] = sc[kBlocks + k0 + k];
+                            if (edge) {
+                                const int at = key0 + (k0 + k) * kBlock;
+                                if (at >= len || at + kBlock <= seen_from(len, live, a.window)) vs[k] = 0.0f;
+                            }
                             vmax = fmaxf(vmax, vs[k]);
                         }
                         if (vmax > R) {

@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
         int t = 0;
         bool ok = true;
         while (ok && walk.next(ms.plan, a, share.n)) {
+            const int from = seen_from(walk.len, walk.live, a.window);
             for (int p0 = walk.begin; p0 < walk.end; p0 += 2, ++t) {
                 const int n_pages = min(2, walk.end - p0), key0 = (walk.page0 + p0 - walk.begin) * kPage;
                 float sc[2] = {0.0f, 0.0f}, vmax = 0.0f;
@@ -267,7 +268,10 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
                     if (!(ok = warp_wait(bar(ms.raw_full[s]), ((p0 + hp) / NR) & 1, abort, status))) break;
                     const bool page_ok = ms.ring_ok[s] != 0;
                     if (lane < 8) sc[hp] = ms.ring_scale[s][lane];
-                    const bool in = page_ok && lane >= 4 && lane < 8 && key0 + hp * kPage + 16 * (lane & 3) < walk.len;
+                    // V's of blocks that no row sees are 0
+                    const int at = key0 + hp * kPage + kBlock * (lane & 3);
+                    const bool in = page_ok && lane >= 4 && lane < 8 && at < walk.len && at + kBlock > from;
+                    if (!in && lane >= 4) sc[hp] = 0.0f;
                     // (positive floats order like their bits)
                     vmax = fmaxf(vmax, __uint_as_float(__reduce_max_sync(0xffffffffu, in ? __float_as_uint(sc[hp]) : 0u)));
                     good |= page_ok ? 1 << hp : 0;

@@ -43,14 +43,16 @@ struct AttnPagedArgs {
     int n_seqs, n_rows, n_kv, group, max_pages, n_pages, window, n_ctas;
 };
 
+// The first position that a row of a sequence sees, or less.
+__device__ __forceinline__ int seen_from(int len, int live, int window) { return window > 0 ? len - live - window + 1 : 0; }
+
 // The visible pages of a sequence: [first, first + n).
 struct Span {
     int first, n;
 };
 __device__ __forceinline__ Span span_of(int len, int live, int window) {
     Span s;
-    const int lo = window > 0 ? max(0, len - live - window + 1) : 0;
-    s.first = lo / kPage;
+    s.first = max(0, seen_from(len, live, window)) / kPage;
     s.n = live > 0 ? (len + kPage - 1) / kPage - s.first : 0;
     return s;
 }

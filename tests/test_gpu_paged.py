@@ -225,6 +225,23 @@ def test_windows(window):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,group", [(1, 6), (6, 2), (8, 3), (8, 6), (8, 8)])
+@pytest.mark.parametrize("window", [20, 40, 90])
+def test_values_before_the_window_do_not_matter(fmt, rows, group, window):
+    """Blocks before every row's window, in pages whose end is seen, get scales of 2^60 and more: output and bounds are
+    those of the cache without them."""
+    c = Cache(44, [500, 442, 1343, 190], 2, fmt)
+    live, dev, hidden = [rows] * 4, c.dev(0), 0
+    for b, n in enumerate(c.lens):
+        first = n - rows - window + 1                        # the first position that a row sees
+        for block in range(first // 64 * 4, first // 16):
+            dev[3][c.table[b][block // 4], :, block % 4] = 2.0 ** (60 + 20 * (block % 4))
+            hidden += 1
+    assert hidden
+    _check(c, _attend(c, dev, live, rows, group, window=window), live, window=window)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("spread,scale", [(40.0, SCALE), (1.0, -0.3), (1.0, 0.0), (1e-4, 5.0), (1.0, 3.0)])
 def test_peaky_flat_and_negative_scores(fmt, spread, scale):
     c = Cache(33, [700, 90], 1, fmt)
