@@ -14,10 +14,8 @@ EncodeTiledFn encode_fn();   // attn_tc.cu
 
 namespace paged {
 
-cudaError_t launch_attn_e4m3(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, const uint8_t* k_codes,
-                             const uint8_t* v_codes, cudaStream_t stream);
-cudaError_t launch_attn_int8(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, const uint8_t* k_codes,
-                             const uint8_t* v_codes, cudaStream_t stream);
+cudaError_t launch_attn_e4m3(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream);
+cudaError_t launch_attn_int8(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream);
 
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kMost = kMaxCtas / kJoinWarps;   // most parts of a warp
@@ -184,6 +182,7 @@ va_status verify_attn_paged_b8(const va_bf16* q, int n_seqs, int n_rows, int n_k
     const int sms = va::device_sm_count();
     AttnPagedArgs a;
     a.q = q; a.n_live = n_live; a.lens = lens; a.table = table;
+    a.k_codes = static_cast<const uint8_t*>(k_codes); a.v_codes = static_cast<const uint8_t*>(v_codes);
     a.k_scale = k_scale; a.v_scale = v_scale; a.sink = sink; a.out = out; a.out_lse = out_lse;
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + kPartFloats);
@@ -197,7 +196,7 @@ va_status verify_attn_paged_b8(const va_bf16* q, int n_seqs, int n_rows, int n_k
     if (n_rows * group <= kFewPairs && !(encode_pool(&mk, k_codes, pool_rows) && encode_pool(&mv, v_codes, pool_rows)))
         return VA_CUDA_ERROR;
     st = launched((format == VA_B8_INT8 ? launch_attn_int8 : launch_attn_e4m3)(
-        a, mk, mv, static_cast<const uint8_t*>(k_codes), static_cast<const uint8_t*>(v_codes), (cudaStream_t)stream));
+        a, mk, mv, (cudaStream_t)stream));
     if (st != VA_OK) return st;
     // about one CTA an SM: a unit each where there are enough, else its pairs are shared out
     const int units = n_seqs * n_kv_heads, pairs = n_rows * group;

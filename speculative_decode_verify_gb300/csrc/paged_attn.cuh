@@ -11,12 +11,14 @@
 //   shared-memory reads of K (two rows a phase) and of V (four rows of even or odd order) then meet no bank twice.
 // The softmax is online, in base 2: p = 2^(t - m + 6) with m raised only when a score passes it by 8, so f16 holds
 // p <= 2^14 to 11 bits down to 2^-20 of the maximum (and to 2^-31 of it absolutely); sums are fp32.  The blocks' V
-// scales go into p relative to R, the largest so far (a power of two), which f16 would not hold by themselves.
+// scales go into p relative to R, the largest so far (a power of two), which f16 would not hold by themselves
+// (scales that lie far apart: paged_exact.cuh).
 // Measured, E4M3, one token of 6 query heads a KV head: 64 sequences of 1 to 16K positions, 8 KV heads (262 MB) 58.3
 // us, 4.5 TB/s; 4 sequences of 1K, one KV head 10.9 us, most of it the two launches' and the segments' one-time work.
 #pragma once
 
 #include "paged_attn_tc.cuh"
+#include "paged_exact.cuh"
 #include "paged_plan.cuh"
 
 namespace va {
@@ -93,11 +95,12 @@ struct Shape {
     static constexpr int kCols = 8 * RT;                                       // pairs
     static constexpr int kSlotFloats = kCols * kD;
     static constexpr int kFixed = kConsumers * (kSlotFloats + 10 * kCols) * 4  // the warps' slots, (m, l) and weights
-                                  + (int)sizeof(Plan) + 2048;                  // barriers, tickets, alignment
+                                  + (int)sizeof(Plan) + 2048;                  // barriers, tickets, share, alignment
     static constexpr int kFit = (227 * 1024 - 1024 - kFixed) / (kTileBytes + 32);
     static constexpr int kStages = kFit < 12 ? kFit : 12;
     static constexpr int kBytes = 1024 + kFixed + kStages * (kTileBytes + 32);
     static_assert(kStages >= 4, "the ring needs a few pages");
+    static_assert(sizeof(ExactSmem) <= kConsumers * kSlotFloats * 4, "in the slots' place");
     static_assert(sizeof(Plan) % 16 == 0, "the scales behind it are written by bulk copies");
 };
 
@@ -119,7 +122,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int* tickets = reinterpret_cast<int*>(scales + NS * 8);
     int* issued = tickets + kTickets;         // each stage's uses so far
     int* valid = issued + 16;                 // whether its tile has a page
-    int* flags = valid + 16;                  // [0]: the CTA gives up
+    int* flags = valid + 16;                  // [0]: the CTA gives up; [1]: it has met V scales far apart
+    Share& share_s = *reinterpret_cast<Share*>(flags + 4);
     const uint32_t full0 = ptx::smem_u32(bars), empty0 = full0 + 8 * 16, free0 = full0 + 8 * 32;
     const uint32_t filled = full0 + 8 * 40, joined = full0 + 8 * 41;
     volatile int* abort = flags;
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ptx::mbar_init(filled, kConsumers);
         ptx::mbar_init(joined, kConsumers);
         ptx::mbar_init_fence();
-        flags[0] = 0;
+        flags[0] = flags[1] = 0;
         for (int s = 0; s < 16; ++s) issued[s] = 0;
     }
     for (int i = tid; i < kTickets; i += kAttnThreads) tickets[i] = 0;
@@ -147,6 +151,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int status = 0;
     const Share share = make_plan<kAttnThreads>(plan, a);
     if ((int)blockIdx.x >= share.n_ctas) return;
+    if (tid == 0) share_s = share;
 
     if (warp >= kConsumers) {
         ptx::set_max_regs_dec<kProducerRegs>();
@@ -199,7 +204,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         float2* my_ml = slot_ml + warp * kCols;
         // how often the slot has been filled for a single warp's join, and for a common one; which was the last
         int uses = 0, joins = 0, slot_use = 0;
-        bool given_up = false;
+        bool given_up = false, far = false;
         Walk walk(share);
         while (!given_up && walk.next(plan, a, share.n)) {
             const int b = walk.b, h = walk.h, len = walk.len, live = walk.live, i_begin = walk.begin, i_end = walk.end;
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         for (int e = 0; e < 4; ++e) o[n][d][e] = 0.0f;
                 }
             }
-            float R = 0.0f, inv_r = 0.0f;
+            float R = 0.0f, inv_r = 0.0f, vmin = INFINITY;
             for (; i < i_end; i += T) {
                 const int st = i % NS;
                 if (!page_wait(issued + st, i / NS, full0 + 8 * st, (i / NS) & 1, abort, status)) {
@@ -291,6 +296,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 if (at >= len || at + kBlock <= seen_from(len, live, a.window)) vs[k] = 0.0f;
                             }
                             vmax = fmaxf(vmax, vs[k]);
+                            vmin = fminf(vmin, vs[k] > 0.0f ? vs[k] : INFINITY);
                         }
                         if (vmax > R) {
                             const uint32_t next = (__float_as_uint(vmax) + 0x7FFFFFu) & 0x7F800000u;
@@ -445,6 +451,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(empty0 + 8 * st);
             }
             if (given_up) break;
+            far = far || R > kFar * vmin;
             // -------------------------------------------------------- sums of the segment, into the warp's slot
             const int active = min(T, seg_len) * KG;              // warps that have a part of it
             if (slot_use == 1 && !warp_wait(free0 + 8 * warp, (uses - 1) & 1, abort, status)) break;
@@ -595,6 +602,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane < active) ptx::mbar_arrive(free0 + 8 * warp_of(lane));
             }
         }
+        // -------------------------------------------------------- segments whose V scales lie far apart, again
+        if (far && lane == 0) flags[1] = 1;
+        static_assert(kConsumers == kExactWarps, "the consumers compute them");
+        ptx::named_bar_sync(1, 32 * kConsumers);
+        if (flags[1] != 0) {
+            const Share again = share_s;
+            exact_segments<kInt8>(a, plan, again, *reinterpret_cast<ExactSmem*>(slots));
+        }
     }
     if (status && a.dev_status) atomicOr(a.dev_status, status);
 }
@@ -615,14 +630,13 @@ cudaError_t launch_shape(const AttnPagedArgs& a, const CUtensorMap& k, const CUt
 // there, 30 of 32 sequences in a window of 4,096 44 us and 35.6 us; 6 pairs of 64 ragged sequences of 1 to 16K 58.3 us
 // here and 124 us there, 4 pairs of 64 sequences of 4K INT8 45.2 us and 96.2 us.
 template <bool kInt8>
-cudaError_t launch_format(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, const uint8_t* k_codes,
-                          const uint8_t* v_codes, cudaStream_t stream) {
+cudaError_t launch_format(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
     const int cols = a.n_rows * a.group;
     if (cols <= 8) return launch_shape<kInt8, 1>(a, k, v, stream);
     if (cols <= kFewPairs) return launch_shape<kInt8, 2>(a, k, v, stream);
-    if (cols <= 32) return tcg::launch<kInt8, 32>(a, k_codes, v_codes, stream);
-    if (cols <= 48) return tcg::launch<kInt8, 48>(a, k_codes, v_codes, stream);
-    return tcg::launch<kInt8, 64>(a, k_codes, v_codes, stream);
+    if (cols <= 32) return tcg::launch<kInt8, 32>(a, stream);
+    if (cols <= 48) return tcg::launch<kInt8, 48>(a, stream);
+    return tcg::launch<kInt8, 64>(a, stream);
 }
 
 }  // namespace paged

@@ -3,9 +3,8 @@
 
 namespace va {
 namespace paged {
-cudaError_t launch_attn_int8(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, const uint8_t* k_codes,
-                             const uint8_t* v_codes, cudaStream_t stream) {
-    return launch_format<true>(a, k, v, k_codes, v_codes, stream);
+cudaError_t launch_attn_int8(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+    return launch_format<true>(a, k, v, stream);
 }
 }  // namespace paged
 }  // namespace va

@@ -11,7 +11,7 @@
 //   issuer     one thread: the scores of tile i + 1 before the products of tile i
 //   scales     one warp: a tile's scales, and the largest V scale
 //   softmax    four warps for every 16 pairs, a key a thread: as in paged_attn.cuh (base 2, a reference that is
-//              raised when a score passes it by 2^8, V's scales relative to the largest so far), with one reference a
+//              raised when a score passes it by 8, V's scales relative to the largest so far), with one reference a
 //              pair for the whole CTA, so that a segment leaves one sum and nothing is joined inside the CTA.  The
 //              warps agree on each tile whether to raise; raising rescales the accumulator in TMEM.
 // Bound by the softmax warps: 1.6 us for a tile of 128 keys at 48 pairs, 2.9 us where a reference is raised; and by
@@ -21,6 +21,7 @@
 // 30 pairs of 32 sequences in a window of 4,096, INT8, two KV heads 35.6 us (37.2 us).
 #pragma once
 
+#include "paged_exact.cuh"
 #include "paged_plan.cuh"
 
 namespace va {
@@ -48,7 +49,8 @@ struct Misc {
     int ring_ok[6], ok[4];
     alignas(16) unsigned char flag[2][kMaxSoftWarps];
     uint32_t tmem;
-    int abort;
+    int abort, far;                                // far: the CTA has met V scales far apart
+    Share share;
     alignas(16) float2 ub[kMaxSoftWarps][16];      // raising: what comes off a pair's exponents, its sums' factor
 };
 
@@ -70,6 +72,7 @@ struct Shape {
     static constexpr int kStages = kFit < 6 ? kFit : 6;
     static constexpr int kBytes = 1024 + (int)kOffRing + kStages * kTileBytes + (int)sizeof(Misc);
     static_assert(kStages >= 4, "two tiles of pages");
+    static_assert(kSoftWarps >= kExactWarps && sizeof(ExactSmem) <= kOffRing, "exact_segments' warps and place");
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int a_mn, int b_mn) {
@@ -114,7 +117,7 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[n]) {
 
 template <bool kInt8, int NC>
 __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
-    attn_paged_tc_kernel(const AttnPagedArgs a, const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ v_codes) {
+    attn_paged_tc_kernel(const AttnPagedArgs a) {
     using S = Shape<NC>;
     constexpr int NR = S::kStages, NH = S::NH, kSoftWarps = S::kSoftWarps, kThreads = S::kThreads;
     constexpr int kIssuer = kSoftWarps + kWideWarps;       // then the producer's and the scales' warp
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
         ptx::mbar_init(bar(ms.join), kSoftWarps);
         ptx::mbar_init(bar(ms.drain), 1);
         ptx::mbar_init_fence();
-        ms.abort = 0;
+        ms.abort = ms.far = 0;
         for (int s = 0; s < 2; ++s) *reinterpret_cast<uint4*>(ms.flag[s]) = make_uint4(0u, 0u, 0u, 0u);
     }
     __syncthreads();
@@ -155,6 +158,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
     int status = 0;
     const Share share = make_plan<kThreads>(ms.plan, a);
     if ((int)blockIdx.x >= share.n_ctas || share.n == 0) return;
+    if (tid == 0) ms.share = share;
     if (warp == 0) ptx::tmem_alloc(ptx::smem_u32(&ms.tmem), kTmemCols);
     ptx::tc_fence_before();
     __syncthreads();
@@ -188,7 +192,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
                 if (r >= 0) {
                     if (lane < 2)
                         ptx::bulk_load(ptx::smem_u32(ring + s * kTileBytes) + lane * kHeadBytes,
-                                       (lane ? v_codes : k_codes) + (size_t)r * kHeadBytes, kHeadBytes, full);
+                                       (lane ? a.v_codes : a.k_codes) + (size_t)r * kHeadBytes, kHeadBytes, full);
                     else if (lane < 4)
                         ptx::bulk_load(ptx::smem_u32(ms.ring_scale[s]) + 16 * (lane - 2),
                                        (lane == 2 ? a.k_scale : a.v_scale) + (size_t)r * kBlocks, 16, full);
@@ -259,6 +263,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
         bool ok = true;
         while (ok && walk.next(ms.plan, a, share.n)) {
             const int from = seen_from(walk.len, walk.live, a.window);
+            uint32_t highest = 0u, lowest = 0x7F800000u;     // of the segment's V scales, this lane's
             for (int p0 = walk.begin; p0 < walk.end; p0 += 2, ++t) {
                 const int n_pages = min(2, walk.end - p0), key0 = (walk.page0 + p0 - walk.begin) * kPage;
                 float sc[2] = {0.0f, 0.0f}, vmax = 0.0f;
@@ -290,7 +295,16 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(ms.k_ready));
+#pragma unroll
+                for (int hp = 0; hp < 2; ++hp) {
+                    const uint32_t s = lane >= 4 ? __float_as_uint(sc[hp]) : 0u;
+                    highest = max(highest, s);
+                    lowest = min(lowest, s == 0u ? 0x7F800000u : s);
+                }
             }
+            highest = __reduce_max_sync(0xffffffffu, highest);
+            lowest = __reduce_min_sync(0xffffffffu, lowest);
+            if (lane == 0 && __uint_as_float(highest) > kFar / 2 * __uint_as_float(lowest)) ms.far = 1;
         }
     }
     } else if (warp >= kSoftWarps) {
@@ -603,16 +617,21 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, kTmemCols);
     }
+    // segments whose V scales lie far apart, again
+    if (ms.far != 0 && warp < kExactWarps) {
+        const Share again = ms.share;
+        exact_segments<kInt8>(a, ms.plan, again, *reinterpret_cast<ExactSmem*>(base));
+    }
 }
 
 template <bool kInt8, int NC>
-cudaError_t launch(const AttnPagedArgs& a, const uint8_t* k, const uint8_t* v, cudaStream_t stream) {
+cudaError_t launch(const AttnPagedArgs& a, cudaStream_t stream) {
     const cudaError_t e = ensure_smem_attr((const void*)attn_paged_tc_kernel<kInt8, NC>, Shape<NC>::kBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     pdl_config(&cfg, attr, dim3((unsigned)a.n_ctas), dim3(Shape<NC>::kThreads), Shape<NC>::kBytes, stream);
-    return cudaLaunchKernelEx(&cfg, attn_paged_tc_kernel<kInt8, NC>, a, k, v);
+    return cudaLaunchKernelEx(&cfg, attn_paged_tc_kernel<kInt8, NC>, a);
 }
 
 }  // namespace tcg

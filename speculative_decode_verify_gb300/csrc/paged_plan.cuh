@@ -32,6 +32,7 @@ constexpr size_t kWorkspaceBytes = sizeof(float) * (kPartFloats + (size_t)2 * kM
 struct AttnPagedArgs {
     const uint16_t* q;
     const int32_t *n_live, *lens, *table;
+    const uint8_t *k_codes, *v_codes;
     const float *k_scale, *v_scale;
     const float* sink;
     float* part_o;

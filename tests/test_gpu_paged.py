@@ -272,6 +272,117 @@ def test_scales_that_differ_by_orders_of_magnitude_with_many_pairs(fmt, rows, gr
     _check(c, _attend(c, c.dev(0), [rows, rows], rows, group), [rows, rows])
 
 
+def _far_apart(seed, lens, kv, fmt, rows, group, down, small=(1,)):
+    """A cache whose blocks `small` of every sequence have V scales 2^-down of the others', and queries whose weight is on a
+    key of the first of them."""
+    c = Cache(seed, lens, kv, fmt)
+    for b, n in enumerate(c.lens):
+        for block in small:
+            if 16 * block < n:
+                c.scale["v"][0, c.table[b][block // 4], :, block % 4] *= np.float32(2.0 ** -down)
+    rng = np.random.default_rng(seed)
+    q = rng.standard_normal((len(lens), rows, kv, group, D)) * 0.1
+    for b, n in enumerate(c.lens):
+        at = 16 * small[0] + 3
+        if at < n - rows:
+            page = c.table[b][at // 64]
+            k = P.decode(c.codes["k"][0, page, :, at % 64], fmt) * c.scale["k"][0, page, :, at % 64 // 16, None]
+            q[b] += k[None, :, None] * np.array([2.0, 0.5, 1.0, 1.5, 0.0, 2.0, 1.0, 0.7])[None, None, :group, None]
+    return c, bf16(q.reshape(len(lens), rows, kv * group, D))
+
+
+def _check_far(c, got, live, small, sink=None, window=0, table=None, status=0):
+    """As _check, but a page with a block of `small` next to others is computed in fp32 (an exponential and sums over at most
+    8 x 256 keys: 2^-16), so that the bound's term for weights below f16's range (2^-30 of n keys of the largest
+    code and scale, at the segment's largest weight) is left for the keys of the other pages alone."""
+    qn, out, lse, st = got
+    table = table or c.table
+    want = P.attention(qn, live, c.lens, table, c.codes["k"][0], c.codes["v"][0], c.scale["k"][0], c.scale["v"][0], c.fmt,
+                       SCALE, sink, window)
+    assert st == status
+    rest = np.zeros(want[1].shape)              # the largest weight of a key in another page
+    for b, n in enumerate(live):
+        pages = [x for x in range(-(-c.lens[b] // 64)) if 0 <= table[b][x] < c.pages and x not in [i // 4 for i in small]]
+        for h in range(qn.shape[2]):
+            for x in pages:
+                kv = h // (qn.shape[2] // c.kv)
+                k = P.decode(c.codes["k"][0, table[b][x], kv], c.fmt) * np.repeat(c.scale["k"][0, table[b][x], kv], 16)[:, None]
+                for r in range(n):
+                    p = c.lens[b] - n + r - 64 * x              # the row's position in the page
+                    lo = max(0, p - window + 1) if window else 0
+                    if p >= lo and lo < 64:
+                        z = SCALE * (k[lo:p + 1].astype(np.float64) @ qn[b, r, h])
+                        rest[b, r, h] = max(rest[b, r, h], np.exp(z.max() - want[1][b, r, h]))
+    tol_out, tol_lse = attention_bounds(*want[:4], want[4] * rest)
+    assert np.all(np.abs(out - want[0]) <= tol_out), np.max(np.abs(out - want[0]) / np.maximum(tol_out, 1e-300))
+    some = np.isfinite(want[1])
+    assert np.array_equal(some, np.isfinite(lse)) and np.all(np.abs(lse[some] - want[1][some]) <= tol_lse[some])
+    for b, n in enumerate(live):
+        assert np.all(out[b, n:] == 0) and np.all(lse[b, n:] == -np.inf)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,group", [(1, 6), (3, 4), (8, 3), (8, 6), (8, 8)])
+@pytest.mark.parametrize("down", [8, 11, 20, 24, 28, 31, 45, 70])
+def test_a_block_of_small_values_that_carries_the_weight(fmt, rows, group, down):
+    c, q = _far_apart(45, [700, 0, 130, 40], 2, fmt, rows, group, down)
+    live = [rows, 0, rows, min(rows, 2)]
+    for sink in (None, list(np.linspace(-2, 30, 2 * group))):
+        got = _attend(c, c.dev(0), live, rows, group, qs=q, sink=sink)
+        if down < 11:
+            _check(c, got, live, sink=sink)
+        else:
+            _check_far(c, got, live, (1,), sink=sink)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,group", [(2, 5), (8, 6)])
+@pytest.mark.parametrize("window,none", [(0, True), (150, False), (150, True), (70, False)])
+def test_scales_far_apart_in_windows_and_with_pages_that_are_none(fmt, rows, group, window, none):
+    small = (41, 42, 43, 14, 17, 1, 2, 80)
+    c, q = _far_apart(46, [700, 300, 64, 1300], 2, fmt, rows, group, 40, small)
+    live = [rows, 1, rows, rows]
+    table = [list(r) for r in c.table]
+    if none:
+        table[0][9] = -1
+        table[3][19] = c.pages
+    _check_far(c, _attend(c, c.dev(0), live, rows, group, qs=q, window=window, table=table), live, small, window=window,
+               table=table, status=128 if none else 0)
+
+
+@pytest.mark.parametrize("rows,group", [(1, 6), (8, 6)])
+def test_scales_far_apart_leave_the_other_heads_bits_alone(rows, group):
+    """Calls in which one sequence's one head has such scales, and calls without them, on one workspace."""
+    c, q = _far_apart(47, [900, 300, 500], 2, "e4m3", rows, group, 0)
+    dev, live = c.dev(0), [rows, rows, 1]
+    ws = torch.full((va.va_paged_workspace_bytes(3, rows, 2, group),), 0xFF, dtype=torch.uint8, device="cuda")
+    plain = _attend(c, dev, live, rows, group, qs=q, ws=ws)
+    c.scale["v"][0, c.table[1][0], 1, 1] *= np.float32(2.0 ** -30)
+    far = [_attend(c, c.dev(0), live, rows, group, qs=q, ws=ws) for _ in range(2)]
+    for i in (1, 2):
+        np.testing.assert_array_equal(far[0][i], far[1][i])
+        same = np.ones(far[0][i].shape, bool)
+        same[1, :, group:] = False
+        np.testing.assert_array_equal(far[0][i][same], plain[i][same])
+    _check(c, far[0], live)
+    again = _attend(c, dev, live, rows, group, qs=q, ws=ws)
+    for i in (1, 2):
+        np.testing.assert_array_equal(again[i], plain[i])
+
+
+@pytest.mark.parametrize("rows,group", [(2, 6), (8, 6)])
+def test_scales_far_apart_and_a_query_without_a_number(rows, group):
+    c, clean = _far_apart(48, [700, 130], 2, "e4m3", rows, group, 30)
+    q = clean[0].clone()
+    q[0, 1, 2, 7] = float("nan")
+    got = [_attend(c, c.dev(0), [rows, rows], rows, group, qs=(t, None)) for t in (clean[0], q)]
+    hit = np.zeros(got[0][2].shape, bool)
+    hit[0, 1, 2] = True
+    assert np.all(np.isnan(got[1][1][hit])) and np.all(np.isnan(got[1][2][hit]))
+    for i in (1, 2):
+        np.testing.assert_array_equal(got[0][i][~hit], got[1][i][~hit])
+
+
 def test_pages_that_are_none_are_masked_and_told():
     c = Cache(35, [300, 200, 64], 1, "e4m3")
     for bad in (-1, c.pages, 2 ** 31 - 1, -7):
