@@ -61,7 +61,7 @@ struct Misc {
 //   NC 64  896 threads x 72 = 512 x  72 + 256 x 64 + 128 x 88
 template <int NC>
 struct Shape {
-    static constexpr int NH = 16;
+    static constexpr int NH = 16;                      // pairs of a softmax warp: one TMEM load's columns
     static constexpr int kSoftWarps = 4 * NC / NH;
     static constexpr int kThreads = 32 * (kSoftWarps + kWideWarps + 4);
     static constexpr int kSoftRegs = NC == 32 ? 120 : (NC == 48 ? 88 : 72), kWideRegs = NC == 64 ? 64 : 72;
@@ -100,19 +100,6 @@ __device__ __forceinline__ void widen16(const uint4& c, uint4& lo, uint4& hi) {
     }
     lo = make_uint4(r[0], r[1], r[2], r[3]);
     hi = make_uint4(r[4], r[5], r[6], r[7]);
-}
-
-template <int n>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[n]) {
-    static_assert(n == 8 || n == 16, "a softmax warp's pairs");
-    if constexpr (n == 8) ptx::tmem_ld8_wait(taddr, v);
-    else ptx::tmem_ld16_wait(taddr, v);
-}
-template <int n>
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[n]) {
-    if constexpr (n == 8) ptx::tmem_st8(taddr, v);
-    else ptx::tmem_st16(taddr, v);
-    ptx::tmem_wait_st();
 }
 
 template <bool kInt8, int NC>
@@ -430,7 +417,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
                 if (!(ok = warp_wait(bar(ms.s_full[t & 1]), (t >> 1) & 1, abort, status))) break;
                 ptx::tc_fence_after();
                 float y[NH];
-                tmem_ld<NH>(tl + kColS + (t & 1) * 64 + n0, y);
+                ptx::tmem_ld16_wait(tl + kColS + (t & 1) * 64 + n0, y);
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(ms.s_free[t & 1]));
@@ -496,7 +483,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
                     if (i > 0) {
                         if (!(ok = warp_wait(bar(ms.pv_done[(t - 1) & 1]), ((t - 1) >> 1) & 1, abort, status))) break;
                         ptx::tc_fence_after();
-                        tmem_ld<NH>(tl + kColO + n0, o);
+                        ptx::tmem_ld16_wait(tl + kColO + n0, o);
                     }
                     // lane c finds pair n0 + c's new reference
                     if (lane < NH) {
@@ -526,7 +513,10 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
                             o[c + 1] *= w.w * r_by;
                         }
                     }
-                    if (i > 0) tmem_st<NH>(tl + kColO + n0, o);
+                    if (i > 0) {
+                        ptx::tmem_st16(tl + kColO + n0, o);
+                        ptx::tmem_wait_st();
+                    }
                     ptx::tc_fence_before();
                     all_set = __all_sync(0xffffffffu, lane >= NH || ref[lane] != kNoScore);
                 }
@@ -561,7 +551,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < NH; ++c) stage[(n0 + c) * kKeys + me] = l[c];
             float o[NH];
-            tmem_ld<NH>(tl + kColO + n0, o);
+            ptx::tmem_ld16_wait(tl + kColO + n0, o);
             ptx::tc_fence_before();
             if (!meet()) break;
             if (lane == 0) ptx::mbar_arrive(bar(ms.o_free));

@@ -217,18 +217,6 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 
 // 16 consecutive 32-bit columns of this thread's TMEM lane (warp-wide, 32x32b shape).  The wait is in the
 // same asm statement, so the outputs cannot be used before the load has completed.
-__device__ __forceinline__ void tmem_ld8_wait(uint32_t taddr, float* v) {
-    uint32_t r[8];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 __device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, float* v) {
     uint32_t r[16];
     asm volatile(
