@@ -50,8 +50,8 @@ __device__ __forceinline__ uint2 round8(const float (&q)[8]) {
 // Eight floats to the codes of their correctly rounded quotients x / s.  inv is 1 / s correctly rounded, and
 // q' = q + (x - q s) inv with q = x inv is then the correctly rounded quotient (P. Markstein, Computation of elementary
 // functions on the IBM RISC System/6000 processor, 1990; his condition that q be within one unit in the last place does
-// not always hold here, but q' was compared with x / s for every x and s that this call forms from bf16 rows, for 8e7
-// random s, and for the s whose quotients come nearest to the places where a code could change).  `careful`: infinities
+// not always hold here, but the tests compare the codes with those of x / s for every significand of a bf16 x and of a
+// block's largest value, and for every code coded again from one such scale to another).  `careful`: infinities
 // among the x, or s so small that the remainder has no digits; these are divided and clamped.
 template <bool kInt8>
 __device__ __forceinline__ uint2 code8(const float (&x)[8], float s, float inv, bool careful) {

@@ -93,6 +93,33 @@ def test_append_rounds_every_quotient_of_bfloat16_values_correctly(fmt, exponent
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("grows", [(0, 1), (2, 5)])             # K's and V's new row, in powers of two
+def test_append_codes_every_older_code_again_correctly_for_every_pair_of_scales(fmt, grows):
+    """A block for each pair of significands of the older rows' largest value and of the new row's; in its older row every
+    code (K: positive, V: negative)."""
+    kv, top = 64, P.TOP[fmt]
+    every = np.minimum(np.arange(128), 126 if fmt == "e4m3" else 127).astype(np.uint8)
+    row = {"k": every, "v": every | 0x80 if fmt == "e4m3" else (-every.astype(np.int8)).view(np.uint8)}
+    for part in range(4):
+        n = 4096 * part + np.arange(4096).reshape(64, kv)
+        older, newer = n // 128, n % 128
+        c = Cache(30, [0] * 64, kv, fmt, spare=64)
+        c.table, c.lens, new = [[b] for b in range(64)], [2] * 64, {}
+        for w, g in zip("kv", grows):
+            c.codes[w][0, :, :, 0] = row[w]
+            c.scale[w][0, :, :, 0] = ((128 + older) / 128).astype(np.float32) / top
+            x = np.zeros((64, 1, kv, D), np.float32)
+            x[:, 0, :, 0] = (128 + newer) / 128 * 2.0 ** g
+            new[w] = bf16(x)
+        dev = c.dev(0)
+        va.kv_page_append_b8(new["k"][0].cuda(), new["v"][0].cuda(), ints([1] * 64), ints(c.lens), ints(c.table), *dev)
+        for w in "kv":
+            for b in range(64):
+                P.append(new[w][1][b].astype(np.float32), 1, 2, c.table[b], c.codes[w][0], c.scale[w][0], fmt)
+        _check_pool(c, dev)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_append_codes_infinities_and_nan_and_says_so(fmt):
     c = Cache(22, [37, 64], 2, fmt)
     dev = c.dev(0)
