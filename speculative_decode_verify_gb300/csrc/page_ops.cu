@@ -5,8 +5,9 @@
 // lowest-numbered free page goes first, so no free list has to be kept in step and the outcome does not depend
 // on the order in which threads run.  The plans (who gets which page) are integers: one CTA makes each, the
 // copies that it asks for run in a launch of their own over all SMs, behind a programmatic dependency.
-// Measured: kv_page_compact of 1,500 live pages of 4,096 (2 heads, 4 layers: 250 MB) 50 us, of which the copy 38 us, 6.5
-// TB/s; kv_page_reorder and kv_page_extend of 32 x 8 hypotheses (4 layers, 2 heads) 17 us, of 1 x 4 7 us.
+// Measured, graph-replayed: kv_page_compact of 1,500 live pages of 4,096 (2 heads, 4 layers: 250 MB) 56 us, of which the
+// copy 38 us, 6.5 TB/s; kv_page_reorder and kv_page_extend behind three copies of the state, 32 x 8 hypotheses (4 layers, 2
+// heads) 22 to 24 us, 1 x 4 (2 layers) 12 to 13 us.
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 

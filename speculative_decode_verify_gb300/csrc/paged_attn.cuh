@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const bool whole = walk.whole;
             int i = i_begin + ((team - i_begin) & (T - 1));
             if (i >= i_end) continue;
-            // Q, each row brought to f16's upper range by a power of two (exact but for elements 2^-39 of the row's
-            // largest); f turns accumulated scores into base-2 exponents
+            // Q, each row brought to f16's upper range by a power of two (exact but for elements below 2^-31 of the row's
+            // largest, which lose digits to 2^-39 and are 0 from there); f turns accumulated scores into base-2 exponents
             uint32_t qf[RT][8][2];
             float f[RT][2], m[RT][2], l[RT][2];
             int p[RT][2];                                     // positions of the columns' rows
