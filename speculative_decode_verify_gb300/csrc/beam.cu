@@ -12,11 +12,12 @@
 // 64 bits.  The last row of a request merges the hypotheses.  Every order is fixed by the keys and by the deal, so the
 // arrivals' order changes nothing.
 // Bytes: the logits once; what a run hands on (k keys) is a thousandth of that.  32 x 8 x 151,669 bf16 logits, 38 of the
-// 256 rows finished (66 MB), take 37.4 us: the tiles' instructions bound it (0.6 us a tile and SM), then the start and
+// 256 rows finished (66 MB), take 37.2 us: the tiles' instructions bound it (0.6 us a tile and SM), then the start and
 // the merges, which are chains of round trips (5 us and 7 us).  On the way: a 64-bit key for every logit 117 us, a
 // ranking for every tile 50 us, finished rows in the deal 50 us, a division for every tile and 32 keys kept in registers
 // for the equal logits' sake 39 us; a list for every warp, which needs no barriers but eight times the insertions,
-// 67 us; three CTAs an SM 37.2 us, the next tile's loads before the barrier 38.3 us (36.5 us with three CTAs).
+// 67 us; then, where four CTAs an SM took 36.9 us, three 37.2 us, and the next tile's loads before the barrier 38.3 us
+// (36.5 us with three CTAs).
 // 1 x 4 x 160,000 logits, one row finished: 10.8 us, all of it such chains.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -13,8 +13,8 @@
 // p <= 2^14 to 11 bits down to 2^-20 of the maximum (and to 2^-31 of it absolutely); sums are fp32.  The blocks' V
 // scales go into p relative to R, the largest so far (a power of two), which f16 would not hold by themselves
 // (scales that lie far apart: paged_exact.cuh).
-// Measured, E4M3, one token of 6 query heads a KV head: 64 sequences of 1 to 16K positions, 8 KV heads (262 MB) 58.3
-// us, 4.5 TB/s; 4 sequences of 1K, one KV head 10.9 us, most of it the two launches' and the segments' one-time work.
+// Measured, E4M3, one token of 6 query heads a KV head: 64 sequences of 1 to 16K positions, 8 KV heads (262 MB) 59.0
+// us, 4.4 TB/s; 4 sequences of 1K, one KV head 10.9 us, most of it the two launches' and the segments' one-time work.
 #pragma once
 
 #include "paged_attn_tc.cuh"
@@ -625,10 +625,12 @@ cudaError_t launch_shape(const AttnPagedArgs& a, const CUtensorMap& k, const CUt
     return cudaLaunchKernelEx(&cfg, attn_paged_kernel<kInt8, RT>, a, k, v);
 }
 
-// By the (row, query head) pairs of a KV head: up to 16 here, more on tcgen05 (paged_attn_tc.cuh).  From 17 on this
-// kernel needs a second warp a code or a third column tile: 48 pairs of one 192K sequence took 48 us here and 36.5 us
-// there, 30 of 32 sequences in a window of 4,096 44 us and 35.6 us; 6 pairs of 64 ragged sequences of 1 to 16K 58.3 us
-// here and 124 us there, 4 pairs of 64 sequences of 4K INT8 45.2 us and 96.2 us.
+// By the (row, query head) pairs of a KV head: up to 16 here, more on tcgen05 (paged_attn_tc.cuh).  Here and there, E4M3,
+// us: 16 pairs of one 192K sequence 24.3 and 31.0, of 64 ragged sequences of 1 to 16K (8 heads) 96.5 and 117, of 64 of 0.1
+// to 1.1K (2 heads) 23.6 and 25.9, of 32 in windows of 4,096 28.2 and 37.3, of 4 of 1K 14.6 and 14.1; 6 pairs of the same
+// 21.0 and 30.7, 60.7 and 115, 16.2 and 24.0, 24.2 and 36.7, 11.1 and 13.5.  From 17 on this kernel needs a second warp a
+// code or a third column tile: 48 pairs of one 192K sequence took 48 us here and 36.5 us there, 30 of 32 sequences in a
+// window of 4,096 44 us and 35.6 us.
 template <bool kInt8>
 cudaError_t launch_format(const AttnPagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
     const int cols = a.n_rows * a.group;

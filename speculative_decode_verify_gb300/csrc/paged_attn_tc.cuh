@@ -16,9 +16,8 @@
 //              warps agree on each tile whether to raise; raising rescales the accumulator in TMEM.
 // Bound by the softmax warps: 1.6 us for a tile of 128 keys at 48 pairs, 2.9 us where a reference is raised; and by
 // what a segment costs once (7.5 us until the first scores, 3 us for its sums).  Measured:
-// 48 pairs of one sequence of 192K, E4M3, one KV head 36.5 us (eight softmax warps, and wideners that took K and V in
-// turn: 38.7 us),
-// 30 pairs of 32 sequences in a window of 4,096, INT8, two KV heads 35.6 us (37.2 us).
+// 48 pairs of one sequence of 192K, E4M3, one KV head 37.1 us, 30 pairs of 32 sequences in a window of 4,096, INT8, two KV
+// heads 36.3 us.  (Eight softmax warps, and wideners that took K and V in turn, took 2.2 and 1.6 us more.)
 #pragma once
 
 #include "paged_exact.cuh"
