@@ -74,7 +74,7 @@ __device__ __forceinline__ void exact_pair(const AttnPagedArgs& a, const Plan& p
             float dot = 0.0f;
 #pragma unroll 2
             for (int c = 0; c < kD / 16; ++c) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(k + key * kD) + c);
+                const uint4 w = reinterpret_cast<const uint4*>(k + key * kD)[c];
                 const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -84,7 +84,7 @@ __device__ __forceinline__ void exact_pair(const AttnPagedArgs& a, const Plan& p
                     for (int d = 0; d < 4; ++d) dot = fmaf(c4[d], sm.q[16 * c + 4 * i + d], dot);
                 }
             }
-            t[e] = key < first || key > last ? -INFINITY : dot * (__ldg(a.k_scale + at * kBlocks + key / kBlock) * a.scale_log2);
+            t[e] = key < first || key > last ? -INFINITY : dot * (a.k_scale[at * kBlocks + key / kBlock] * a.scale_log2);
         }
         float now = fmaxf(t[0], t[1]);
 #pragma unroll
@@ -101,12 +101,12 @@ __device__ __forceinline__ void exact_pair(const AttnPagedArgs& a, const Plan& p
         // (of keys that the row does not see: weight 0, and codes that may be NaN)
 #pragma unroll 1
         for (int block = first / kBlock; block <= last / kBlock; ++block) {
-            const float s = __ldg(a.v_scale + at * kBlocks + block);
+            const float s = a.v_scale[at * kBlocks + block];
 #pragma unroll 8
             for (int i = 0; i < kBlock; ++i) {
                 const int key = block * kBlock + i;
                 const float w = s * __shfl_sync(0xffffffffu, block < 2 ? w0 : w1, key & 31);
-                const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(v + key * kD) + lane);
+                const uint32_t word = reinterpret_cast<const uint32_t*>(v + key * kD)[lane];
                 float x4[4];
                 decode4<kInt8>(key < first || key > last ? 0u : word, x4);
                 acc.x = fmaf(w, x4[0], acc.x);
