@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(empty0 + 8 * st);
             }
             if (given_up) break;
-            far = far || R > kFar * vmin;
+            far = far || R > fminf(kFar * vmin, kHuge);
             // -------------------------------------------------------- sums of the segment, into the warp's slot
             const int active = min(T, seg_len) * KG;              // warps that have a part of it
             if (slot_use == 1 && !warp_wait(free0 + 8 * warp, (uses - 1) & 1, abort, status)) break;

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
             }
             highest = __reduce_max_sync(0xffffffffu, highest);
             lowest = __reduce_min_sync(0xffffffffu, lowest);
-            if (lane == 0 && __uint_as_float(highest) > kFar / 2 * __uint_as_float(lowest)) ms.far = 1;
+            if (lane == 0 && __uint_as_float(highest) > fminf(kFar / 2 * __uint_as_float(lowest), kHuge / 2)) ms.far = 1;
         }
     }
     } else if (warp >= kSoftWarps) {

@@ -3,8 +3,9 @@
 // The split kernels hold weights w = p s in f16, p = 2^(t - m + 6) and s a block's V scale relative to the largest so far.
 // A scale more than 2^10 below that brings the weights of its keys, at 2^6 units by themselves, to where f16 begins to
 // lose digits: at 2^-5, where n others that are rounded to 2^-25 of a unit cost them n 2^-20, and from a ratio of 2^31 on
-// nothing is left, though these keys may carry all the weight.  A CTA that has met such scales (0 aside) computes its
-// segments with such scales again, here: in fp32, from the definition, over what the segment has left.
+// nothing is left, though these keys may carry all the weight.  And at the other end the sums of 2^6 to 2^14 v pass fp32's
+// range where scales pass 2^104.  A CTA that has met scales that far apart (0 aside) or above 2^90 computes its segments
+// with such scales again, here: in fp32, from the definition, over what the segment has left.
 //   Eight warps share a segment's pages and take its (row, query head) pairs one after the other; a lane has two keys'
 // scores and four dimensions' sums.  Caches hardly hold such scales, so this is short rather than fast.  With one block of
 // 2^-20 in each sequence, decode of 64 ragged sequences of 1 to 16K takes 0.99 ms (59 us without), 48 pairs of one
@@ -18,6 +19,7 @@ namespace va {
 namespace paged {
 
 constexpr float kFar = 1024.0f;
+constexpr float kHuge = 1.2379400e27f;      // 2^90
 constexpr int kExactWarps = 8;
 
 struct ExactSmem {
@@ -26,8 +28,8 @@ struct ExactSmem {
     float q[kD];
 };
 
-// Whether the V scales of pages x0 .. x1 - 1 that some row sees lie far apart.  Half of kFar: at least as soon as a split
-// kernel, whose unit is up to twice the largest scale.  Every warp looks at all pages.
+// Whether the V scales of pages x0 .. x1 - 1 that some row sees lie far apart or high.  Half of kFar and kHuge: at least as
+// soon as a split kernel, whose unit is up to twice the largest scale.  Every warp looks at all pages.
 __device__ __forceinline__ bool scales_far_apart(const AttnPagedArgs& a, const Walk& w, int x0, int x1) {
     const int lane = threadIdx.x & 31, from = seen_from(w.len, w.live, a.window);
     uint32_t lowest = 0x7F800000u, highest = 0u;      // (positive floats order like their bits)
@@ -46,7 +48,7 @@ __device__ __forceinline__ bool scales_far_apart(const AttnPagedArgs& a, const W
     }
     lowest = __reduce_min_sync(0xffffffffu, lowest);
     highest = __reduce_max_sync(0xffffffffu, highest);
-    return __uint_as_float(highest) > kFar / 2 * __uint_as_float(lowest);
+    return __uint_as_float(highest) > fminf(kFar / 2 * __uint_as_float(lowest), kHuge / 2);
 }
 
 // Pair `col` over pages x0 .. x1 - 1.

@@ -410,6 +410,22 @@ def test_scales_far_apart_and_a_query_without_a_number(rows, group):
         np.testing.assert_array_equal(got[0][i][~hit], got[1][i][~hit])
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,group", [(1, 6), (3, 4), (8, 6)])
+@pytest.mark.parametrize("up", [-130, -60, 85, 97, 110, 118])
+def test_values_near_the_ends_of_the_range(fmt, rows, group, up):
+    """All values times 2^up: the weighted sums stay in fp32's range as long as the output does (values of 2^-130 lose digits
+    of their scales, which the oracle takes as they are; an output below 2^-126 is a multiple of 2^-133 in bf16)."""
+    c = Cache(49, [700, 64, 130], 2, fmt)
+    with np.errstate(all="ignore"):
+        c.scale["v"] = (c.scale["v"] * 2.0 ** up).astype(np.float32)
+    live = [rows] * 3
+    qn, out, lse, st = _attend(c, c.dev(0), live, rows, group)
+    want = P.attention(qn, live, c.lens, c.table, c.codes["k"][0], c.codes["v"][0], c.scale["k"][0], c.scale["v"][0], fmt, SCALE)
+    tol, _ = attention_bounds(*want)
+    assert st == 0 and np.all(np.isfinite(out)) and np.all(np.abs(out - want[0]) <= tol + 2.0 ** -133)
+
+
 def test_pages_that_are_none_are_masked_and_told():
     c = Cache(35, [300, 200, 64], 1, "e4m3")
     for bad in (-1, c.pages, 2 ** 31 - 1, -7):
