@@ -83,8 +83,8 @@ VA_API va_status kv_page_append_b8(const va_bf16 *k_new, const va_bf16 *v_new, i
  *   out           device, as q: the attention output rounded once to bf16; padding rows 0
  *   out_lse       optional device float [n_seqs][n_rows][n_kv_heads * group]: log-sum-exp of the scores and the
  *                 sink; -inf for padding rows
- * Weights are rounded to 11 bits, but where a head's seen V scales lie more than 2^9 apart (0 aside) or pass 2^89: such parts of the
- * history are computed in fp32, which takes about twenty times as long.
+ * Weights are rounded to 11 bits.  Where a head's seen V scales lie more than 2^9 apart (0 aside) or pass 2^89, those parts
+ * of the history are computed in fp32 instead, which takes twenty to forty times as long.
  * Only pages that hold a visible position are read, so entries below every row's window may be -1; a page's
  * positions past the sequence's end may hold anything.  A needed entry that is no page sets VA_DEV_BAD_PAGE and
  * its positions count as masked (a row that sees nothing: out 0, out_lse the sink, or -inf).
