@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (far && lane == 0) flags[1] = 1;
         static_assert(kConsumers == kExactWarps, "the consumers compute them");
         ptx::named_bar_sync(1, 32 * kConsumers);
-        if (flags[1] != 0) {
+        if (__builtin_expect(flags[1] != 0, 0)) {
             const Share again = share_s;
             exact_segments<kInt8>(a, plan, again, *reinterpret_cast<ExactSmem*>(slots));
         }

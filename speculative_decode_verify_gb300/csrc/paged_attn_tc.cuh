@@ -17,7 +17,7 @@
 // Bound by the softmax warps: 1.6 us for a tile of 128 keys at 48 pairs, 2.9 us where a reference is raised; and by
 // what a segment costs once (7.5 us until the first scores, 3 us for its sums).  Measured:
 // 48 pairs of one sequence of 192K, E4M3, one KV head 37.1 us, 30 pairs of 32 sequences in a window of 4,096, INT8, two KV
-// heads 36.3 us.  (Eight softmax warps, and wideners that took K and V in turn, took 2.2 and 1.6 us more.)
+// heads 36.2 us.  (Eight softmax warps, and wideners that took K and V in turn, took 2.2 and 1.6 us more.)
 #pragma once
 
 #include "paged_exact.cuh"
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(Shape<NC>::kThreads, 1)
         ptx::tmem_dealloc(tmem, kTmemCols);
     }
     // segments whose V scales lie far apart, again
-    if (ms.far != 0 && warp < kExactWarps) {
+    if (__builtin_expect(ms.far != 0, 0) && warp < kExactWarps) {
         const Share again = ms.share;
         exact_segments<kInt8>(a, ms.plan, again, *reinterpret_cast<ExactSmem*>(base));
     }

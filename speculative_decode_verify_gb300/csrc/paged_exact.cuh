@@ -9,8 +9,9 @@
 //   Eight warps share a segment's pages and take its (row, query head) pairs one after the other; a lane has two keys'
 // scores and four dimensions' sums.  Caches hardly hold such scales, so this is short rather than fast.  With one block of
 // 2^-20 in each sequence, decode of 64 ragged sequences of 1 to 16K takes 1.0 ms (59 us without), 48 pairs of one
-// sequence of 192K 1.1 ms (37 us).  Being there costs the ordinary calls 0.1 to 1.3 us; in the joining kernel, behind its
-// ordinary end, it cost each 1 to 1.5 us, and code unrolled further another 0.8 us of the windows.
+// sequence of 192K 1.1 ms (37 us).  Being there costs the ordinary calls 0.1 to 0.7 us; in the joining kernel, behind its
+// ordinary end, it cost each 1 to 1.5 us, and code unrolled further, or not marked as unlikely, another 0.7 us of the
+// windows.
 #pragma once
 
 #include "paged_plan.cuh"
