@@ -16,7 +16,8 @@
  *                 for keys and values alike.  An element stands for scale x code.  (The append writes no
  *                 NaN code.)
  * Sequences
- *   table         int32 [n_seqs][max_pages]: entry x is the page of positions 64 x .. 64 x + 63, -1 = none
+ *   table         int32 [n_seqs][max_pages]: entry x is the page of positions 64 x .. 64 x + 63, -1 = none;
+ *                 max_pages 1..2^25 - 1
  *   lens          int32 [n_seqs]: positions of the sequence, its live rows among them
  *   n_live        int32 [n_seqs]: live rows of the call, 0..n_rows; row r sits at position
  *                 lens - n_live + r.  Rows past n_live are padding.
@@ -141,7 +142,8 @@ VA_API va_status kv_page_reorder(int32_t *table, int32_t *lens, int n_seqs, int 
 
 /*
  * kv_page_copy - page dst[i] becomes a copy of page src[i] (codes and scales, all layers), i < n_pairs.
- *   src, dst      device int32 [n_pairs]; no page may be a destination twice, or a source and a destination
+ *   src, dst      device int32 [n_pairs], n_pairs 0..n_pages; no page may be a destination twice, or a source and a
+ *                 destination
  *   dev_status    VA_DEV_BAD_PAGE: a pair that names no page is skipped
  * Returns VA_OK, VA_INVALID_ARG, VA_UNSUPPORTED or VA_CUDA_ERROR.
  */
