@@ -9,7 +9,8 @@
  *   first_row     int32 [n_seqs]: sequence b's live rows are rows first_row[b] .. first_row[b] + n_live[b] - 1; row r of
  *                 them sits at position lens[b] - n_live[b] + r.  No two sequences' rows overlap.  Rows that belong to
  *                 none may lie between, before and behind them; what a call writes leaves them as they were.  (Rows
- *                 of the padded layout of kv_pages.h, [n_seqs][n_rows], are first_row[b] = b n_rows.)
+ *                 of the padded layout of kv_pages.h, [n_seqs][n_rows], are first_row[b] = b n_rows.)  Of a sequence
+ *                 without live rows it is not looked at.
  *   n_live        int32 [n_seqs]: 0..n_tokens
  * A sequence whose rows do not lie within the array (VA_DEV_BAD_COUNT) counts as empty.
  */

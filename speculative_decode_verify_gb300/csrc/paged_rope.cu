@@ -43,7 +43,7 @@ __device__ __forceinline__ RopeSeq rope_seq(const RopeArgs& a, int b) {
     r.live = s.live;
     r.status = s.status;
     r.first = __ldcg(a.first_row + b);
-    if (r.first < 0 || r.first > a.n_tokens - r.live) r.status |= VA_DEV_BAD_COUNT;
+    if (r.live > 0 && (r.first < 0 || r.first > a.n_tokens - r.live)) r.status |= VA_DEV_BAD_COUNT;
     if (r.len > a.n_positions && r.live > 0) r.status |= VA_DEV_BEYOND_TABLE;
     if (r.status) r.len = r.live = 0;
     return r;

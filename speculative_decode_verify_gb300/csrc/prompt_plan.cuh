@@ -83,7 +83,7 @@ __device__ __forceinline__ Packed load_packed(const Args& a, int b) {
     p.live = s.live;
     p.status = s.status;
     p.first = __ldcg(a.first_row + b);
-    if (p.first < 0 || p.first > a.n_rows - p.live) p.status |= VA_DEV_BAD_COUNT;
+    if (p.live > 0 && (p.first < 0 || p.first > a.n_rows - p.live)) p.status |= VA_DEV_BAD_COUNT;
     if (p.status) p.len = p.live = 0;
     return p;
 }
