@@ -25,6 +25,7 @@ extern "C" {
 
 #define VA_MAX_TOKENS 16777216    /* packed rows of one call */
 #define VA_DEV_BEYOND_TABLE 2048  /* a position past the end of the rotation's table */
+#define VA_DEV_VALUE_SCALE 4096   /* a value scale, not 0, outside 2^-60..2^60 */
 
 /*
  * kv_page_append_rope_b8 - rotate the live rows' queries and keys by their positions, and code the keys and the
@@ -62,11 +63,14 @@ VA_API va_status kv_page_append_rope_b8(const va_bf16 *q, const va_bf16 *k_new, 
  *   n_tokens      1..VA_MAX_TOKENS; n_seqs 1..VA_PAGED_MAX_SEQS; group 1..VA_PAGED_MAX_GROUP
  *   window, scale, sink, workspace  as for verify_attn_paged_b8; va_prompt_workspace_bytes bytes
  * Weights are rounded to 11 bits, those below 2^-17 of a row's largest to 2^-28 of that.  Value scales below 2^-60 count
- * as 2^-60; a head's value scales that lie more than 2^100 apart, or above 2^60, may cost accuracy.
+ * as 2^-60, those above 2^60 may cost accuracy (VA_DEV_VALUE_SCALE tells of either), as may a head's value scales that lie
+ * more than 2^100 apart.
  * A needed table entry that is no page sets VA_DEV_BAD_PAGE and its positions count as masked (a row that sees
  * nothing: out 0, out_lse the sink, or -inf).
  *   dev_status    VA_DEV_BAD_PAGE; VA_DEV_BAD_COUNT, VA_DEV_BEYOND_CACHE: that sequence's rows stay as they were (all
  *                 sequences' where the counts add up to more than n_tokens: VA_DEV_BAD_COUNT);
+ *                 VA_DEV_VALUE_SCALE: a page that is read has a value scale (of a position that the sequence has)
+ *                 beyond the range above;
  *                 VA_DEV_TIMEOUT: a wait took more than a second, the output is void
  * Returns VA_OK, VA_INVALID_ARG, VA_UNSUPPORTED (a pool of more than 2^31 - 1 rows) or VA_CUDA_ERROR.
  */
@@ -88,8 +92,9 @@ VA_API size_t va_prompt_workspace_bytes(int n_seqs, int n_tokens, int n_kv_heads
  * on the device; of them those pages are shared that every live row sees to their end.  Nothing has to be in common:
  * a group that shares no page is computed slot by slot, and so are all where the sizes given (max_pages and the window for
  * the lengths) say that little is read twice: small calls, and few rows in groups of two or three.  All other arguments, results and status bits are as for
- * verify_attn_paged_b8, the workspace is of va_shared_workspace_bytes bytes, and value scales are limited as for
- * prompt_attn_paged_b8.  out and out_lse must not overlap q.
+ * verify_attn_paged_b8, the workspace is of va_shared_workspace_bytes bytes.  Value scales are limited as for
+ * prompt_attn_paged_b8, and VA_DEV_VALUE_SCALE tells where one was not within the limits, but in the calls that are computed
+ * slot by slot for their sizes, which have no such limits.  out and out_lse must not overlap q.
  * Returns VA_OK, VA_INVALID_ARG, VA_UNSUPPORTED (a pool of more than 2^31 - 1 rows) or VA_CUDA_ERROR.
  */
 VA_API va_status verify_attn_shared_b8(const va_bf16 *q, int n_seqs, int n_rows, int n_kv_heads, int group, int share,

@@ -47,7 +47,9 @@ constexpr float kUnit = 3.0f, kRaise = 12.0f;
 // Exponents from where on t - m is taken of the rounded t: their own roundings, and those of m + log2 v, would come to more
 // than a twentieth, and soon to more than f16 holds.
 constexpr float kFar = 262144.0f;
-constexpr float kLeastScale = 8.673617e-19f;                  // 2^-60, the least scale of values
+// 2^-60, which smaller scales of values (and zeros, whose keys weigh in the sum) count as: from an inverse of 2^80 on sums
+// of weights could pass fp32.  And 2^60, beyond which weights may be lost next to smaller scales.  Both are told of.
+constexpr float kLeastScale = 8.673617e-19f, kMostScale = 1.152921505e18f;
 
 template <bool kShared>
 struct Misc {
@@ -251,6 +253,7 @@ __device__ __forceinline__ void tile_scales(const Args& a, Misc<kShared>& ms, in
                 float* const to = &ms.scale[tt & 3][block >> 1][block & 1];
                 to[2 * kv] = kv ? log2f(least) : x;
                 if (kv) to[4] = 1.0f / least;
+                if (kv && x != 0.0f && !(x >= kLeastScale && x <= kMostScale)) status |= VA_DEV_VALUE_SCALE;
                 if (lane < 8 && block % kBlocks == 0) ms.bad[tt & 3][block / kBlocks] = page == -1;
             }
             __syncwarp();
