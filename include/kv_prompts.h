@@ -62,9 +62,12 @@ VA_API va_status kv_page_append_rope_b8(const va_bf16 *q, const va_bf16 *k_new, 
  *   out_lse       optional device float [n_tokens][n_kv_heads * group]: log-sum-exp of the scores and the sink
  *   n_tokens      1..VA_MAX_TOKENS; n_seqs 1..VA_PAGED_MAX_SEQS; group 1..VA_PAGED_MAX_GROUP
  *   window, scale, sink, workspace  as for verify_attn_paged_b8; va_prompt_workspace_bytes bytes
- * Weights are rounded to 11 bits, those below 2^-17 of a row's largest to 2^-28 of that.  Value scales below 2^-60 count
- * as 2^-60, those above 2^60 may cost accuracy (VA_DEV_VALUE_SCALE tells of either), as may a head's value scales that lie
- * more than 2^100 apart.
+ * What is rounded of a key is its weight times its value scale: to 11 bits, and where that is below 2^-17 of the row's
+ * largest such product, to 2^-28 of the largest.  Next to a key of a larger scale, one of equal weight and a scale 2^-17 or
+ * less of it so loses digits, and from 2^-28 on all of them: 448 x 2^-28 of the larger product at most, where the larger
+ * key's own codes are steps of 2^-9 of it or more.  (verify_attn_paged_b8 computes scales so far apart in fp32.)  Value
+ * scales below 2^-60 count as 2^-60, those above 2^60 may cost accuracy (VA_DEV_VALUE_SCALE tells of either), as may a
+ * head's value scales that lie more than 2^100 apart.
  * A needed table entry that is no page sets VA_DEV_BAD_PAGE and its positions count as masked (a row that sees
  * nothing: out 0, out_lse the sink, or -inf).
  *   dev_status    VA_DEV_BAD_PAGE; VA_DEV_BAD_COUNT, VA_DEV_BEYOND_CACHE: that sequence's rows stay as they were (all
@@ -90,11 +93,14 @@ VA_API size_t va_prompt_workspace_bytes(int n_seqs, int n_tokens, int n_kv_heads
  *   share         slots per group (0: one group of all); n_seqs is a multiple of it
  * The leading entries that all of a group's table rows (but those of slots without live rows) have in common are found
  * on the device; of them those pages are shared that every live row sees to their end.  Nothing has to be in common:
- * a group that shares no page is computed slot by slot, and so are all where the sizes given (max_pages and the window for
- * the lengths) say that little is read twice: small calls, and few rows in groups of two or three.  All other arguments, results and status bits are as for
- * verify_attn_paged_b8, the workspace is of va_shared_workspace_bytes bytes.  Value scales are limited as for
- * prompt_attn_paged_b8, and VA_DEV_VALUE_SCALE tells where one was not within the limits, but in the calls that are computed
- * slot by slot for their sizes, which have no such limits.  out and out_lse must not overlap q.
+ * of a group that shares no page each slot is attended by itself, by the same kernels, which takes up to 2.4 times as long
+ * as verify_attn_paged_b8 where slots have few (row, query head) pairs and long histories; that is the call for slots
+ * that are known to share nothing.  Where the sizes given (max_pages and the window for the lengths) say that little is
+ * read twice, small calls and few rows in groups of two or three, the call is handed to verify_attn_paged_b8 whole.
+ *   All other arguments, results and status bits are as for verify_attn_paged_b8, the workspace is of
+ * va_shared_workspace_bytes bytes.  Roundings and the limits of value scales are those of prompt_attn_paged_b8, and
+ * VA_DEV_VALUE_SCALE tells of scales beyond the limits, but in calls that are handed on, which round as
+ * verify_attn_paged_b8 does and have no such limits.  out and out_lse must not overlap q.
  * Returns VA_OK, VA_INVALID_ARG, VA_UNSUPPORTED (a pool of more than 2^31 - 1 rows) or VA_CUDA_ERROR.
  */
 VA_API va_status verify_attn_shared_b8(const va_bf16 *q, int n_seqs, int n_rows, int n_kv_heads, int group, int share,

@@ -349,7 +349,11 @@ static int cost_shift(long long units, int max_pages) {
 // Measured (us, slot by slot and shared): 2 x 4 slots, 1 head, 6 pairs, 4K positions 12.2 and 17.5; 8 slots, 8 heads, 6 pairs,
 // 4K 19.3 and 22.3, 8K 26.2 and 26.1, 16K 40.8 and 31.0; 4 slots, 8 heads, 4 pairs, 16K 25.2 and 29.6, 64K 70.6 and 67.2; 4
 // slots, 4 heads, 64 pairs, 16K 50.0 and 30.1; 4 x 16 slots, 8 heads, 4 pairs, 1K 36.9 and 45.6, 2K 51.6 and 46.9; 32 x 4
-// slots, 8 heads, 4 pairs, 1K 65.8 and 104.6, 4K 174.6 and 173.8.
+// slots, 8 heads, 4 pairs, 1K 65.8 and 104.6, 4K 174.6 and 173.8.  Where the table is wider than the lengths need the rule errs
+// towards sharing: 2 x 4 slots, 1 head, 6 pairs, 1K 11.2 us by a table of 18 columns, 17.2 by one of 2,048 (8 x 8 slots, 4 heads, 4
+// pairs, 4K 38.3 and 39.2).  Groups that share nothing (known on the device alone): 8 x 8 slots, 4 heads, 4 pairs, 4K 54.0 and
+// 117.8; 32 slots, 8 heads, 6 pairs, 16K 169.6 and 408.4; 8 slots, 8 heads, 6 pairs, 128K 318 and 778; 8 x 8 slots, 1 head, 6 pairs, 32K
+// 90.6 and 210.4; 2 x 4 slots, 1 head, 48 pairs, 64K 64.0 and 68.4; 4 x 8 slots, 2 heads, 64 pairs, 8K 90.3 and 70.7.
 static bool slot_by_slot(long long n_seqs, int n_rows, int n_kv, int group, int share, int max_pages, int window) {
     const long long pages = window > 0 ? std::min<long long>(max_pages, ((long long)window + n_rows) / kPage + 2) : max_pages;
     const int pairs = n_rows * group, all = pairs * share;

@@ -7,7 +7,8 @@
 // pairs, two times four elements that lie rot_dim / 2 apart or next to each other, so that no lane asks another.
 //
 // Bound by memory: 16K tokens of 48 + 2 x 8 heads take 94 us (5.4 TB/s of what has to be read and written; a copy of as much
-// 75).  Calls of single tokens are bound by their launch and the chain of loads (lengths, table, rows): 7 us for 64 of them.
+// 75), with 216 to 240 bytes of spills at 128 registers, two CTAs an SM.  Calls of single tokens are bound by their launch and
+// the chain of loads (lengths, table, rows): 7 us for 64 of them.
 #include <cuda_bf16.h>
 
 #include "paged_code.cuh"

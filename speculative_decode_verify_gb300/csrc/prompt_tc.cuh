@@ -17,7 +17,8 @@
 //              longer code cost more than that gave, turns 221 -> 238 us)
 // What bounds it: a step takes 3,780 cycles, of which the products are 2,048 and no other unit is busier: each 128 pairs' chain of
 // scores, exponents, weights and products, of which tensor memory holds two and no third.  A chunk of 2K rows at 128K (6 heads
-// on 1, INT8) takes 644 us, 1.27 PFLOP/s, a 16K prompt 353 us (its join 12 of them).  Tried and slower: pairs of CTAs that widen half the keys each
+// on 1, INT8) takes 644 us, 1.27 PFLOP/s, a 16K prompt 353 us (its join 12 of them).  Widening, done again for every unit that
+// reads a page, is 101 us of the chunk.  Tried and slower: pairs of CTAs that widen half the keys each
 // (chunk 925 us, handoffs through the cluster); 16 softmax warps with half a pair's keys a thread (699); no wideners, the
 // softmax warps widening (999); no search for a maximum but a check of the sums (779).
 // Registers: 640 threads x 96 at launch = 256 x 144 (softmax) + 384 x 64.  The code is kept short (one copy of each step, in
@@ -39,10 +40,10 @@ constexpr uint32_t kHalf = kKeys * 128;                       // 64 dimensions o
 constexpr uint32_t kOffQ = 0, kOffK = 4 * kHalf, kOffV = 8 * kHalf;   // two of each
 constexpr uint32_t kOffMisc = 12 * kHalf;
 constexpr uint32_t kColO = 256, kTmemCols = 512;
-// p = 2^(t - m + kUnit); m is raised when a t passes it by kRaise, so that p stays below 2^15.  A weight of 2^-17 of the
-// largest or less loses digits in f16 (it is rounded to 2^-28 of it).  Raising costs the row of O once through the registers:
-// with 2^6 and 8, where a third of the tiles of a long history with some large keys raised in one of 128 rows, a chunk of 2K
-// rows at 128K took 958 us, with 2^3 and 12 873.
+// p = 2^(t - m + kUnit); m is raised when a t passes it by kRaise, so that p stays below 2^15.  A product of weight and value
+// scale of 2^-17 of the row's largest or less loses digits in f16 (it is rounded to 2^-28 of that).  Raising costs the row of
+// O once through the registers: with 2^6 and 8, where a third of the tiles of a long history with some large keys raised in one
+// of 128 rows, a chunk of 2K rows at 128K took 958 us, with 2^3 and 12 873.
 constexpr float kUnit = 3.0f, kRaise = 12.0f;
 // Exponents from where on t - m is taken of the rounded t: their own roundings, and those of m + log2 v, would come to more
 // than a twentieth, and soon to more than f16 holds.
